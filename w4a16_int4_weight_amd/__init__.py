@@ -20,6 +20,16 @@ Functions keep the C names:
   w4a16_embedding(ids, packed, K, N, group_size, dtype, out=None, stream=None) -> out [T, K]
   w4a16_status_str(code)                         -> str
 
+Training through frozen packed weights, and scoring (include/w4a16_train.h; the same
+functions as differentiable torch operations: the `autograd` module):
+  w4a16_gemm_grad(dy, packed, K, group_size)               -> dx [M, K] = dy . W^T
+  w4a16_gated(x, packed, F, group_size, act)               -> h [M, F] = a(x Wg) * (x Wu)
+  w4a16_gated_grad(x, dh, packed, F, group_size, act)      -> dx [M, K]
+  w4a16_cross_entropy(x, labels, packed, V, group_size, dloss, grad) -> (loss, lse[, dx])
+  w4a16_distill(x, top_ids, top_logits, packed, V, group_size, temperature, dloss, grad)
+      -> (loss, lse[, dx])
+  (each takes its outputs, workspace and stream as keywords, like w4a16_gemm)
+
 Load-path helpers built on those calls (host-side data movement only):
   repack_from_host(qweight, qzeros, scales, group_size, fmt, chunk_columns, device)
       checkpoint tensors in host memory -> packed device buffer, one column chunk of
@@ -46,6 +56,9 @@ __all__ = [
     "w4a16_gemm", "w4a16_gemm_ex", "w4a16_gemm_noalloc", "w4a16_embedding", "w4a16_status_str", "STATUS", "PATHS",
     "w4a16_stream_sink_bytes", "w4a16_stream_read", "w4a16_stream_copy", "w4a16_clock_stamp",
     "w4a16_wall_clock_hz",
+    "ACTS", "w4a16_gemm_grad", "w4a16_gemm_grad_workspace_bytes", "w4a16_gated", "w4a16_gated_grad",
+    "w4a16_gated_workspace_bytes", "w4a16_cross_entropy", "w4a16_cross_entropy_workspace_bytes", "w4a16_distill",
+    "w4a16_distill_workspace_bytes",
 ]
 
 STATUS = {
@@ -57,6 +70,7 @@ HEADER_BYTES = 64
 PAYLOAD_OFFSET = 1 << 16       # packed bytes start 64 KiB into a saved file (page aligned)
 DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 PATHS = {"auto": 0, "gemv": 1, "mfma": 2}
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
 class W4A16Error(RuntimeError):
@@ -129,6 +143,27 @@ def _load():
     h.w4a16_clock_stamp.restype = _int
     h.w4a16_wall_clock_hz.argtypes = [ctypes.POINTER(_i64)]
     h.w4a16_wall_clock_hz.restype = _int
+    _f32 = ctypes.c_float
+    h.w4a16_gemm_grad_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+    h.w4a16_gemm_grad_workspace_bytes.restype = _sz
+    h.w4a16_gemm_grad.argtypes = [_vp, _vp, _sz, _int, _vp, _i64, _i64, _i64, _i64, _vp, _sz, _vp]
+    h.w4a16_gemm_grad.restype = _int
+    h.w4a16_gated_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _int]
+    h.w4a16_gated_workspace_bytes.restype = _sz
+    h.w4a16_gated.argtypes = [_vp, _vp, _sz, _int, _vp, _i64, _i64, _i64, _i64, _int, _vp, _sz, _vp]
+    h.w4a16_gated.restype = _int
+    h.w4a16_gated_grad.argtypes = [_vp, _vp, _vp, _sz, _int, _vp, _i64, _i64, _i64, _i64, _int, _vp, _sz, _vp]
+    h.w4a16_gated_grad.restype = _int
+    h.w4a16_cross_entropy_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _int]
+    h.w4a16_cross_entropy_workspace_bytes.restype = _sz
+    h.w4a16_cross_entropy.argtypes = [_vp, _vp, _vp, _sz, _int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz,
+                                      _vp]
+    h.w4a16_cross_entropy.restype = _int
+    h.w4a16_distill_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64, _int]
+    h.w4a16_distill_workspace_bytes.restype = _sz
+    h.w4a16_distill.argtypes = [_vp, _vp, _vp, _vp, _sz, _int, _i64, _i64, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp,
+                                _vp, _sz, _vp]
+    h.w4a16_distill.restype = _int
     h.w4a16_status_str.argtypes = [_int]
     h.w4a16_status_str.restype = ctypes.c_char_p
     _lib = h
@@ -492,6 +527,150 @@ def w4a8_linear(x, packed, N, group_size=128, bias=None, y=None, act=None, works
     M, K = x.shape
     act = w4a8_quantize(x, act=act, stream=stream)
     return w4a8_gemm(act, packed, M, K, N, group_size, x.dtype, bias, y, workspace, stream)
+
+
+# ---------------------------------------------------------------- training and scoring
+# (include/w4a16_train.h)
+
+def w4a16_gemm_grad_workspace_bytes(M, K, N, group_size):
+    return _load().w4a16_gemm_grad_workspace_bytes(M, K, N, group_size)
+
+
+def w4a16_gated_workspace_bytes(M, K, F, group_size, grad=False):
+    return _load().w4a16_gated_workspace_bytes(M, K, F, group_size, 1 if grad else 0)
+
+
+def w4a16_cross_entropy_workspace_bytes(M, K, V, group_size, grad=False):
+    return _load().w4a16_cross_entropy_workspace_bytes(M, K, V, group_size, 1 if grad else 0)
+
+
+def w4a16_distill_workspace_bytes(M, K, V, group_size, T, grad=False):
+    return _load().w4a16_distill_workspace_bytes(M, K, V, group_size, T, 1 if grad else 0)
+
+
+def _rows(t, name):
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-dimensional tensor")
+    return t.shape
+
+
+def _result(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor of {dtype}")
+    return t
+
+
+def _space(workspace, need, device, stream):
+    """(pointer, bytes) of the caller's workspace, or of the (device, stream)'s own."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = _default_workspace(device, need, stream)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def w4a16_gemm_grad(dy, packed, K, group_size=128, dx=None, workspace=None, stream=None):
+    """dy [M, N] (fp16/bf16) times the transposed packed [K, N] weight -> dx [M, K]: the
+    gradient of w4a16_gemm with respect to x."""
+    M, N = _rows(dy, "dy")
+    h = _load()
+    dx = _result(dx, "dx", (M, K), dy.dtype, dy.device)
+    ws, ws_bytes = _space(workspace, h.w4a16_gemm_grad_workspace_bytes(M, K, N, group_size), dy.device, stream)
+    _check(h.w4a16_gemm_grad(dy.data_ptr(), packed.data_ptr(), packed.numel() * packed.element_size(),
+                             _dtype_code(dy.dtype), dx.data_ptr(), M, K, N, group_size, ws, ws_bytes,
+                             _stream(stream, dy.device)), "w4a16_gemm_grad")
+    return dx
+
+
+def _act_code(act):
+    if act not in ACTS:
+        raise W4A16Error(9, f"act {act!r}")
+    return ACTS[act]
+
+
+def w4a16_gated(x, packed, F, group_size=128, act="silu", h=None, workspace=None, stream=None):
+    """Gated feed-forward block on one packed [K, 2F] weight (gate columns, then up):
+    x [M, K] -> h [M, F] = act(x Wg) * (x Wu). act: "silu", "gelu" or "gelu_tanh"."""
+    M, K = _rows(x, "x")
+    lib = _load()
+    h = _result(h, "h", (M, F), x.dtype, x.device)
+    ws, ws_bytes = _space(workspace, lib.w4a16_gated_workspace_bytes(M, K, F, group_size, 0), x.device, stream)
+    _check(lib.w4a16_gated(x.data_ptr(), packed.data_ptr(), packed.numel() * packed.element_size(),
+                           _dtype_code(x.dtype), h.data_ptr(), M, K, F, group_size, _act_code(act), ws, ws_bytes,
+                           _stream(stream, x.device)), "w4a16_gated")
+    return h
+
+
+def w4a16_gated_grad(x, dh, packed, F, group_size=128, act="silu", dx=None, workspace=None, stream=None):
+    """Backward of w4a16_gated with respect to x: dh [M, F] -> dx [M, K]. The projections
+    are formed again from x."""
+    M, K = _rows(x, "x")
+    if _rows(dh, "dh") != (M, F) or dh.dtype != x.dtype:
+        raise ValueError("dh must be a contiguous [M, F] tensor of x's dtype")
+    lib = _load()
+    dx = _result(dx, "dx", (M, K), x.dtype, x.device)
+    ws, ws_bytes = _space(workspace, lib.w4a16_gated_workspace_bytes(M, K, F, group_size, 1), x.device, stream)
+    _check(lib.w4a16_gated_grad(x.data_ptr(), dh.data_ptr(), packed.data_ptr(), packed.numel() * packed.element_size(),
+                                _dtype_code(x.dtype), dx.data_ptr(), M, K, F, group_size, _act_code(act), ws, ws_bytes,
+                                _stream(stream, x.device)), "w4a16_gated_grad")
+    return dx
+
+
+def _loss_args(x, dloss, grad, loss, lse, dx):
+    M, K = _rows(x, "x")
+    loss = _result(loss, "loss", (M,), torch.float32, x.device)
+    lse = _result(lse, "lse", (M,), torch.float32, x.device)
+    if grad:
+        dx = _result(dx, "dx", (M, K), x.dtype, x.device)
+        if dloss is not None and (tuple(dloss.shape) != (M,) or dloss.dtype != torch.float32 or not dloss.is_contiguous()):
+            raise ValueError("dloss must be a contiguous float32 [M] tensor")
+    elif dloss is not None or dx is not None:
+        raise ValueError("dloss and dx go with grad=True")
+    return M, K, loss, lse, dx
+
+
+def w4a16_cross_entropy(x, labels, packed, V, group_size=128, dloss=None, grad=False, loss=None, lse=None, dx=None,
+                        workspace=None, stream=None):
+    """Softmax cross entropy over a packed [K, V] head without the logits. x [M, K]
+    (fp16/bf16), labels int32 [M] (outside [0, V): ignored, loss and gradient 0) -> (loss, lse), float32 [M];
+    with grad=True (loss, lse, dx), dx [M, K] = dloss[m] times the loss's gradient
+    (dloss float32 [M], None: 1)."""
+    M, K, loss, lse, dx = _loss_args(x, dloss, grad, loss, lse, dx)
+    if tuple(labels.shape) != (M,) or labels.dtype != torch.int32 or not labels.is_contiguous():
+        raise ValueError("labels must be a contiguous int32 [M] tensor")
+    h = _load()
+    ws, ws_bytes = _space(workspace, h.w4a16_cross_entropy_workspace_bytes(M, K, V, group_size, 1 if grad else 0),
+                          x.device, stream)
+    _check(h.w4a16_cross_entropy(x.data_ptr(), labels.data_ptr(), packed.data_ptr(),
+                                 packed.numel() * packed.element_size(), _dtype_code(x.dtype), M, K, V, group_size,
+                                 None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                                 dx.data_ptr() if grad else None, ws, ws_bytes, _stream(stream, x.device)),
+           "w4a16_cross_entropy")
+    return (loss, lse, dx) if grad else (loss, lse)
+
+
+def w4a16_distill(x, top_ids, top_logits, packed, V, group_size=128, temperature=1.0, dloss=None, grad=False, loss=None,
+                  lse=None, dx=None, workspace=None, stream=None):
+    """Distillation from a teacher's top logits over a packed [K, V] head. top_ids int32
+    [M, T] (outside [0, V): none), top_logits float32 [M, T], T <= 256 -> as
+    w4a16_cross_entropy, with loss = t^2 KL(teacher's softmax over the row's entries ||
+    softmax(x W / t)) and lse that of x W / t."""
+    M, K, loss, lse, dx = _loss_args(x, dloss, grad, loss, lse, dx)
+    Mi, T = _rows(top_ids, "top_ids")
+    if Mi != M or top_ids.dtype != torch.int32:
+        raise ValueError("top_ids must be an int32 [M, T] tensor")
+    if _rows(top_logits, "top_logits") != (M, T) or top_logits.dtype != torch.float32:
+        raise ValueError("top_logits must be a float32 [M, T] tensor")
+    h = _load()
+    ws, ws_bytes = _space(workspace, h.w4a16_distill_workspace_bytes(M, K, V, group_size, T, 1 if grad else 0),
+                          x.device, stream)
+    _check(h.w4a16_distill(x.data_ptr(), top_ids.data_ptr(), top_logits.data_ptr(), packed.data_ptr(),
+                           packed.numel() * packed.element_size(), _dtype_code(x.dtype), M, K, V, group_size, T,
+                           temperature, None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                           dx.data_ptr() if grad else None, ws, ws_bytes, _stream(stream, x.device)), "w4a16_distill")
+    return (loss, lse, dx) if grad else (loss, lse)
 
 
 # ---------------------------------------------------------------- streaming references

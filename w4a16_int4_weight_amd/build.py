@@ -7,16 +7,19 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "libw4a16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["api.hip", "repack.hip", "gemv.hip", "gemv_strip.hip", "gemv_small.hip", "gemm.hip", "embedding.hip", "w4a8.hip", "measure.hip"]
+SOURCES = ["api.hip", "repack.hip", "gemv.hip", "gemv_strip.hip", "gemv_small.hip", "gemm.hip", "embedding.hip", "w4a8.hip", "measure.hip",
+           "api_train.hip", "gated.hip", "gemm_grad.hip", "loss.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
-    "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-shared",
+    "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",
     # keep hipcc from forming packed fp32 instructions on its own
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-command-line-argument",
@@ -51,17 +54,27 @@ def build(verbose=False, out=None, sanitize_host=False):
     target = out or LIB_PATH
     tmp = target + ".tmp"
     flags = HIPCC_FLAGS + (SANITIZE_HOST_FLAGS if sanitize_host else [])
-    cmd = [hipcc()] + flags + ["-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    # hipcc's host pass does not know the packed-fp32 feature and says so: harmless
-    noise = "is not a recognized feature for this target"
-    msgs = [l for l in (res.stdout + res.stderr).splitlines() if noise not in l and l.strip()]
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
-    if verbose and msgs:
-        print("\n".join(msgs), flush=True)
+    # one compiler process per source, as many at a time as there are cores; MAX_JOBS caps it
+    jobs = min(len(SOURCES), os.cpu_count() or 1, int(os.environ.get("MAX_JOBS") or 8))
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        # hipcc's host pass does not know the packed-fp32 feature and says so: harmless
+        noise = "is not a recognized feature for this target"
+        msgs = [l for l in (res.stdout + res.stderr).splitlines() if noise not in l and l.strip()]
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        if verbose and msgs:
+            print("\n".join(msgs), flush=True)
+
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, s.replace(".hip", ".o")) for s in SOURCES]
+        with ThreadPoolExecutor(max_workers=max(1, jobs)) as pool:
+            list(pool.map(run, [[hipcc()] + flags + ["-c", "-o", o, os.path.join(CSRC, s)]
+                                for s, o in zip(SOURCES, objects)]))
+        run([hipcc()] + flags + ["-shared", "-o", tmp] + objects)
     os.replace(tmp, target)
     return target
 

@@ -4,15 +4,23 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <atomic>
 #include <mutex>
 
 #include "../../include/w4a16.h"
+#include "api_common.h"
 #include "device_common.h"
 #include "launch.h"
 #include "split_k.h"
 
 namespace {
+
+using w4a16::aligned;
+using w4a16::check_device;
+using w4a16::check_shape;
+using w4a16::kMaxDevices;
+using w4a16::kMaxK;
+using w4a16::kMaxMK;
+using w4a16::packed_size;
 
 constexpr int kLayoutVersion = 2;
 constexpr int64_t kGemvMaxRows = 16;      // rows one GEMV A operand holds
@@ -38,32 +46,6 @@ int64_t default_gemv_max_m(int64_t K, int64_t N, int64_t G) {
     if (code_bytes <= (int64_t(16) << 20)) return 12;
     return kDefaultGemvMaxM;
 }
-constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxK = int64_t(1) << 20;   // kernels index rows and columns with 32-bit integers
-constexpr int64_t kMaxN = int64_t(1) << 28;
-constexpr int64_t kMaxKN = int64_t(1) << 37;  // packed codes index in 32-bit 16-byte units
-constexpr int64_t kMaxMK = int64_t(1) << 32;  // activations index in 32-bit elements
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Resolved group size, or 0 if (K, N, group_size) is outside the tile layout.
-w4a16_status check_shape(int64_t K, int64_t N, int64_t group_size, int64_t* G_out) {
-    if (K <= 0 || N <= 0 || K % 128 != 0 || N % 8 != 0) return W4A16_ERR_SHAPE;
-    if (K > kMaxK || N > kMaxN || K * N > kMaxKN) return W4A16_ERR_SHAPE;
-    const int64_t G = group_size == -1 ? K : group_size;
-    if (G <= 0 || K % G != 0 || (G % 128 != 0 && G != 32 && G != 64)) return W4A16_ERR_GROUP;
-    *G_out = G;
-    return W4A16_OK;
-}
-
-// K x Np codes (Np = N rounded up to 16 columns) + one 32-bit word per column per
-// unit of min(G, 128) rows, the unit count rounded up to 4 (G resolved)
-size_t packed_size(int64_t K, int64_t N, int64_t G) {
-    const size_t uw = (size_t)w4a16::padded_units(K, G);
-    const size_t np = (size_t)w4a16::padded_cols(N);
-    return (size_t)K * np / 2 + (size_t)4 * uw * np;
-}
-
 // W4A8 activation buffer: codes (M*K bytes), row scales (M fp32), block sums
 // (M*K/128 fp32), each part starting on a 256-byte boundary.
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -79,23 +61,6 @@ w4a16::W4A8Act act_parts(void* act, int64_t M, int64_t K) {
     uint8_t* base = static_cast<uint8_t*>(act);
     return w4a16::W4A8Act{base, reinterpret_cast<float*>(base + act_scale_offset(M, K)),
                           reinterpret_cast<float*>(base + act_sum_offset(M, K))};
-}
-
-// 0 = unknown, 1 = gfx950, 2 = other; cached per device ordinal.
-std::atomic<int> g_device_kind[kMaxDevices];
-
-w4a16_status check_device() {
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return W4A16_ERR_DEVICE;
-    if (dev < 0 || dev >= kMaxDevices) return W4A16_ERR_DEVICE;
-    int kind = g_device_kind[dev].load(std::memory_order_relaxed);
-    if (kind == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return W4A16_ERR_DEVICE;
-        kind = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-        g_device_kind[dev].store(kind, std::memory_order_relaxed);
-    }
-    return kind == 1 ? W4A16_OK : W4A16_ERR_DEVICE;
 }
 
 // Host-side checks of a GEMM call (everything but the workspace and the device).

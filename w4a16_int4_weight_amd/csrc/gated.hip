@@ -1,0 +1,223 @@
+// Gated feed-forward block on one packed [K, 2F] weight (gate columns 0 .. F-1, up
+// columns F .. 2F-1, as checkpoints fuse them):
+//
+//   forward   h  = a(g) u,             g = x Wg, u = x Wu
+//   backward  dg = dh u a'(g), du = dh a(g);   dx = dg Wg^T + du Wu^T
+//
+// Both projections of an output element sit in one lane: a wave owns HB gate column
+// blocks and the HB matching up blocks, so g and u never leave its registers and the
+// block costs one product and one pass over x. The backward recomputes them (keeping
+// them would take 4 F bytes a token and round them to 16 bits), writes dg and du to the
+// workspace in bf16, whatever the dtype - their range is the gradients', which fp16 does
+// not hold without a scale chosen for them - and one product with W^T follows.
+#include "device_common.h"
+#include "launch.h"
+#include "tile_product.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kTargetWorkgroups = 256;      // one per compute unit
+
+// a(g) and a'(g) in fp32. kAct: 0 silu g/(1 + e^-g); 1 gelu g Phi(g); 2 gelu's tanh form,
+// 0.5 (1 + tanh y) = 1/(1 + e^-2y). The polynomial's argument is clamped at +-30, where
+// its logistic is 0 or 1 exactly, so that no infinity meets a zero.
+template <int kAct>
+__device__ __forceinline__ float gate_prob(float g, float* slope) {
+    if constexpr (kAct == 0) {
+        const float e = __builtin_amdgcn_rcpf(1.f + __expf(-g));
+        *slope = e * (1.f - e);
+        return e;
+    } else if constexpr (kAct == 1) {
+        *slope = 0.3989422804f * __expf(-0.5f * g * g);
+        return 0.5f * erfcf(-0.7071067812f * g);
+    } else {
+        const float y = fminf(fmaxf(g, -30.f), 30.f);
+        const float e = __builtin_amdgcn_rcpf(1.f + __expf(-1.5957691216f * y * (1.f + 0.044715f * y * y)));
+        *slope = e * (1.f - e) * 1.5957691216f * (1.f + 0.134145f * y * y);
+        return e;
+    }
+}
+
+struct GatedArgs {
+    ProductArgs p;
+    uint16_t* h;            // forward: [M, F]
+    const uint16_t* dh;     // backward: [M, F]
+    uint16_t* d;            // backward: [M, 2F] bf16, dg then du
+    int act;
+};
+
+template <class P, bool kGrad, int kAct>
+__device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::Shared& sh, int m0, int f0,
+                                               f32x4 (&acc)[P::MR][P::CBW]) {
+    constexpr int BM = P::BM, BN = P::BN, HB = P::HB;
+    constexpr int kRow = BN * 2 + 16;                        // bytes of a tile row, padded
+    constexpr int kChunks = BN / 8;
+    static_assert((kGrad ? 2 : 1) * BM * kRow <= (int)sizeof(typename P::Shared), "the output tiles fit in LDS");
+    const int tid = threadIdx.x;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63;
+    const int c = lane & 15, h = lane >> 4;
+    const int M = a.p.M, F = a.p.F;
+    uint8_t* t0 = reinterpret_cast<uint8_t*>(&sh);
+    uint8_t* t1 = t0 + BM * kRow;
+    if constexpr (kGrad) {
+        // dh's tile through LDS: whole 16-byte chunks (F % 8 == 0), zero outside
+        for (int q = tid; q < BM * kChunks; q += P::kThreads) {
+            const int row = q / kChunks, ch = q % kChunks;
+            const int m = m0 + row, f = f0 + 8 * ch;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (m < M && f < F) v = *reinterpret_cast<const uint4*>(a.dh + (size_t)m * F + f);
+            *reinterpret_cast<uint4*>(t0 + row * kRow + 16 * ch) = v;
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < P::MR; ++r) {
+#pragma unroll
+        for (int j = 0; j < HB; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int at = (16 * r + 4 * h + e) * kRow + 2 * (16 * (w * HB + j) + c);
+                const float g = acc[r][j][e], u = acc[r][j + HB][e];
+                float slope;
+                const float pr = gate_prob<kAct>(g, &slope);
+                if constexpr (!kGrad) {
+                    *reinterpret_cast<uint16_t*>(t0 + at) = f32_to_half_bits<P::kBF16>(g * pr * u);
+                } else {
+                    const float d = half_bits_to_f32<P::kBF16>(*reinterpret_cast<const uint16_t*>(t0 + at));
+                    *reinterpret_cast<uint16_t*>(t0 + at) = f32_to_half_bits<true>(d * u * fmaf(g, slope, pr));
+                    *reinterpret_cast<uint16_t*>(t1 + at) = f32_to_half_bits<true>(d * (g * pr));
+                }
+            }
+        }
+    }
+    __syncthreads();
+    for (int q = tid; q < BM * kChunks; q += P::kThreads) {
+        const int row = q / kChunks, ch = q % kChunks;
+        const int m = m0 + row, f = f0 + 8 * ch;
+        if (m >= M || f >= F) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(t0 + row * kRow + 16 * ch);
+        if constexpr (!kGrad) {
+            *reinterpret_cast<uint4*>(a.h + (size_t)m * F + f) = v;
+        } else {
+            *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + f) = v;
+            *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + F + f) =
+                *reinterpret_cast<const uint4*>(t1 + row * kRow + 16 * ch);
+        }
+    }
+}
+
+template <class P, bool kGrad>
+__global__ __launch_bounds__(P::kThreads) void gated_kernel(const GatedArgs a) {
+    __shared__ typename P::Shared sh;
+    int m_tile, n_tile, split;
+    if (!product_tile(a.p, (int)blockIdx.x, &m_tile, &n_tile, &split)) return;
+    f32x4 acc[P::MR][P::CBW];
+    P::run(a.p, sh, m_tile, n_tile, split, acc);
+    if (a.p.splits > 1 && !reduce_splits<P::MR, P::CBW, P::W>(acc, a.p.counters, a.p.partials,
+                                                              m_tile * a.p.tiles_n + n_tile, split, a.p.splits))
+        return;
+    const int m0 = m_tile * P::BM, f0 = n_tile * P::BN;
+    if (a.act == 0) gated_epilogue<P, kGrad, 0>(a, sh, m0, f0, acc);
+    else if (a.act == 1) gated_epilogue<P, kGrad, 1>(a, sh, m0, f0, acc);
+    else gated_epilogue<P, kGrad, 2>(a, sh, m0, f0, acc);
+}
+
+template <bool kBF16, int MR, int CBW, int kSub, bool kGrad>
+void launch_cfg(GatedArgs& a, hipStream_t s) {
+    using P = TileProduct<kBF16, MR, CBW, 8, kSub, true>;
+    const int64_t ids = product_ids(a.p.tiles_m, a.p.tiles_n, a.p.splits);
+    hipLaunchKernelGGL((gated_kernel<P, kGrad>), dim3((unsigned)ids), dim3(P::kThreads), 0, s, a);
+}
+
+template <bool kBF16, bool kGrad>
+void launch_typed(const ProductPlan& p, GatedArgs& a, hipStream_t s) {
+    if (p.sub == 4) {
+        if (p.mr == 1) launch_cfg<kBF16, 1, 2, 4, kGrad>(a, s);
+        else launch_cfg<kBF16, 4, 2, 4, kGrad>(a, s);
+    } else if (p.sub == 2) {
+        if (p.mr == 1) launch_cfg<kBF16, 1, 2, 2, kGrad>(a, s);
+        else launch_cfg<kBF16, 4, 2, 2, kGrad>(a, s);
+    } else if (p.mr == 1) launch_cfg<kBF16, 1, 2, 1, kGrad>(a, s);
+    else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 1, kGrad>(a, s);
+    else if (p.mr == 4) launch_cfg<kBF16, 4, 2, 1, kGrad>(a, s);
+    else launch_cfg<kBF16, 8, 2, 1, kGrad>(a, s);
+}
+
+}  // namespace
+
+// Tile shape: rows by M; at more than 64 rows the tile (128 x 256 or 64 x 256
+// columns of the weight) whose rounds over the compute units cost least, by area over the
+// rate each shape was measured at with every compute unit busy. Outputs of few tiles split
+// K over workgroups, at least 4 row blocks each.
+ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gated) {
+    ProductPlan p{};
+    p.sub = units_per_block(G);
+    const int64_t KB = K / kRowsPerBlock;
+    struct Shape { int mr, cbw; double rate; };
+    static constexpr Shape kShapes[] = {{8, 2, 0.85}, {4, 2, 0.7}};
+    if (p.sub > 1) {
+        p.mr = M <= 16 ? 1 : 4;
+        p.cbw = 2;
+    } else if (M <= 64) {
+        p.mr = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+        p.cbw = 2;
+    } else {
+        double best = 0.0;
+        for (const Shape& c : kShapes) {
+            const int64_t tm = (M + 16 * c.mr - 1) / (16 * c.mr);
+            const int64_t tn = (cols + 128 * c.cbw - 1) / (128 * c.cbw);
+            const int64_t rounds = (tm * tn + kTargetWorkgroups - 1) / kTargetWorkgroups;
+            const double cost = (double)rounds * c.mr * c.cbw / c.rate;
+            if (best == 0.0 || cost < best) {
+                best = cost;
+                p.mr = c.mr;
+                p.cbw = c.cbw;
+            }
+        }
+    }
+    const int64_t width = 128 * p.cbw;      // weight columns of a tile
+    p.tiles_m = (int)((M + 16 * p.mr - 1) / (16 * p.mr));
+    p.tiles_n = (int)(gated ? (cols / 2 + width / 2 - 1) / (width / 2) : (cols + width - 1) / width);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    p.splits = 1;
+    static_assert(kTargetWorkgroups / 2 <= kMaxSplitTiles, "split tiles must fit the counter region");
+    if (tiles < kTargetWorkgroups / 2 && KB >= 8) {
+        const int64_t want = kTargetWorkgroups / tiles;
+        const int64_t most = KB / 4;
+        p.splits = (int)(want < most ? want : most);
+    }
+    p.partial_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)tiles * (size_t)(16 * p.mr) * (size_t)width * 4 : 0;
+    return p;
+}
+
+hipError_t launch_gated(const GatedCall& q, hipStream_t stream) {
+    const ProductPlan p = plan_product(q.M, q.K, 2 * q.F, q.G, true);
+    GatedArgs a{};
+    a.p.x = q.x;
+    a.p.packed = q.packed;
+    a.p.M = (int)q.M;
+    a.p.K = (int)q.K;
+    a.p.N = (int)(2 * q.F);
+    a.p.F = (int)q.F;
+    a.p.tiles_m = p.tiles_m;
+    a.p.tiles_n = p.tiles_n;
+    a.p.splits = p.splits;
+    a.p.counters = q.counters;
+    a.p.partials = q.partials;
+    a.h = q.h;
+    a.dh = q.dh;
+    a.d = q.d;
+    a.act = q.act;
+    if (q.d) {
+        if (q.bf16) launch_typed<true, true>(p, a, stream);
+        else launch_typed<false, true>(p, a, stream);
+    } else {
+        if (q.bf16) launch_typed<true, false>(p, a, stream);
+        else launch_typed<false, false>(p, a, stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace w4a16

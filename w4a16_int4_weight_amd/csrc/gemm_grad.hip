@@ -1,0 +1,351 @@
+// The product with the transposed weight, dx = D W^T, from the packed buffer the forward
+// reads: D [M, N] (an output gradient, or the gradient an operator formed itself), W [K, N].
+//
+//   dx[m, k] = sum_n D[m, n] (q[k, n] - z[g, n]) s[g, n],   g = k div G
+//
+// The sum now runs along n, where neighbouring weights lie in different lanes of a packed
+// block and every term has a scale of its own. A weight is decoded once per workgroup:
+// each thread takes 16 bytes of the stage (32 codes of one column), forms (q - z) s rounded
+// once to the operand type (at most half a step each, errors of both signs over a sum of N
+// terms), and writes 8-row runs into LDS as rows of n. The transposing LDS read
+// (ds_read_b64_tr_b16: lane l of 16 receives element l of four rows) then delivers matrix
+// operands that run along n: no nibble is moved between lanes by hand, and one packed
+// buffer serves both directions. fp32 accumulators, no rounding between.
+//
+// Workgroup: a tile of BM rows x 256 columns of dx, 8 waves as WM x WK. A stage is 64
+// columns of W: D's rows by direct global -> LDS copies (16-byte chunks XOR-swizzled by
+// row), the codes through registers one stage ahead; two stages alternate, and the next
+// one is decoded between the products of the current one. Small M, or few tiles: the sum
+// is split over workgroups into fp32 partial tiles, added in split order by a second
+// kernel (the result does not depend on the order of arrival).
+#include "device_common.h"
+#include "launch.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kTargetWorkgroups = 256;      // one per compute unit
+constexpr int kStageN = 64;
+constexpr int kTileK = 256;
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+struct GradArgs {
+    const uint16_t* d;
+    int64_t ld;
+    const uint8_t* packed;
+    uint16_t* dx;
+    float* part;
+    int M, K, N, KB, UW;
+    int n0, n;              // this call's columns
+    int tiles_m, tiles_k, splits;
+    int add;
+};
+
+// 8 codes -> 8 operand values (q - z) s in row order
+template <bool kOpBF16, bool kScaleBF16>
+struct Decode {
+    float s, nzs;
+    __device__ __forceinline__ explicit Decode(uint32_t md) {
+        s = half_bits_to_f32<kScaleBF16>(md & 0xFFFFu);
+        nzs = -(float)((md >> 16) & 0xFu) * s;
+    }
+    __device__ __forceinline__ uint4 operator()(uint32_t d) const {
+        static_assert(kOpBF16, "fp16 operands decode in packed fp16");
+        uint32_t lo = d & 0x0F0F0F0Fu, hi = (d >> 4) & 0x0F0F0F0Fu;    // rows 0,4,1,5 / 2,6,3,7
+        asm volatile("" : "+v"(lo), "+v"(hi));
+        const float r0 = fmaf((float)(lo & 0xFFu), s, nzs), r4 = fmaf((float)((lo >> 8) & 0xFFu), s, nzs);
+        const float r1 = fmaf((float)((lo >> 16) & 0xFFu), s, nzs), r5 = fmaf((float)(lo >> 24), s, nzs);
+        const float r2 = fmaf((float)(hi & 0xFFu), s, nzs), r6 = fmaf((float)((hi >> 8) & 0xFFu), s, nzs);
+        const float r3 = fmaf((float)((hi >> 16) & 0xFFu), s, nzs), r7 = fmaf((float)(hi >> 24), s, nzs);
+        return make_uint4(pack2_rne<true>(r0, r1), pack2_rne<true>(r2, r3), pack2_rne<true>(r4, r5),
+                          pack2_rne<true>(r6, r7));
+    }
+};
+template <>
+struct Decode<false, false> : Dequant<false> {
+    __device__ __forceinline__ explicit Decode(uint32_t md) : Dequant<false>(md) {}
+};
+
+// One stage: D rows [BM][8 chunks of 16 bytes], chunk j of row r at j ^ (r % 8); W rows
+// [64 n][32 chunks of 8 k], chunk j of row n at j ^ swz(n). swz spreads the 8 lanes of a
+// write (8 consecutive n, one chunk) over 8 chunks and the 16 rows of a transposing read
+// (n % 8 in a half, all n / 8) evenly over 4 chunk pairs.
+__device__ __forceinline__ int swz(int n) { return (n & 7) ^ (2 * ((n >> 3) & 3)); }
+
+template <bool kOpBF16, bool kScaleBF16, int MR, int WM, int CK, int kSub>
+__global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
+    constexpr int WK = 8 / WM;
+    constexpr int BM = 16 * MR * WM;
+    static_assert(16 * CK * WK == kTileK, "the waves cover the tile's columns");
+    constexpr int kSlabs = BM / 8;                    // 1 KiB slabs (8 rows) of the D stage
+    struct Stage {
+        uint4 d[BM * 8];
+        uint4 w[kStageN * 32];
+    };
+    __shared__ Stage ring[2];
+
+    const int tid = threadIdx.x;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63;
+    const int c = lane & 15, h = lane >> 4;
+    const int wm = w / WK, wk = w % WK;
+
+    // ids id, id + 8, ... share an XCD, which takes whole splits' tiles in turn: row tiles
+    // fastest, so that one stage's codes serve several of its workgroups from its L2
+    int id = (int)blockIdx.x;
+    const int total = a.tiles_m * a.tiles_k * a.splits;
+    id = xcd_share(id, total);
+    const int m_tile = id % a.tiles_m;
+    const int rest = id / a.tiles_m;
+    const int k_tile = rest % a.tiles_k;
+    const int split = rest / a.tiles_k;
+    const int m0 = m_tile * BM, k0 = k_tile * kTileK;
+    const int stages = (a.n + kStageN - 1) / kStageN;
+    const int st_lo = (int)((int64_t)stages * split / a.splits);
+    const int st_hi = (int)((int64_t)stages * (split + 1) / a.splits);
+
+    // this thread's 16 bytes of a stage: column 16 nbi + cc, row block kbi of the tile,
+    // lane quarter hh
+    const int nbi = tid >> 7, kbi = (tid >> 6) & 1, hh = (tid >> 4) & 3, cc = tid & 15;
+    const int kb = k0 / kRowsPerBlock + kbi;
+    const int kbc = kb < a.KB ? kb : a.KB - 1;
+    const int Np = (int)padded_cols(a.N);
+    const int NB = Np / kColsPerBlock;
+    const uint8_t* meta = a.packed + (size_t)a.K * Np / 2;
+
+    uint4 code;
+    uint32_t md[kSub];
+    auto load_codes = [&](int t) {
+        const int n = a.n0 + t * kStageN + 16 * nbi + cc;
+        const int nb = n / kColsPerBlock < NB ? n / kColsPerBlock : NB - 1;
+        code = *reinterpret_cast<const uint4*>(a.packed + ((size_t)nb * a.KB + kbc) * kBlockBytes + 16 * (16 * hh + cc));
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(
+                meta + 4 * ((size_t)(nb * kColsPerBlock + cc) * a.UW + kbc * kSub + u));
+            md[u] = n < a.n0 + a.n ? v : 0u;          // columns past the call's weigh zero
+        }
+    };
+    auto store_codes = [&](int slot) {
+        const int row = 16 * nbi + cc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Decode<kOpBF16, kScaleBF16> dq(md[(i * kSub) / 4]);
+            const uint32_t d = i == 0 ? code.x : i == 1 ? code.y : i == 2 ? code.z : code.w;
+            ring[slot].w[row * 32 + ((16 * kbi + 4 * i + hh) ^ swz(row))] = dq(d);
+        }
+    };
+    // D rows m0 + 8 slab + lane / 8, 16-byte chunk (lane % 8) ^ (row % 8). Rows past M read
+    // row M - 1. A stage that ends past the call's columns is read with a test per chunk
+    // instead (n % 8 == 0), zero outside: what lies there may be no number.
+    const uint8_t* dbase = uniform_ptr(a.d + (size_t)m0 * a.ld);
+    auto issue_d = [&](int slot, int t) {
+        const int nn = t * kStageN;
+        if (nn + kStageN <= a.n) {
+#pragma unroll
+            for (int q = 0; q < (kSlabs + 7) / 8; ++q) {
+                const int slab = w + 8 * q;
+                if (kSlabs % 8 == 0 || slab < kSlabs) {
+                    const int row = 8 * slab + (lane >> 3);
+                    const int m = m0 + row < a.M ? row : a.M - 1 - m0;
+                    dma16(dbase + (size_t)nn * 2, 2u * ((uint32_t)m * (uint32_t)a.ld + 8u * (uint32_t)((lane & 7) ^ (row & 7))),
+                          lds_addr(&ring[slot].d[0]) + 1024u * (uint32_t)slab);
+                }
+            }
+        } else {
+            for (int q = tid; q < BM * 8; q += 512) {
+                const int row = q >> 3, ch = q & 7;
+                const int m = m0 + row < a.M ? m0 + row : a.M - 1;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (nn + 8 * ch < a.n) v = *reinterpret_cast<const uint4*>(a.d + (size_t)m * a.ld + nn + 8 * ch);
+                ring[slot].d[row * 8 + (ch ^ (row & 7))] = v;
+            }
+        }
+    };
+
+    f32x4 acc[MR][CK];
+#pragma unroll
+    for (int r = 0; r < MR; ++r)
+#pragma unroll
+        for (int j = 0; j < CK; ++j) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if (st_lo < st_hi) {
+        load_codes(st_lo);
+        issue_d(0, st_lo);
+        store_codes(0);
+        if (st_lo + 1 < st_hi) load_codes(st_lo + 1);
+    }
+    for (int t = st_lo; t < st_hi; ++t) {
+        const int slot = (t - st_lo) & 1;
+        wait_vmcnt<0>();                  // this wave's copies of stage t, and its codes of t + 1
+        wait_lgkmcnt0();                  // its decoded rows of stage t are written
+        lds_barrier();                    // everyone's; and everyone has read stage t - 1
+        if (t + 1 < st_hi) {
+            issue_d(slot ^ 1, t + 1);
+            store_codes(slot ^ 1);
+        }
+        if (t + 2 < st_hi) load_codes(t + 2);
+        const Stage& st = ring[slot];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint4 b[CK], f[MR];
+#pragma unroll
+            for (int j = 0; j < CK; ++j) {
+                // rows n = 32 i + 8 h + (0..3) and + (4..7), 16 columns k from 16 (wk CK + j):
+                // lane c of the 16 points at row c / 4, columns 4 (c % 4)
+                const int ch = 2 * (wk * CK + j) + ((c >> 1) & 1);
+                i16x4 v[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int n = 32 * i + 8 * h + 4 * q + (c >> 2);
+                    const uint8_t* p = reinterpret_cast<const uint8_t*>(&st.w[n * 32 + (ch ^ swz(n))]) + 8 * (c & 1);
+                    v[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) i16x4*)(const __attribute__((address_space(3))) void*)p);
+                }
+                const uint2 lo = __builtin_bit_cast(uint2, v[0]), hi = __builtin_bit_cast(uint2, v[1]);
+                b[j] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+#pragma unroll
+            for (int r = 0; r < MR; ++r) {
+                const int row = 16 * (wm * MR + r) + c;
+                f[r] = st.d[row * 8 + ((4 * i + h) ^ (row & 7))];
+            }
+            // transposed tiles: lane (c, h), register e -> row 16 r + c, column 16 j + 4 h + e
+#pragma unroll
+            for (int r = 0; r < MR; ++r)
+#pragma unroll
+                for (int j = 0; j < CK; ++j) acc[r][j] = mfma16x16x32<kOpBF16>(b[j], f[r], acc[r][j]);
+        }
+    }
+
+#pragma unroll
+    for (int r = 0; r < MR; ++r) {
+        const int m = m0 + 16 * (wm * MR + r) + c;
+        if (m >= a.M) continue;
+#pragma unroll
+        for (int j = 0; j < CK; ++j) {
+            const int k = k0 + 16 * (wk * CK + j) + 4 * h;
+            if (k >= a.K) continue;
+            f32x4 v = acc[r][j];
+            if (a.part) {
+                f32x4* o = reinterpret_cast<f32x4*>(a.part + ((size_t)split * a.M + m) * a.K + k);
+                if (a.add) v += *o;
+                *o = v;
+            } else {
+                const uint2 o = make_uint2(pack2_rne<kScaleBF16>(v[0], v[1]), pack2_rne<kScaleBF16>(v[2], v[3]));
+                *reinterpret_cast<uint2*>(a.dx + (size_t)m * a.K + k) = o;
+            }
+        }
+    }
+}
+
+// dx = coef sum_s part[s], 8 values a thread; bandwidth-bound over the partials
+template <bool kBF16>
+__global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restrict__ part, int splits, int64_t MK, int K,
+                                                          const float* __restrict__ coef, uint16_t* __restrict__ dx) {
+    const int64_t at = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (at >= MK) return;
+    f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+    for (int s = 0; s < splits; ++s) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(part + s * MK + at);
+        s0 += p[0];
+        s1 += p[1];
+    }
+    uint4 o;
+    const float f = coef ? coef[at / K] : 1.f;
+    if (f == 0.f) {
+        o = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        o = make_uint4(pack2_rne<kBF16>(s0[0] * f, s0[1] * f), pack2_rne<kBF16>(s0[2] * f, s0[3] * f),
+                       pack2_rne<kBF16>(s1[0] * f, s1[1] * f), pack2_rne<kBF16>(s1[2] * f, s1[3] * f));
+    }
+    *reinterpret_cast<uint4*>(dx + at) = o;
+}
+
+template <bool kOp, bool kSc, int kSub>
+void launch_sub(int bm, const GradArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_k * a.splits)), block(512);
+    if (bm == 16) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 1, 1, 2, kSub>), grid, block, 0, s, a);
+    else if (bm == 32) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 2, 1, 2, kSub>), grid, block, 0, s, a);
+    else if (bm == 64) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 1, 2, kSub>), grid, block, 0, s, a);
+    else if (bm == 128) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 2, 4, kSub>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((grad_kernel<kOp, kSc, 8, 2, 4, kSub>), grid, block, 0, s, a);
+}
+
+template <bool kOp, bool kSc>
+void launch_typed(int bm, int sub, const GradArgs& a, hipStream_t s) {
+    if (sub == 4) launch_sub<kOp, kSc, 4>(bm, a, s);
+    else if (sub == 2) launch_sub<kOp, kSc, 2>(bm, a, s);
+    else launch_sub<kOp, kSc, 1>(bm, a, s);
+}
+
+}  // namespace
+
+// Rows of a tile by M; above 128 rows, 256 or 128 by the rounds of tiles over the compute
+// units. The sum is split where the tiles leave compute units idle, at least 4 stages each.
+GradPlan plan_grad(int64_t M, int64_t K, int64_t n, bool forced) {
+    GradPlan p{};
+    p.tiles_k = (int)((K + kTileK - 1) / kTileK);
+    const int64_t stages = (n + kStageN - 1) / kStageN;
+    const int64_t most = stages / 4 > 1 ? stages / 4 : 1;
+    auto splits_of = [&](int64_t tiles) {
+        int64_t s = kTargetWorkgroups / tiles;
+        if (s < 1) s = 1;
+        return s < most ? s : most;
+    };
+    p.bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    if (M > 128) {
+        auto cost = [&](int bm, double rate) {
+            const int64_t tiles = (M + bm - 1) / bm * p.tiles_k;
+            const int64_t s = splits_of(tiles);
+            const int64_t rounds = (tiles * s + kTargetWorkgroups - 1) / kTargetWorkgroups;
+            return (double)rounds * bm / ((double)s * rate);
+        };
+        if (cost(256, 1.0) <= cost(128, 0.8)) p.bm = 256;
+    }
+    p.tiles_m = (int)((M + p.bm - 1) / p.bm);
+    p.splits = (int)splits_of((int64_t)p.tiles_m * p.tiles_k);
+    p.part_bytes = forced || p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)K * 4 : 0;
+    return p;
+}
+
+hipError_t launch_grad(const GradPlan& plan, const GradCall& q, hipStream_t stream) {
+    GradArgs a{};
+    a.d = q.d;
+    a.ld = q.ld;
+    a.packed = q.packed;
+    a.dx = q.dx;
+    a.part = q.part;
+    a.add = q.add ? 1 : 0;
+    a.M = (int)q.M;
+    a.K = (int)q.K;
+    a.N = (int)q.N;
+    a.KB = (int)(q.K / kRowsPerBlock);
+    a.UW = (int)padded_units(q.K, q.G);
+    a.n0 = (int)q.n0;
+    a.n = (int)q.n;
+    a.tiles_m = plan.tiles_m;
+    a.tiles_k = plan.tiles_k;
+    a.splits = plan.splits;
+    if ((plan.splits > 1 || !q.dx) && !q.part) return hipErrorInvalidValue;
+    const int sub = units_per_block(q.G);
+    if (q.op_bf16) {
+        if (q.scale_bf16) launch_typed<true, true>(plan.bm, sub, a, stream);
+        else launch_typed<true, false>(plan.bm, sub, a, stream);
+    } else {
+        launch_typed<false, false>(plan.bm, sub, a, stream);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, const float* coef, uint16_t* dx,
+                              bool bf16, hipStream_t stream) {
+    const int64_t MK = M * K;
+    const dim3 grid((unsigned)((MK / 8 + 255) / 256)), block(256);
+    if (bf16) hipLaunchKernelGGL((grad_finish_kernel<true>), grid, block, 0, stream, part, splits, MK, (int)K, coef, dx);
+    else hipLaunchKernelGGL((grad_finish_kernel<false>), grid, block, 0, stream, part, splits, MK, (int)K, coef, dx);
+    return hipGetLastError();
+}
+
+}  // namespace w4a16

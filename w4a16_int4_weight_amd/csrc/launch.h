@@ -110,4 +110,80 @@ hipError_t launch_w4a8_quantize(const uint16_t* x, int64_t M, int64_t K, bool bf
 hipError_t launch_w4a8_gemm(const W4A8Act& a, const uint8_t* packed, const uint16_t* bias, uint16_t* y, int64_t M,
                             int64_t K, int64_t N, int64_t G, bool bf16, void* workspace, hipStream_t stream);
 
+// Tiles of the training and scoring products (csrc/tile_product.h): `cols` columns of the
+// weight (2F for a gated block), 8 waves of cbw column blocks, 16 mr rows.
+struct ProductPlan {
+    int mr, cbw, sub;
+    int tiles_m, tiles_n, splits;
+    size_t partial_bytes;  // fp32 partial tiles of a K split (0 without one)
+};
+ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gated);
+
+// Gated block: h = a(x Wg) (x Wu) when d is NULL; else d = [dg, du] bf16 [M, 2F] from dh.
+// act: 0 silu, 1 gelu, 2 gelu's tanh form. counters / partials as plan_product asks.
+struct GatedCall {
+    const uint16_t* x;
+    const uint16_t* dh;
+    const uint8_t* packed;
+    uint16_t* h;
+    uint16_t* d;
+    int64_t M, K, F, G;
+    int act;
+    bool bf16;
+    uint32_t* counters;
+    float* partials;
+};
+hipError_t launch_gated(const GatedCall& call, hipStream_t stream);
+
+// dx = coef . (D W^T): D [M, columns n0 .. n0 + n) of the weight, row stride ld, operands
+// bf16 (op_bf16) or fp16; out 16-bit of out_bf16. The sum over columns is split over
+// `splits` workgroups and may be cut into calls: with `part` set, partial tiles
+// [splits][M][K] fp32 are written (or, with `add`, added to); grad_finish sums them.
+struct GradCall {
+    const uint16_t* d;
+    int64_t ld;
+    const uint8_t* packed;
+    uint16_t* dx;          // NULL when `part` is set
+    float* part;
+    bool add;
+    int64_t M, K, N, G;    // N: columns of the weight
+    int64_t n0, n;         // n0 % 64 == 0
+    bool op_bf16, scale_bf16;
+    int splits;
+};
+struct GradPlan {
+    int bm;                // rows of a tile: 16, 32, 64, 128 or 256
+    int tiles_m, tiles_k;
+    int splits;
+    size_t part_bytes;     // [splits][M][K] fp32 when splits > 1
+};
+// `forced`: the sum comes in several calls, so partials are needed at any split.
+GradPlan plan_grad(int64_t M, int64_t K, int64_t n, bool forced);
+hipError_t launch_grad(const GradPlan& plan, const GradCall& call, hipStream_t stream);
+// dx[m, k] = coef[m] sum_s part[s][m][k], rounded once; a row whose
+// coef is zero is zero whatever its sum holds. coef may be NULL (1).
+hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, const float* coef, uint16_t* dx,
+                              bool bf16, hipStream_t stream);
+
+// Cross entropy (top NULL, T = 1) or distillation over the packed head. lse and loss
+// [M] fp32; dx (or NULL) with dloss (or NULL: 1). The workspace holds loss_workspace(...)
+// bytes whose counter part is zero; the kernels leave it zero.
+struct LossCall {
+    const uint16_t* x;
+    const int32_t* ids;    // [M, T]
+    const float* top;      // [M, T] teacher logits
+    const uint8_t* packed;
+    const float* dloss;
+    float* loss;
+    float* lse;
+    uint16_t* dx;
+    int64_t M, K, V, G, T;
+    float tau;
+    bool bf16;
+    void* workspace;
+};
+int max_loss_targets();
+size_t loss_workspace(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bool distill, bool grad);
+hipError_t launch_loss(const LossCall& call, hipStream_t stream);
+
 }  // namespace w4a16
