@@ -76,20 +76,28 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::S
     for (int r = 0; r < P::MR; ++r) {
 #pragma unroll
         for (int j = 0; j < HB; ++j) {
+            const int at = (16 * r + c) * kRow + 2 * (16 * (w * HB + j) + 4 * h);      // 4 columns of a row
+            float o0[4], o1[4];
+            uint2 dv = make_uint2(0u, 0u);
+            if constexpr (kGrad) dv = *reinterpret_cast<const uint2*>(t0 + at);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int at = (16 * r + 4 * h + e) * kRow + 2 * (16 * (w * HB + j) + c);
                 const float g = acc[r][j][e], u = acc[r][j + HB][e];
                 float slope;
                 const float pr = gate_prob<kAct>(g, &slope);
                 if constexpr (!kGrad) {
-                    *reinterpret_cast<uint16_t*>(t0 + at) = f32_to_half_bits<P::kBF16>(g * pr * u);
+                    o0[e] = g * pr * u;
                 } else {
-                    const float d = half_bits_to_f32<P::kBF16>(*reinterpret_cast<const uint16_t*>(t0 + at));
-                    *reinterpret_cast<uint16_t*>(t0 + at) = f32_to_half_bits<true>(d * u * fmaf(g, slope, pr));
-                    *reinterpret_cast<uint16_t*>(t1 + at) = f32_to_half_bits<true>(d * (g * pr));
+                    const uint32_t dw = e < 2 ? dv.x : dv.y;
+                    const float d = half_bits_to_f32<P::kBF16>(e & 1 ? dw >> 16 : dw & 0xFFFFu);
+                    o0[e] = d * u * fmaf(g, slope, pr);
+                    o1[e] = d * (g * pr);
                 }
             }
+            constexpr bool kOut = kGrad || P::kBF16;
+            *reinterpret_cast<uint2*>(t0 + at) = make_uint2(pack2_rne<kOut>(o0[0], o0[1]), pack2_rne<kOut>(o0[2], o0[3]));
+            if constexpr (kGrad)
+                *reinterpret_cast<uint2*>(t1 + at) = make_uint2(pack2_rne<true>(o1[0], o1[1]), pack2_rne<true>(o1[2], o1[3]));
         }
     }
     __syncthreads();

@@ -37,23 +37,6 @@ struct LossArgs {
     int ldq;
 };
 
-template <int kRor>
-__device__ __forceinline__ float dpp_ror(float v) {      // lane c takes lane c - kRor of its 16
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + kRor, 0xF, 0xF, false));
-}
-__device__ __forceinline__ float max16(float v) {
-    v = fmaxf(v, dpp_ror<8>(v));
-    v = fmaxf(v, dpp_ror<4>(v));
-    v = fmaxf(v, dpp_ror<2>(v));
-    return fmaxf(v, dpp_ror<1>(v));
-}
-__device__ __forceinline__ float sum16(float v) {
-    v += dpp_ror<8>(v);
-    v += dpp_ror<4>(v);
-    v += dpp_ror<2>(v);
-    return v + dpp_ror<1>(v);
-}
-
 template <class P>
 __device__ __forceinline__ void stats_epilogue(const LossArgs& a, typename P::Shared& sh, int m0, int n_tile,
                                                f32x4 (&acc)[P::MR][P::CBW]) {
@@ -85,7 +68,7 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, typename P::Sh
 #pragma unroll
             for (int j = 0; j < P::CBW; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) scratch[(4 * h + e) * kPitch + 16 * j + c] = acc[r][j][e];
+                for (int e = 0; e < 4; ++e) scratch[c * kPitch + 16 * j + 4 * h + e] = acc[r][j][e];
             __builtin_amdgcn_wave_barrier();
             if (any) {
                 for (int j = h; j < T; j += 4) {
@@ -95,22 +78,23 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, typename P::Sh
             }
             __builtin_amdgcn_wave_barrier();
         }
+        float top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float top = -INFINITY;
+        for (int j = 0; j < P::CBW; ++j)
 #pragma unroll
-            for (int j = 0; j < P::CBW; ++j) {
-                if (nw + 16 * j + c >= N) acc[r][j][e] = -INFINITY;
+            for (int e = 0; e < 4; ++e) {
+                if (nw + 16 * j + 4 * h + e >= N) acc[r][j][e] = -INFINITY;
                 top = fmaxf(top, acc[r][j][e]);
             }
-            top = max16(top);
-            const float ref = top == -INFINITY ? 0.f : top;
-            float sum = 0.f;
+        top = quarter_max(top);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < P::CBW; ++j) sum += __expf(acc[r][j][e] - ref);
-            sum = sum16(sum);
-            if (c == 0) red[w * P::BM + 16 * r + 4 * h + e] = make_float2(top, sum);
-        }
+        for (int j = 0; j < P::CBW; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += __expf(acc[r][j][e] - ref);
+        sum = quarter_sum(sum);
+        if (h == 0) red[w * P::BM + 16 * r + c] = make_float2(top, sum);
     }
     __syncthreads();
     if (tid < P::BM && m0 + tid < M) {
@@ -141,17 +125,17 @@ __device__ __forceinline__ void prob_epilogue(const LossArgs& a, typename P::Sha
     const int n0 = a.p.n_begin + n_tile * P::BN;
 #pragma unroll
     for (int r = 0; r < P::MR; ++r) {
+        const int row = 16 * r + c;
+        const int m = m0 + row < M ? m0 + row : M - 1;
+        const float lse = a.lse[m];
+        const bool live = a.coef[m] != 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = 16 * r + 4 * h + e;
-            const int m = m0 + row < M ? m0 + row : M - 1;
-            const float lse = a.lse[m];
-            const bool live = a.coef[m] != 0.f;
+        for (int j = 0; j < P::CBW; ++j) {
+            float q[4];
 #pragma unroll
-            for (int j = 0; j < P::CBW; ++j) {
-                const float q = live ? __expf(acc[r][j][e] * a.inv_tau - lse) : 0.f;
-                *reinterpret_cast<uint16_t*>(tile + row * kRow + 2 * (16 * (w * P::CBW + j) + c)) = f32_to_half_bits<true>(q);
-            }
+            for (int e = 0; e < 4; ++e) q[e] = live ? __expf(acc[r][j][e] * a.inv_tau - lse) : 0.f;
+            *reinterpret_cast<uint2*>(tile + row * kRow + 2 * (16 * (w * P::CBW + j) + 4 * h)) =
+                make_uint2(pack2_rne<true>(q[0], q[1]), pack2_rne<true>(q[2], q[3]));
         }
     }
     __syncthreads();

@@ -18,8 +18,14 @@
 // XOR-swizzled by row) and the waves' packed codes, filled by direct global -> LDS
 // copies; a wave decodes its codes of the block into registers once and runs through
 // its MR row fragments with them, so each weight is decoded once per 16 MR rows.
-// X is summed by wave r for fragment r while it multiplies, passed on through LDS and
-// taken off one block later, behind the barrier that the ring needs anyway.
+// What bounds it at 128 rows: the issue of vector instructions between the MFMAs (about 3
+// each) and the registers that let them be placed there. Measured on 4096 x 2048 x 131072
+// with the loss's epilogue: 3530 us with the decoding and scaling left to the compiler's
+// order, 2420 us in the order below and with the zero points on the matrix cores (bf16,
+// 908 TFLOP/s; fp16, whose codes lose their zero point in 16 bits, 2230 us).
+// X is summed by wave r for fragment r, passed on through LDS and taken off every fourth
+// row block. The MFMA takes the weights as its first operand, so a lane holds four adjacent
+// columns of one row.
 #pragma once
 
 #include <stddef.h>
@@ -71,6 +77,22 @@ __device__ __forceinline__ float product_dot2(uint32_t a, uint32_t b, float c) {
         return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c, false);
 }
 
+// sum and maximum over the four lanes c, c + 16, c + 32, c + 48, left in all four
+__device__ __forceinline__ float quarter_sum(float v) {
+    typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+    u32x2_t p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+__device__ __forceinline__ float quarter_max(float v) {
+    typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+    u32x2_t p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
 template <bool kBF16_, int MR_, int CBW_, int W_, int kSub_, bool kGated_>
 struct TileProduct {
     static constexpr bool kBF16 = kBF16_, kGated = kGated_;
@@ -83,20 +105,25 @@ struct TileProduct {
     static constexpr int kSlabs = (kXSlabs + W - 1) / W;   // copied per wave (a wave without one of its own repeats one)
     static constexpr int kDma = kSlabs + CBW;              // copies per wave and stage
     static constexpr int kMeta = CBW * kSub;               // + these every 4th stage
+    static constexpr int kUnits = 4 * kSub;                // metadata units of a group of 4 row blocks
+    // Stages t and t + 1 are read in turn t, t + 2 is on its way. (Rings of 4 to 6 stages, where
+    // they fit, measured the same for 64-row tiles and 15% slower for 16-row ones, which then
+    // run one workgroup a compute unit instead of two.)
+    static constexpr int kStages = 3;
+    static constexpr int kMetaSlots = 2;                   // a group's is read until its last block is done
     struct Stage {
         uint4 x[BM * 16];                 // chunk j of row r at chunk j ^ (r % 16)
         uint4 w[W * CBW * 64];
     };
-    // two stages where three do not fit beside the metadata
-    static constexpr int kStages = 3 * sizeof(Stage) + 2 * W * kMeta * 256 + 8192 <= 160 * 1024 ? 3 : 2;
     struct Shared {
         Stage ring[kStages];
-        uint32_t meta[2][W][64 * kMeta];  // [column of the wave][unit of 4 row blocks]
-        float xsum[2][kSub][BM];
+        uint32_t meta[kMetaSlots][W][64 * kMeta];  // [group of 4 row blocks][column of the wave][its units]
+        float scale[W][kSub][16 * CBW];   // one row block's, passed between the lanes of a wave
+        float xsum[2][kUnits][BM];        // [group % 2][unit]
     };
     static_assert(!kGated || CBW % 2 == 0, "a gated wave holds both halves");
     static_assert(MR <= W, "wave r sums the activations of fragment r");
-    static_assert(sizeof(Shared) <= 160 * 1024, "LDS");
+    static_assert(sizeof(Shared) + 16 <= 160 * 1024, "LDS");
 
     // weight column of lane column c in block j of wave w (clamped into the weight)
     static __device__ __forceinline__ int column(const ProductArgs& a, int n_tile, int w, int j, int c) {
@@ -110,6 +137,13 @@ struct TileProduct {
         }
     }
 
+    // one row block's decoded operands and scales
+    struct Operands {
+        uint4 b[CBW][4];
+        f32x4 s[CBW][kSub];               // columns 4 h .. 4 h + 3 of block j
+    };
+
+    // acc[r][j] register e of lane (c, h): row 16 r + c, column 16 j + 4 h + e of the wave
     static __device__ __forceinline__ void run(const ProductArgs& a, Shared& sh, int m_tile, int n_tile, int split,
                                                f32x4 (&acc)[MR][CBW]) {
         const int K = a.K;
@@ -160,11 +194,11 @@ struct TileProduct {
             for (int q = 0; q < kSlabs; ++q)
                 dma16(xbase + (size_t)kb * kRowsPerBlock * 2, xoff[q], st + (uint32_t)xslab[q] * 1024u);
             if ((t & 3) == 0) {
-                const uint32_t dst = meta_base + (uint32_t)((t >> 2) & 1) * (uint32_t)(W * kMeta * 256);
+                const uint32_t dst = meta_base + (uint32_t)((t >> 2) % kMetaSlots) * (uint32_t)(W * kMeta * 256);
 #pragma unroll
                 for (int i = 0; i < kMeta; ++i) {
                     const int wi = 64 * i + lane;
-                    const int cl = (wi / (4 * kSub)) & 15, u = wi % (4 * kSub);
+                    const int cl = (wi / kUnits) & 15, u = wi % kUnits;
                     const int j = i / kSub;
                     const int n = column(a, n_tile, w, j, cl);
                     const int first = column(a, n_tile, w, j, 0);
@@ -173,124 +207,380 @@ struct TileProduct {
                 }
             }
         };
-
+        // this wave's copies of stages t and t + 1 have landed (later ones may be on their way;
+        // metadata copies among them only make the wait longer), and everyone's after the barrier
+        auto arrive = [&](int t) {
+            if (t + kStages - 2 < nkb) wait_vmcnt<(kStages - 3) * kDma>();
+            else wait_vmcnt<0>();
+            wait_lgkmcnt0();
+            lds_barrier();
+        };
+        auto word = [](const uint4& q, int i) { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; };
+        // scales of block t: each lane converts its own column's and reads back those of the
+        // four columns its accumulators hold
+        auto scales = [&](Operands& o, int t, uint32_t (&md)[CBW][kSub]) {
+#pragma unroll
+            for (int j = 0; j < CBW; ++j)
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    md[j][u] = sh.meta[(t >> 2) % kMetaSlots][w][(16 * j + c) * kUnits + (t & 3) * kSub + u];
+                    sh.scale[w][u][16 * j + c] = half_bits_to_f32<kBF16>(md[j][u] & 0xFFFFu);
+                }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int j = 0; j < CBW; ++j)
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) o.s[j][u] = *reinterpret_cast<const f32x4*>(&sh.scale[w][u][16 * j + 4 * h]);
+            __builtin_amdgcn_wave_barrier();
+        };
+        auto decode = [&](Operands& o, int j, int i, uint32_t d, const uint32_t (&md)[CBW][kSub]) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = ((d >> (4 * e)) & 0x000F000Fu) | Magic<kBF16>::kBase2;
+            if constexpr (!kBF16) {
+                const _Float16 zb = (_Float16)(1024.0f + (float)((md[j][(i * kSub) / 4] >> 16) & 0xFu));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    p[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p[e]) - f16x2{zb, zb});
+            }
+            o.b[j][i] = make_uint4(p[0], p[1], p[2], p[3]);
+        };
+        // Zero points of the group of row blocks 4 g .. 4 g + n - 1, by the matrix cores:
+        // acc -= sum over its units of s (128 + z) X. Lane quarter h takes unit 4 v + h of
+        // MFMA v. X (24 bits) is cut into three bf16 values, s (128 + z) (16 bits) into two,
+        // each exactly, and their six products fill six of a quarter's eight places.
+        auto take_off = [&](int g, int n) {
+#pragma unroll
+            for (int v = 0; v < kSub; ++v) {
+                const int u = 4 * v + h;
+                const bool in = u < n * kSub;
+                uint4 S[CBW];
+#pragma unroll
+                for (int j = 0; j < CBW; ++j) {
+                    const uint32_t md = sh.meta[g % kMetaSlots][w][(16 * j + c) * kUnits + u];
+                    const float f = -half_bits_to_f32<true>(md & 0xFFFFu) * (128.f + (float)((md >> 16) & 0xFu));
+                    const float f1 = bf16_bits_to_f32(f32_to_half_bits<true>(f));
+                    const uint32_t p = in ? pack2_rne<true>(f1, f - f1) : 0u;
+                    S[j] = make_uint4(p, p, p, 0u);
+                }
+#pragma unroll
+                for (int r = 0; r < MR; ++r) {
+                    const float X = in ? sh.xsum[g & 1][u][16 * r + c] : 0.f;
+                    const uint32_t x1 = f32_to_half_bits<true>(X);
+                    const float r1 = X - bf16_bits_to_f32(x1);
+                    const uint32_t x2 = f32_to_half_bits<true>(r1);
+                    const uint32_t x3 = f32_to_half_bits<true>(r1 - bf16_bits_to_f32(x2));
+                    const uint4 xx = make_uint4(x1 * 0x10001u, x2 * 0x10001u, x3 * 0x10001u, 0u);
+#pragma unroll
+                    for (int j = 0; j < CBW; ++j) acc[r][j] = mfma16x16x32<true>(S[j], xx, acc[r][j]);
+                }
+            }
+        };
 #pragma unroll
         for (int r = 0; r < MR; ++r)
 #pragma unroll
             for (int j = 0; j < CBW; ++j) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        float szp[CBW][kSub];             // s (b + z) of the block before
-        if constexpr (kBF16) {
+
+        // Block t on operands `cur`; block t + 1 is decoded into `nxt` behind its MFMAs, and
+        // each fragment is scaled behind those of the next. Stages t and t + 1 are in LDS,
+        // t + 2 is on its way.
+        auto block = [&](int t, Operands& cur, Operands& nxt) {
+            arrive(t);
+            if (t + kStages - 1 < nkb) issue(t + kStages - 1);
+            if constexpr (kBF16) {
+                if ((t & 3) == 0 && t > 0) take_off((t >> 2) - 1, 4);
+            }
+            const Stage& st = sh.ring[t % kStages];
+            const Stage& sn = sh.ring[(t + 1) % kStages];
+            uint4 q[CBW], f[4], fn[4];
+            uint32_t md[CBW][kSub];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = st.x[c * 16 + ((4 * i + h) ^ c)];
+#pragma unroll
+            for (int j = 0; j < CBW; ++j) q[j] = sn.w[(w * CBW + j) * 64 + lane];
+            scales(nxt, t + 1, md);
+            if constexpr (kBF16) {
+                // X of fragment w % MR (four lanes write the same value)
+                const int rx = w % MR;
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    float X = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4 / kSub; ++i) {
+                        const uint4 v = st.x[(16 * rx + c) * 16 + ((4 * (u * (4 / kSub) + i) + h) ^ c)];
+                        X = product_dot2<true>(v.x, 0x3F803F80u, X);
+                        X = product_dot2<true>(v.y, 0x3F803F80u, X);
+                        X = product_dot2<true>(v.z, 0x3F803F80u, X);
+                        X = product_dot2<true>(v.w, 0x3F803F80u, X);
+                    }
+                    X = quarter_sum(X);
+                    sh.xsum[(t >> 2) & 1][(t & 3) * kSub + u][16 * rx + c] = X;
+                }
+            }
+            f32x4 T[2][CBW][kSub];
+            constexpr int kWords = (4 * CBW + MR - 1) / MR;              // decoded behind a fragment
+#pragma unroll
+            for (int r = 0; r < MR; ++r) {
+                if (r + 1 < MR) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) fn[i] = st.x[(16 * (r + 1) + c) * 16 + ((4 * i + h) ^ c)];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < CBW; ++j) {
+                        const int u = i * kSub / 4;
+                        const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
+                        T[r & 1][j][u] = mfma16x16x32<kBF16>(cur.b[j][i], f[i], i % (4 / kSub) == 0 ? zero : T[r & 1][j][u]);
+                    }
+                if (r > 0) {
+#pragma unroll
+                    for (int j = 0; j < CBW; ++j)
+#pragma unroll
+                        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc[r - 1][j][e] = fmaf(cur.s[j][u][e], T[(r - 1) & 1][j][u][e], acc[r - 1][j][e]);
+                }
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) {
+                    const int wd = r * kWords + k;
+                    if (wd < 4 * CBW) decode(nxt, wd / 4, wd % 4, word(q[wd / 4], wd % 4), md);
+                }
+                if (r + 1 < MR) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = fn[i];
+                }
+            }
 #pragma unroll
             for (int j = 0; j < CBW; ++j)
 #pragma unroll
-                for (int u = 0; u < kSub; ++u) szp[j][u] = 0.f;
-            for (int i = tid; i < kSub * BM; i += kThreads) (&sh.xsum[1][0][0])[i] = 0.f;
-        }
-        auto take_off = [&](int t, int r) {           // the zero points of block t, fragment r
+                for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                const f32x4 X = *reinterpret_cast<const f32x4*>(&sh.xsum[t & 1][u][16 * r + 4 * h]);
+                    for (int e = 0; e < 4; ++e)
+                        acc[MR - 1][j][e] = fmaf(cur.s[j][u][e], T[(MR - 1) & 1][j][u][e], acc[MR - 1][j][e]);
+            // keep the decoding and the sums in this block: they would be moved down to
+            // their next use, behind the barrier and away from the MFMAs that hide them
 #pragma unroll
-                for (int j = 0; j < CBW; ++j)
+            for (int j = 0; j < CBW; ++j) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[r][j][e] = fmaf(-szp[j][u], X[e], acc[r][j][e]);
+                for (int i = 0; i < 4; ++i)
+                    asm volatile("" : "+v"(nxt.b[j][i].x), "+v"(nxt.b[j][i].y), "+v"(nxt.b[j][i].z), "+v"(nxt.b[j][i].w));
+#pragma unroll
+                for (int r = 0; r < MR; ++r) asm volatile("" : "+v"(acc[r][j]));
             }
         };
 
-        issue(0);
-        if constexpr (kStages == 3) {
-            if (nkb > 1) issue(1);
-        }
-        for (int t = 0; t < nkb; ++t) {
-            if (kStages == 2 || t + 1 >= nkb) wait_vmcnt<0>();
-            else if (((t + 1) & 3) == 0) wait_vmcnt<kDma + kMeta>();
-            else wait_vmcnt<kDma>();
-            wait_lgkmcnt0();
-            lds_barrier();
-            if (t + kStages - 1 < nkb) issue(t + kStages - 1);
-
-            const Stage& st = sh.ring[t % kStages];
-            uint4 b[CBW][4];
-            float s[CBW][kSub], sz[CBW][kSub];
+        Operands ops[2];
+        if constexpr (MR >= 2) {
+            // Tiles of several fragments: one MFMA, then a few vector instructions, in this
+            // order (sched_barrier keeps it): a wave hides two or three of them behind each
+            // MFMA, not a burst. The last fragment of a block is multiplied behind the next
+            // block's barrier, where the first reads of LDS are on their way; a fragment is
+            // scaled behind the one after it.
+            f32x4 T[2][CBW][kSub], sc[CBW][kSub];
+            uint4 f[2][4];
+            constexpr int kFma = 4 * CBW * kSub;
+            constexpr int kN = 4 * CBW;                                  // MFMAs of a fragment
+            auto read_scale = [&](int j, int u) {
+                sc[j][u] = *reinterpret_cast<const f32x4*>(&sh.scale[w][u][16 * j + 4 * h]);
+            };
+            auto write_scale = [&](int j, int u, uint32_t m) {
+                sh.scale[w][u][16 * j + c] = half_bits_to_f32<kBF16>(m & 0xFFFFu);
+            };
+            // behind the last fragment of a block the next block's scales come in, each
+            // after its last use
+            auto scale_part = [&](int r, int from, int to) {
 #pragma unroll
-            for (int j = 0; j < CBW; ++j) {
-                const uint4 q = st.w[(w * CBW + j) * 64 + lane];
-                uint32_t md[kSub];
-#pragma unroll
-                for (int u = 0; u < kSub; ++u) {
-                    md[u] = sh.meta[(t >> 2) & 1][w][(16 * j + c) * 4 * kSub + (t & 3) * kSub + u];
-                    s[j][u] = half_bits_to_f32<kBF16>(md[u] & 0xFFFFu);
-                    sz[j][u] = s[j][u] * (128.f + (float)((md[u] >> 16) & 0xFu));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t d = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
-                    uint32_t p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ((d >> (4 * e)) & 0x000F000Fu) | Magic<kBF16>::kBase2;
-                    if constexpr (!kBF16) {
-                        const _Float16 zb = (_Float16)(1024.0f + (float)((md[(i * kSub) / 4] >> 16) & 0xFu));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            p[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p[e]) - f16x2{zb, zb});
+                for (int i = 0; i < kFma; ++i)
+                    if (i >= from && i < to) {
+                        const int u = i / (4 * CBW), j = i / 4 % CBW, e = i % 4;
+                        acc[r][j][e] = fmaf(sc[j][u][e], T[r & 1][j][u][e], acc[r][j][e]);
+                        if (r == MR - 1 && e == 3) read_scale(j, u);
                     }
-                    b[j][i] = make_uint4(p[0], p[1], p[2], p[3]);
+            };
+            auto mfma_slot = [&](const Operands& o, int r, int k) {
+                const int i = k / CBW, j = k % CBW, u = i * kSub / 4;
+                const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
+                T[r & 1][j][u] = mfma16x16x32<kBF16>(o.b[j][i], f[r & 1][i], i % (4 / kSub) == 0 ? zero : T[r & 1][j][u]);
+            };
+            auto wide_block = [&](int t, Operands& cur, Operands& nxt) {
+                arrive(t);
+                const Stage& st = sh.ring[t % kStages];
+                const Stage& sn = sh.ring[(t + 1) % kStages];
+                uint4 q[CBW];
+                uint32_t md[CBW][kSub];
+                [[maybe_unused]] uint4 xf[4];
+                [[maybe_unused]] float X[kSub];
+                [[maybe_unused]] const int rx = w % MR;
+                static_assert(MR % 2 == 0, "fragment 0 and the last one use different registers");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[0][i] = st.x[c * 16 + ((4 * i + h) ^ c)];
+#pragma unroll
+                for (int j = 0; j < CBW; ++j) {
+                    q[j] = sn.w[(w * CBW + j) * 64 + lane];
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u)
+                        md[j][u] = sh.meta[((t + 1) >> 2) % kMetaSlots][w][(16 * j + c) * kUnits + ((t + 1) & 3) * kSub + u];
                 }
-            }
-#pragma unroll
-            for (int r = 0; r < MR; ++r) {
-                uint4 f[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = st.x[(16 * r + c) * 16 + ((4 * i + h) ^ c)];
                 if constexpr (kBF16) {
-                    if (r == w) {
 #pragma unroll
-                        for (int u = 0; u < kSub; ++u) {
-                            float X = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 4 / kSub; ++i) {
-                                const uint4 v = f[u * (4 / kSub) + i];
-                                X = product_dot2<true>(v.x, 0x3F803F80u, X);
-                                X = product_dot2<true>(v.y, 0x3F803F80u, X);
-                                X = product_dot2<true>(v.z, 0x3F803F80u, X);
-                                X = product_dot2<true>(v.w, 0x3F803F80u, X);
-                            }
-                            X += __shfl_xor(X, 16);
-                            X += __shfl_xor(X, 32);
-                            if (h == 0) sh.xsum[t & 1][u][16 * r + c] = X;
-                        }
-                    }
-                    take_off(t + 1, r);               // block t - 1 (the same slot parity)
+                    for (int i = 0; i < 4; ++i) xf[i] = st.x[(16 * rx + c) * 16 + ((4 * i + h) ^ c)];
                 }
+                if (t + kStages - 1 < nkb) issue(t + kStages - 1);
+                __builtin_amdgcn_sched_barrier(0);
+                // phase 0: the last fragment of block t - 1; phase p: fragment p - 1
+#pragma unroll
+                for (int p = 0; p < MR; ++p) {
+                    const int r = p == 0 ? MR - 1 : p - 1;
+                    Operands& o = p == 0 ? nxt : cur;
+                    const int rs = p == 0 ? MR - 2 : p == 1 ? MR - 1 : p - 2;       // the fragment to scale
+                    constexpr int kPhases = MR - 1;
+#pragma unroll
+                    for (int k = 0; k < kN; ++k) {
+                        mfma_slot(o, r, k);
+                        // the next fragment's operands
+                        if (p >= 1 && k % CBW == 0) {
+                            const int i = k / CBW;
+                            f[p & 1][i] = st.x[(16 * p + c) * 16 + ((4 * i + h) ^ c)];
+                        }
+                        if (k >= 1) scale_part(rs, (k - 1) * kFma / (kN - 1), k * kFma / (kN - 1));
+                        if (p >= 1) {
+                            // words of block t + 1, a quarter (two codes a register) at a time
+                            const int all = 16 * CBW, at = (p - 1) * kN + k, slots = kPhases * kN;
+#pragma unroll
+                            for (int d = 0; d < 16 * CBW; ++d)
+                                if (d >= at * all / slots && d < (at + 1) * all / slots) {
+                                    const int j = d / 16, i = d / 4 % 4, e = d % 4;
+                                    const uint32_t wd = word(q[j], i);
+                                    uint32_t v = ((wd >> (4 * e)) & 0x000F000Fu) | Magic<kBF16>::kBase2;
+                                    if constexpr (!kBF16) {
+                                        const _Float16 zb = (_Float16)(1024.0f + (float)((md[j][(i * kSub) / 4] >> 16) & 0xFu));
+                                        v = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) - f16x2{zb, zb});
+                                    }
+                                    (e == 0 ? nxt.b[j][i].x : e == 1 ? nxt.b[j][i].y : e == 2 ? nxt.b[j][i].z : nxt.b[j][i].w) = v;
+                                }
+                        }
+                        // the block's sums of activations, two terms a slot
+                        if constexpr (kBF16) {
+                            constexpr int kFrom = MR > 2 ? kN : 0;
+                            const int at = p * kN + k - kFrom;
+                            if (at >= 0 && at < 8) {
+                                const int i = at / 2, u = i * kSub / 4;
+                                if (i % (4 / kSub) == 0 && at % 2 == 0) X[u] = 0.f;
+                                X[u] = product_dot2<true>(at % 2 ? xf[i].z : xf[i].x, 0x3F803F80u, X[u]);
+                                X[u] = product_dot2<true>(at % 2 ? xf[i].w : xf[i].y, 0x3F803F80u, X[u]);
+                            }
+                            if (at >= 8 && at < 8 + kSub) {
+                                const int u = at - 8;
+                                X[u] = quarter_sum(X[u]);
+                                sh.xsum[(t >> 2) & 1][(t & 3) * kSub + u][16 * rx + c] = X[u];
+                            }
+                        }
+                        // the scales of block t + 1, through LDS
+                        if (p == MR - 1 && k == kN - 1) {
+#pragma unroll
+                            for (int j = 0; j < CBW; ++j)
+#pragma unroll
+                                for (int u = 0; u < kSub; ++u) write_scale(j, u, md[j][u]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                // keep the decoding and the sums in this block: they would be moved down to
+                // their next use, behind the barrier and away from the MFMAs that hide them
+#pragma unroll
+                for (int j = 0; j < CBW; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        asm volatile("" : "+v"(nxt.b[j][i].x), "+v"(nxt.b[j][i].y), "+v"(nxt.b[j][i].z), "+v"(nxt.b[j][i].w));
+#pragma unroll
+                    for (int r = 0; r < MR; ++r) asm volatile("" : "+v"(acc[r][j]));
+                }
+            };
+            for (int t = 0; t < kStages - 1 && t < nkb; ++t) issue(t);
+            if (kStages - 1 <= nkb) wait_vmcnt<(kStages - 2) * kDma>();
+            else wait_vmcnt<0>();
+            {
+                uint32_t md[CBW][kSub];
 #pragma unroll
                 for (int j = 0; j < CBW; ++j) {
 #pragma unroll
                     for (int u = 0; u < kSub; ++u) {
-                        f32x4 T = f32x4{0.f, 0.f, 0.f, 0.f};
+                        md[j][u] = sh.meta[0][w][(16 * j + c) * kUnits + u];
+                        write_scale(j, u, md[j][u]);
+                    }
+                    const uint4 q = sh.ring[0].w[(w * CBW + j) * 64 + lane];
 #pragma unroll
-                        for (int i = 0; i < 4 / kSub; ++i)
-                            T = mfma16x16x32<kBF16>(f[u * (4 / kSub) + i], b[j][u * (4 / kSub) + i], T);
+                    for (int i = 0; i < 4; ++i) decode(ops[0], j, i, word(q, i), md);
+                }
+            }
+            // nothing before block 0
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[r][j][e] = fmaf(s[j][u], T[e], acc[r][j][e]);
+            for (int j = 0; j < CBW; ++j) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ops[1].b[j][i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    sc[j][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    T[0][j][u] = T[1][j][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[1][i] = make_uint4(0u, 0u, 0u, 0u);
+            auto last = [&](const Operands& o) {
+#pragma unroll
+                for (int k = 0; k < kN; ++k) mfma_slot(o, MR - 1, k);
+                scale_part(MR - 2, 0, kFma);
+                scale_part(MR - 1, 0, kFma);
+            };
+            int t = 0;
+            for (; t + 1 < nkb; t += 2) {
+                wide_block(t, ops[0], ops[1]);
+                wide_block(t + 1, ops[1], ops[0]);
+                if constexpr (kBF16) {
+                    if ((t & 3) == 2 && t + 2 < nkb) {
+                        wait_lgkmcnt0();
+                        lds_barrier();
+                        take_off(t >> 2, 4);
                     }
                 }
             }
-            if constexpr (kBF16) {
-#pragma unroll
-                for (int j = 0; j < CBW; ++j)
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u) szp[j][u] = sz[j][u];
+            if (t < nkb) {
+                wide_block(t, ops[0], ops[1]);
+                last(ops[0]);
+            } else {
+                last(ops[1]);
             }
-        }
-        if constexpr (kBF16) {
-            wait_lgkmcnt0();
-            lds_barrier();
+        } else {
+            for (int t = 0; t < kStages - 1 && t < nkb; ++t) issue(t);
+            if (kStages - 1 <= nkb) wait_vmcnt<(kStages - 2) * kDma>();
+            else wait_vmcnt<0>();
+            {
+                uint32_t md[CBW][kSub];
+                scales(ops[0], 0, md);
 #pragma unroll
-            for (int r = 0; r < MR; ++r) take_off(nkb - 1, r);
+                for (int j = 0; j < CBW; ++j) {
+                    const uint4 q = sh.ring[0].w[(w * CBW + j) * 64 + lane];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) decode(ops[0], j, i, word(q, i), md);
+                }
+            }
+            int t = 0;
+            for (; t + 1 < nkb; t += 2) {
+                block(t, ops[0], ops[1]);
+                block(t + 1, ops[1], ops[0]);
+            }
+            if (t < nkb) block(t, ops[0], ops[1]);
         }
-        // the ring may be reused by the caller: every wave is done with it
         wait_lgkmcnt0();
         lds_barrier();
+        if constexpr (kBF16) {
+            take_off((nkb - 1) >> 2, ((nkb - 1) & 3) + 1);
+            wait_lgkmcnt0();
+            lds_barrier();
+        }
+        // the ring may be reused by the caller: every wave is done with it
     }
 };
 
