@@ -191,7 +191,7 @@ w4a16_status w4a16_gemm_grad(const void* dy, const void* packed, size_t packed_b
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err = w4a16::launch_grad(plan, q, s);
     if (err == hipSuccess && part)
-        err = w4a16::launch_grad_finish(part, plan.splits, M, K, nullptr, static_cast<uint16_t*>(dx), bf16, s);
+        err = w4a16::launch_grad_finish(part, plan.splits, M, K, static_cast<uint16_t*>(dx), bf16, s);
     return from_hip(err);
 }
 
@@ -288,7 +288,7 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         g.op_bf16 = true;
         g.scale_bf16 = bf16;
         err = w4a16::launch_grad(plan, g, s);
-        if (err == hipSuccess && part) err = w4a16::launch_grad_finish(part, plan.splits, rows, K, nullptr, out, bf16, s);
+        if (err == hipSuccess && part) err = w4a16::launch_grad_finish(part, plan.splits, rows, K, out, bf16, s);
         if (err != hipSuccess) return W4A16_ERR_HIP;
     }
     return W4A16_OK;

@@ -40,6 +40,10 @@ struct GradArgs {
     int n0, n;              // this call's columns
     int tiles_m, tiles_k, splits;
     int add;
+    const int* hot;         // factors of D's rows and of what `add` adds to
+    const float* factor;
+    const float* before;
+    int factor_stages;      // stages of one column of `factor`
 };
 
 // 8 codes -> 8 operand values (q - z) s in row order
@@ -170,6 +174,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
 #pragma unroll
         for (int j = 0; j < CK; ++j) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    const bool hot = a.hot && *a.hot != 0;
     if (st_lo < st_hi) {
         load_codes(st_lo);
         issue_d(0, st_lo);
@@ -181,6 +186,21 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         wait_vmcnt<0>();                  // this wave's copies of stage t, and its codes of t + 1
         wait_lgkmcnt0();                  // its decoded rows of stage t are written
         lds_barrier();                    // everyone's; and everyone has read stage t - 1
+        if constexpr (kOpBF16) {
+            if (hot) {
+                const float* fac = a.factor + (size_t)(t / a.factor_stages) * a.M;
+                for (int q = tid; q < BM * 8; q += 512) {
+                    const int row = q >> 3;
+                    const float fr = fac[m0 + row < a.M ? m0 + row : a.M - 1];
+                    uint4 v = ring[slot].d[q];
+                    auto times = [&](uint32_t p) {
+                        return pack2_rne<true>(bf16_bits_to_f32(p & 0xFFFFu) * fr, bf16_bits_to_f32(p >> 16) * fr);
+                    };
+                    ring[slot].d[q] = make_uint4(times(v.x), times(v.y), times(v.z), times(v.w));
+                }
+                __syncthreads();
+            }
+        }
         if (t + 1 < st_hi) {
             issue_d(slot ^ 1, t + 1);
             store_codes(slot ^ 1);
@@ -230,7 +250,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
             f32x4 v = acc[r][j];
             if (a.part) {
                 f32x4* o = reinterpret_cast<f32x4*>(a.part + ((size_t)split * a.M + m) * a.K + k);
-                if (a.add) v += *o;
+                if (a.add) v += hot ? *o * a.before[m] : *o;
                 *o = v;
             } else {
                 const uint2 o = make_uint2(pack2_rne<kScaleBF16>(v[0], v[1]), pack2_rne<kScaleBF16>(v[2], v[3]));
@@ -240,27 +260,21 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     }
 }
 
-// dx = coef sum_s part[s], 8 values a thread; bandwidth-bound over the partials
+// dx = sum_s part[s], 8 values a thread; bandwidth-bound over the partials
 template <bool kBF16>
-__global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restrict__ part, int splits, int64_t MK, int K,
-                                                          const float* __restrict__ coef, uint16_t* __restrict__ dx) {
+__global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restrict__ part, int splits, int64_t MK,
+                                                          uint16_t* __restrict__ dx) {
     const int64_t at = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (at >= MK) return;
     f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+#pragma unroll 4
     for (int s = 0; s < splits; ++s) {
         const f32x4* p = reinterpret_cast<const f32x4*>(part + s * MK + at);
         s0 += p[0];
         s1 += p[1];
     }
-    uint4 o;
-    const float f = coef ? coef[at / K] : 1.f;
-    if (f == 0.f) {
-        o = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-        o = make_uint4(pack2_rne<kBF16>(s0[0] * f, s0[1] * f), pack2_rne<kBF16>(s0[2] * f, s0[3] * f),
-                       pack2_rne<kBF16>(s1[0] * f, s1[1] * f), pack2_rne<kBF16>(s1[2] * f, s1[3] * f));
-    }
-    *reinterpret_cast<uint4*>(dx + at) = o;
+    *reinterpret_cast<uint4*>(dx + at) = make_uint4(pack2_rne<kBF16>(s0[0], s0[1]), pack2_rne<kBF16>(s0[2], s0[3]),
+                                                    pack2_rne<kBF16>(s1[0], s1[1]), pack2_rne<kBF16>(s1[2], s1[3]));
 }
 
 template <bool kOp, bool kSc, int kSub>
@@ -328,6 +342,10 @@ hipError_t launch_grad(const GradPlan& plan, const GradCall& q, hipStream_t stre
     a.tiles_m = plan.tiles_m;
     a.tiles_k = plan.tiles_k;
     a.splits = plan.splits;
+    a.hot = q.hot;
+    a.factor = q.factor;
+    a.before = q.before;
+    a.factor_stages = q.factor_columns / kStageN;
     if ((plan.splits > 1 || !q.dx) && !q.part) return hipErrorInvalidValue;
     const int sub = units_per_block(q.G);
     if (q.op_bf16) {
@@ -339,12 +357,12 @@ hipError_t launch_grad(const GradPlan& plan, const GradCall& q, hipStream_t stre
     return hipGetLastError();
 }
 
-hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, const float* coef, uint16_t* dx,
-                              bool bf16, hipStream_t stream) {
+hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, uint16_t* dx, bool bf16,
+                              hipStream_t stream) {
     const int64_t MK = M * K;
     const dim3 grid((unsigned)((MK / 8 + 255) / 256)), block(256);
-    if (bf16) hipLaunchKernelGGL((grad_finish_kernel<true>), grid, block, 0, stream, part, splits, MK, (int)K, coef, dx);
-    else hipLaunchKernelGGL((grad_finish_kernel<false>), grid, block, 0, stream, part, splits, MK, (int)K, coef, dx);
+    if (bf16) hipLaunchKernelGGL((grad_finish_kernel<true>), grid, block, 0, stream, part, splits, MK, dx);
+    else hipLaunchKernelGGL((grad_finish_kernel<false>), grid, block, 0, stream, part, splits, MK, dx);
     return hipGetLastError();
 }
 

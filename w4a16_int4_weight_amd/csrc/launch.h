@@ -149,7 +149,12 @@ struct GradCall {
     int64_t M, K, N, G;    // N: columns of the weight
     int64_t n0, n;         // n0 % 64 == 0
     bool op_bf16, scale_bf16;
-    int splits;
+    // when *hot is set: D's rows are multiplied by factor[tile][M], tile of factor_columns
+    // columns from n0, and what `add` adds to by before[M]. hot may be NULL.
+    const int* hot;
+    const float* factor;
+    const float* before;
+    int factor_columns;
 };
 struct GradPlan {
     int bm;                // rows of a tile: 16, 32, 64, 128 or 256
@@ -160,10 +165,9 @@ struct GradPlan {
 // `forced`: the sum comes in several calls, so partials are needed at any split.
 GradPlan plan_grad(int64_t M, int64_t K, int64_t n, bool forced);
 hipError_t launch_grad(const GradPlan& plan, const GradCall& call, hipStream_t stream);
-// dx[m, k] = coef[m] sum_s part[s][m][k], rounded once; a row whose
-// coef is zero is zero whatever its sum holds. coef may be NULL (1).
-hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, const float* coef, uint16_t* dx,
-                              bool bf16, hipStream_t stream);
+// dx[m, k] = sum_s part[s][m][k], rounded once
+hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, uint16_t* dx, bool bf16,
+                              hipStream_t stream);
 
 // Cross entropy (top NULL, T = 1) or distillation over the packed head. lse and loss
 // [M] fp32; dx (or NULL) with dloss (or NULL: 1). The workspace holds loss_workspace(...)

@@ -4,18 +4,23 @@
 //   loss = tau^2 sum_j p_j (log p_j - z_{id_j} + lse)          (p: the row's targets)
 //   dx   = dloss tau sum_v (q_v - sum_{j: id_j = v} p_j) W_v
 //
-// Cross entropy is one target of weight 1 at tau = 1. Three steps:
-//   1. statistics: each tile of x . W leaves per row its maximum m and sum e^{z - m}
-//      (fp32) and the logits of the row's targets; the tile itself is dropped;
-//   2. rows: the tiles' (m, sum) joined in a fixed order into lse, the loss, and the
-//      row's factor dloss tau (0 for a row without a target: its dx is zero whatever x
-//      holds);
-//   3. with a gradient, piece by piece of the vocabulary: the tile again, q - p rounded
-//      once to bf16 (for fp16 too: probabilities go below fp16's range) into a piece
-//      buffer, and the product with W^T of that piece, added up in fp32.
-// Recomputing the tile costs one product more than keeping e^{z - m} would, and gives
-// q - p in fp32 before its one rounding: for a confident row q_target - 1 is small and a
-// difference of two rounded numbers would lose it.
+// Cross entropy is one target of weight 1 at tau = 1. The targets' own logits are short
+// dot products with single columns, taken by a kernel of their own; the vocabulary is
+// met in tiles of x W.
+//
+// Every row has a reference r from the start, its largest target logit. Each tile leaves,
+// per row, the sum of P = e^{z - r} (fp32), and a last kernel joins them in a fixed order.
+// With a gradient each tile is still formed once (bf16): P goes to a piece buffer as it is
+// formed, the product with W^T of that piece follows, and at the end
+// dx = e^{r - lse} (P W^T). r need only lie within 40 of the row's maximum: P is bf16, of
+// fp32's range. A row that goes higher in some tile takes that tile's maximum as the tile's
+// reference, and the product with W^T brings the row's tiles to a common one ("hot": rare,
+// right for any logits, off the usual path).
+// fp16 has not that range: there the statistics come first, in a product of their own, and
+// P = 2^15 q is formed with r = lse - 15 log 2, in fp16 (the target term of a loss in fp16
+// is 8 times finer than bf16's rounding).
+// The targets' columns are zero in P and enter at the end in fp32, (q_t - p_t) W_t: for a
+// confident row that difference is small, and of two rounded numbers it would be lost.
 #include "device_common.h"
 #include "launch.h"
 #include "tile_product.h"
@@ -23,136 +28,118 @@
 namespace w4a16 {
 namespace {
 
+constexpr float kHeadroom = 40.f;           // far inside fp32's range, sums and gains too
+constexpr int kShiftBits = 15;              // fp16: P = 2^15 q
+
 struct LossArgs {
     ProductArgs p;
     float inv_tau;
-    int T;
-    const int32_t* ids;      // [M, T] targets, negative or past the head: none
-    const float* weight;     // [M, T] or NULL (1)
-    float* zsel;             // [M, T] logits of the targets
-    float2* part;            // [tiles_n][M] (max, sum) of a tile's row
-    const float* lse;        // [M]
-    const float* coef;       // [M], 0: no gradient
-    uint16_t* q;             // [M, ldq] bf16
+    float2* part;            // [tiles_n][M] (reference, sum) of a tile's row, from this launch's first tile
+    const float* ref;        // [M]
+    uint16_t* q;             // [M, ldq] P
     int ldq;
+    int* hot;                // set when a tile took a reference of its own
 };
 
-template <class P>
-__device__ __forceinline__ void stats_epilogue(const LossArgs& a, typename P::Shared& sh, int m0, int n_tile,
-                                               f32x4 (&acc)[P::MR][P::CBW]) {
-    constexpr int kCols = 16 * P::CBW;                       // of a wave
-    constexpr int kPitch = kCols + 1;
-    const int tid = threadIdx.x;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lane = tid & 63;
-    const int c = lane & 15, h = lane >> 4;
-    const int M = a.p.M, N = a.p.N, T = a.T;
-    float* scratch = reinterpret_cast<float*>(&sh) + w * 16 * kPitch;          // 16 rows of this wave
-    float2* red = reinterpret_cast<float2*>(reinterpret_cast<float*>(&sh) + P::W * 16 * kPitch);   // [W][BM]
-    static_assert(P::W * 16 * kPitch * 4 + P::W * P::BM * 8 <= (int)sizeof(typename P::Shared), "LDS");
-    const int nw = a.p.n_begin + n_tile * P::BN + w * kCols;                   // the wave's first column
-#pragma unroll
-    for (int r = 0; r < P::MR; ++r) {
-#pragma unroll
-        for (int j = 0; j < P::CBW; ++j) acc[r][j] *= a.inv_tau;
-        // targets among this wave's columns: row 16 r + c, entries h, h + 4, ...
-        const int m = m0 + 16 * r + c;
-        bool any = false;
-        if (m < M) {
-            for (int j = h; j < T; j += 4) {
-                const int id = a.ids[(size_t)m * T + j];
-                any |= id >= nw && id < nw + kCols && id < N;
-            }
-        }
-        if (__any(any)) {
-#pragma unroll
-            for (int j = 0; j < P::CBW; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) scratch[c * kPitch + 16 * j + 4 * h + e] = acc[r][j][e];
-            __builtin_amdgcn_wave_barrier();
-            if (any) {
-                for (int j = h; j < T; j += 4) {
-                    const int id = a.ids[(size_t)m * T + j];
-                    if (id >= nw && id < nw + kCols && id < N) a.zsel[(size_t)m * T + j] = scratch[c * kPitch + id - nw];
-                }
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < P::CBW; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (nw + 16 * j + 4 * h + e >= N) acc[r][j][e] = -INFINITY;
-                top = fmaxf(top, acc[r][j][e]);
-            }
-        top = quarter_max(top);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < P::CBW; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum += __expf(acc[r][j][e] - ref);
-        sum = quarter_sum(sum);
-        if (h == 0) red[w * P::BM + 16 * r + c] = make_float2(top, sum);
-    }
-    __syncthreads();
-    if (tid < P::BM && m0 + tid < M) {
-        float2 v = red[tid];
-#pragma unroll
-        for (int i = 1; i < P::W; ++i) {
-            const float2 o = red[i * P::BM + tid];
-            const float top = fmaxf(v.x, o.x);
-            if (top != -INFINITY) v = make_float2(top, v.y * __expf(v.x - top) + o.y * __expf(o.x - top));
-        }
-        a.part[(size_t)n_tile * M + m0 + tid] = v;
-    }
-}
-
-// q - p of the tile, bf16
-template <class P>
-__device__ __forceinline__ void prob_epilogue(const LossArgs& a, typename P::Shared& sh, int m0, int n_tile,
+// kSums: the rows' sums over the tile; kOut: P of the tile to the piece buffer
+template <class P, bool kSums, bool kOut>
+__device__ __forceinline__ void loss_epilogue(const LossArgs& a, typename P::Shared& sh, int m0, int n_tile,
                                               f32x4 (&acc)[P::MR][P::CBW]) {
     constexpr int kRow = P::BN * 2 + 16;
     constexpr int kChunks = P::BN / 8;
-    static_assert(P::BM * kRow <= (int)sizeof(typename P::Shared), "LDS");
+    static_assert(P::BM * kRow + P::W * P::BM * 4 + 64 <= (int)sizeof(typename P::Shared), "LDS");
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lane = tid & 63;
     const int c = lane & 15, h = lane >> 4;
-    const int M = a.p.M, T = a.T;
+    const int M = a.p.M;
     uint8_t* tile = reinterpret_cast<uint8_t*>(&sh);
+    float* red = reinterpret_cast<float*>(tile + P::BM * kRow);                // [W][BM]
+    int* flag = reinterpret_cast<int*>(red + P::W * P::BM);
     const int n0 = a.p.n_begin + n_tile * P::BN;
+    const int nw = n0 + w * 16 * P::CBW;
+    const bool whole = nw + 16 * P::CBW <= a.p.N;
+    float ref[P::MR];
 #pragma unroll
     for (int r = 0; r < P::MR; ++r) {
-        const int row = 16 * r + c;
-        const int m = m0 + row < M ? m0 + row : M - 1;
-        const float lse = a.lse[m];
-        const bool live = a.coef[m] != 0.f;
-#pragma unroll
-        for (int j = 0; j < P::CBW; ++j) {
-            float q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = live ? __expf(acc[r][j][e] * a.inv_tau - lse) : 0.f;
-            *reinterpret_cast<uint2*>(tile + row * kRow + 2 * (16 * (w * P::CBW + j) + 4 * h)) =
-                make_uint2(pack2_rne<true>(q[0], q[1]), pack2_rne<true>(q[2], q[3]));
-        }
+        const int m = m0 + 16 * r + c;
+        ref[r] = a.ref[m < M ? m : M - 1];
     }
-    __syncthreads();
-    // the targets' entries, again in fp32 from the logit kept in step 1 (a row's ids are
-    // distinct here, so no entry has two writers)
-    for (int row = tid >> 2; row < P::BM; row += P::kThreads / 4) {
-        const int m = m0 + row;
-        if (m >= M || a.coef[m] == 0.f) continue;
-        for (int j = tid & 3; j < T; j += 4) {
-            const int id = a.ids[(size_t)m * T + j];
-            if (id < n0 || id >= n0 + P::BN || id >= a.p.N) continue;
-            const float p = a.weight ? a.weight[(size_t)m * T + j] : 1.f;
-            *reinterpret_cast<uint16_t*>(tile + row * kRow + 2 * (id - n0)) =
-                f32_to_half_bits<true>(__expf(a.zsel[(size_t)m * T + j] - a.lse[m]) - p);
+    auto emit = [&](const float* rf) -> bool {       // true: a sum is out of range (or no number)
+        bool high = false;
+#pragma unroll
+        for (int r = 0; r < P::MR; ++r) {
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < P::CBW; ++j) {
+                float q[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    q[e] = __expf(fmaf(acc[r][j][e], a.inv_tau, -rf[r]));
+                    if (!whole && nw + 16 * j + 4 * h + e >= a.p.N) q[e] = 0.f;
+                    sum += q[e];
+                }
+                if constexpr (kOut)
+                    *reinterpret_cast<uint2*>(tile + (16 * r + c) * kRow + 2 * (16 * (w * P::CBW + j) + 4 * h)) =
+                        make_uint2(pack2_rne<P::kBF16>(q[0], q[1]), pack2_rne<P::kBF16>(q[2], q[3]));
+            }
+            if constexpr (kSums) {
+                high |= !(sum < 2e17f);              // e^40
+                sum = quarter_sum(sum);
+                if (h == 0) red[w * P::BM + 16 * r + c] = sum;
+            }
         }
+        return high;
+    };
+    if constexpr (kSums) {
+        if (tid == 0) *flag = 0;
+        __syncthreads();
     }
-    __syncthreads();
+    const bool high = emit(ref);
+    if constexpr (kSums) {
+        if (high) *flag = 1;
+        __syncthreads();
+        if (*flag) {
+            // the row's maximum over the tile takes the reference's place where it is higher
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < P::MR; ++r) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < P::CBW; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (whole || nw + 16 * j + 4 * h + e < a.p.N) top = fmaxf(top, acc[r][j][e] * a.inv_tau);
+                top = quarter_max(top);
+                if (h == 0) red[w * P::BM + 16 * r + c] = top;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < P::MR; ++r) {
+                float top = -INFINITY;
+                for (int i = 0; i < P::W; ++i) top = fmaxf(top, red[i * P::BM + 16 * r + c]);
+                if (top > ref[r] + kHeadroom - 8.f) ref[r] = top;
+            }
+            __syncthreads();
+            emit(ref);
+            if (tid == 0 && a.hot) __hip_atomic_store(a.hot, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+        }
+        // (reference, sum): lane c of wave 0 holds the references of rows 16 r + c
+        if (w == 0) {
+#pragma unroll
+            for (int r = 0; r < P::MR; ++r) {
+                const int m = m0 + 16 * r + c;
+                if (h != 0 || m >= M) continue;
+                float sum = red[16 * r + c];
+                for (int i = 1; i < P::W; ++i) sum += red[i * P::BM + 16 * r + c];
+                a.part[(size_t)n_tile * M + m] = make_float2(ref[r], sum);
+            }
+        }
+    } else {
+        __syncthreads();
+    }
+    if constexpr (!kOut) return;
     for (int i = tid; i < P::BM * kChunks; i += P::kThreads) {
         const int row = i / kChunks, ch = i % kChunks;
         const int m = m0 + row, n = n0 + 8 * ch;
@@ -172,47 +159,114 @@ __global__ __launch_bounds__(P::kThreads) void loss_kernel(const LossArgs a) {
     if (a.p.splits > 1 && !reduce_splits<P::MR, P::CBW, P::W>(acc, a.p.counters, a.p.partials,
                                                               m_tile * a.p.tiles_n + n_tile, split, a.p.splits))
         return;
-    if constexpr (kProb) prob_epilogue<P>(a, sh, m_tile * P::BM, n_tile, acc);
-    else stats_epilogue<P>(a, sh, m_tile * P::BM, n_tile, acc);
+    loss_epilogue<P, P::kBF16 || !kProb, kProb>(a, sh, m_tile * P::BM, n_tile, acc);
 }
 
-// A teacher's list -> target weights, one wave a row: p = softmax of t / tau over the
-// row's valid ids (0 where the id is none or t is -inf; all 0 if nothing is left). An id
-// that comes more than once keeps its first entry, with the sum of the weights, so that
-// later steps meet each column once; ent = sum p log p is of the entries as given.
+// One wave: x . W_id in fp32, (q - z) s exactly. Lane: row block lane / 4 (+ 16, ...), rows
+// 8 (lane % 4) + 32 i of it.
+template <bool kBF16>
+__device__ __forceinline__ float column_dot(const uint16_t* __restrict__ x, const uint8_t* __restrict__ packed, int K, int Np,
+                                            int UW, int sub, int id, int lane) {
+    const int KB = K / kRowsPerBlock;
+    const int h = lane & 3;
+    const uint8_t* codes = packed + (size_t)(id >> 4) * KB * kBlockBytes + 16 * (16 * h + (id & 15));
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(packed + (size_t)K * Np / 2) + (size_t)id * UW;
+    float total = 0.f;
+    for (int kb = lane >> 2; kb < KB; kb += 16) {
+        const uint4 q = *reinterpret_cast<const uint4*>(codes + (size_t)kb * kBlockBytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t md = meta[kb * sub + ((i * sub) >> 2)];
+            const uint4 xv = *reinterpret_cast<const uint4*>(x + (size_t)kb * kRowsPerBlock + 32 * i + 8 * h);
+            const uint32_t d = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+            const float z = (float)((md >> 16) & 0xFu);
+            float a = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t xp = e == 0 ? xv.x : e == 1 ? xv.y : e == 2 ? xv.z : xv.w;
+                a = fmaf(half_bits_to_f32<kBF16>(xp & 0xFFFFu), (float)((d >> (4 * e)) & 0xFu) - z, a);
+                a = fmaf(half_bits_to_f32<kBF16>(xp >> 16), (float)((d >> (4 * e + 16)) & 0xFu) - z, a);
+            }
+            total = fmaf(half_bits_to_f32<kBF16>(md & 0xFFFFu), a, total);
+        }
+    }
+    for (int s = 32; s > 0; s >>= 1) total += __shfl_xor(total, s);
+    return total;
+}
+
 constexpr int kMaxTargets = 256;
-__global__ __launch_bounds__(64) void targets_kernel(const int32_t* __restrict__ ids, const float* __restrict__ t, int M,
-                                                     int T, int N, float inv_tau, int32_t* __restrict__ out_ids,
-                                                     float* __restrict__ out_p, float* __restrict__ ent) {
-    __shared__ int sid[kMaxTargets];
+
+struct TargetArgs {
+    const uint16_t* x;
+    const uint8_t* packed;
+    const int32_t* ids;      // [M, T] as given
+    const float* top;        // [M, T] teacher logits, or NULL: one target of weight 1
+    int M, K, N, T, UW, sub;
+    float inv_tau;
+    int32_t* out_ids;        // [M, T] each column once, -1: none (distillation)
+    float* weight;           // [M, T]
+    float* ent;              // [M] sum p log p
+    float* zsel;             // [M, T]
+    float* ref;              // [M] the largest target logit, without a target column 0's
+    int* hot;
+};
+
+// Cross entropy: a wave a row.
+template <bool kBF16>
+__global__ __launch_bounds__(256) void label_kernel(const TargetArgs a) {
+    const int m = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63;
+    if (a.hot && blockIdx.x == 0 && threadIdx.x == 0) *a.hot = 0;
+    if (m >= a.M) return;
+    int id = a.ids[m];
+    if (id < 0 || id >= a.N) id = 0;
+    const float z = a.inv_tau * column_dot<kBF16>(a.x + (size_t)m * a.K, a.packed, a.K, (int)padded_cols(a.N), a.UW, a.sub, id, lane);
+    if (lane == 0) {
+        a.zsel[m] = z;
+        a.ref[m] = z;
+    }
+}
+
+// Distillation: a workgroup a row. The teacher's list -> target weights, p = softmax of
+// t / tau over the row's valid ids (0 where the id is none or t is -inf; all 0 if nothing is
+// left). An id that comes more than once keeps its first entry, with the sum of the weights,
+// so that later steps meet each column once; ent = sum p log p is of the entries as given.
+template <bool kBF16>
+__global__ __launch_bounds__(256) void targets_kernel(const TargetArgs a) {
+    __shared__ int sid[kMaxTargets], first_id[kMaxTargets];
     __shared__ float sp[kMaxTargets];
-    const int m = (int)blockIdx.x, lane = (int)threadIdx.x;
-    float top = -INFINITY;
-    for (int j = lane; j < T; j += 64) {
-        const int id = ids[(size_t)m * T + j];
-        const bool ok = id >= 0 && id < N;
-        const float v = ok ? t[(size_t)m * T + j] * inv_tau : -INFINITY;
-        sid[j] = ok ? id : -1;
-        sp[j] = v;
-        top = fmaxf(top, v);
+    __shared__ float wave_top[4];
+    const int m = (int)blockIdx.x, tid = (int)threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int T = a.T;
+    if (a.hot && m == 0 && tid == 0) *a.hot = 0;
+    if (w == 0) {
+        float top = -INFINITY;
+        for (int j = lane; j < T; j += 64) {
+            const int id = a.ids[(size_t)m * T + j];
+            const bool ok = id >= 0 && id < a.N;
+            const float v = ok ? a.top[(size_t)m * T + j] * a.inv_tau : -INFINITY;
+            sid[j] = ok ? id : -1;
+            sp[j] = v;
+            top = fmaxf(top, v);
+        }
+        for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+        const float ref = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        for (int j = lane; j < T; j += 64) {
+            sp[j] = __expf(sp[j] - ref);
+            sum += sp[j];
+        }
+        for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        float en = 0.f;
+        for (int j = lane; j < T; j += 64) {
+            sp[j] *= inv;
+            if (sp[j] > 0.f) en += sp[j] * logf(sp[j]);
+        }
+        for (int s = 32; s > 0; s >>= 1) en += __shfl_xor(en, s);
+        if (lane == 0) a.ent[m] = en;
     }
-    for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    for (int j = lane; j < T; j += 64) {
-        sp[j] = __expf(sp[j] - ref);
-        sum += sp[j];
-    }
-    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    float en = 0.f;
-    for (int j = lane; j < T; j += 64) {
-        sp[j] *= inv;
-        if (sp[j] > 0.f) en += sp[j] * logf(sp[j]);
-    }
-    for (int s = 32; s > 0; s >>= 1) en += __shfl_xor(en, s);
     __syncthreads();
-    for (int j = lane; j < T; j += 64) {
+    for (int j = tid; j < T; j += 256) {
         const int id = sid[j];
         float p = sp[j];
         bool first = id >= 0;
@@ -221,46 +275,104 @@ __global__ __launch_bounds__(64) void targets_kernel(const int32_t* __restrict__
             if (i < j) first = false;
             p += sp[i];
         }
-        out_ids[(size_t)m * T + j] = first ? id : -1;
-        out_p[(size_t)m * T + j] = first ? p : 0.f;
+        first_id[j] = first ? id : -1;
+        a.out_ids[(size_t)m * T + j] = first ? id : -1;
+        a.weight[(size_t)m * T + j] = first ? p : 0.f;
     }
-    if (lane == 0) ent[m] = en;
+    __syncthreads();
+    const uint16_t* x = a.x + (size_t)m * a.K;
+    float top = -INFINITY;
+    for (int j = w; j < T; j += 4) {
+        const int id = first_id[j];
+        if (id < 0) continue;
+        const float z = a.inv_tau * column_dot<kBF16>(x, a.packed, a.K, (int)padded_cols(a.N), a.UW, a.sub, id, lane);
+        if (lane == 0) a.zsel[(size_t)m * T + j] = z;
+        top = fmaxf(top, z);
+    }
+    if (lane == 0) wave_top[w] = top;
+    __syncthreads();
+    if (w == 0) {
+        top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+        if (top == -INFINITY)
+            top = a.inv_tau * column_dot<kBF16>(x, a.packed, a.K, (int)padded_cols(a.N), a.UW, a.sub, 0, lane);
+        if (lane == 0) a.ref[m] = top;
+    }
+}
+
+// Between a piece's two products: the targets' places in P become zero, and where a tile
+// took a reference of its own the rows' tiles are given the factors that bring them, and
+// the sums of the pieces before, to the row's highest reference.
+__global__ __launch_bounds__(256) void settle_kernel(const int32_t* __restrict__ ids, int M, int T, int N, int n0, int n,
+                                                     uint16_t* __restrict__ q, int ldq, const int* __restrict__ hot,
+                                                     const float2* __restrict__ part, int tiles, float* __restrict__ ref,
+                                                     float* __restrict__ factor, float* __restrict__ before) {
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at < (int64_t)M * T) {
+        const int id = ids[at];
+        if (id >= n0 && id < n0 + n && id < N) q[(at / T) * (int64_t)ldq + (id - n0)] = 0;
+    }
+    if (!hot || *hot == 0 || at >= M) return;
+    const int m = (int)at;
+    const float old = ref[m];
+    float top = old;
+    for (int t = 0; t < tiles; ++t) top = fmaxf(top, part[(size_t)t * M + m].x);
+    for (int t = 0; t < tiles; ++t) factor[(size_t)t * M + m] = __expf(part[(size_t)t * M + m].x - top);
+    before[m] = __expf(old - top);
+    ref[m] = top;
 }
 
 // Rows: 16 rows a workgroup, 16 threads a row; the tiles' statistics and the targets'
 // terms are added in an order that depends on the shape alone.
-__global__ __launch_bounds__(256) void rows_kernel(const float2* __restrict__ part, int tiles, int M, int N, int T,
-                                                   const int32_t* __restrict__ ids, const float* __restrict__ weight,
-                                                   const float* __restrict__ ent, const float* __restrict__ zsel, float tau,
-                                                   const float* __restrict__ dloss, float* __restrict__ loss,
-                                                   float* __restrict__ lse_out, float* __restrict__ coef) {
+struct RowArgs {
+    const float2* part;
+    int tiles, M, N, T;
+    const int32_t* ids;
+    const float* weight;
+    const float* ent;
+    const float* zsel;
+    float tau;
+    const float* dloss;
+    float* loss;
+    float* lse;
+    float* coef;             // [M] dloss tau, 0 for a row without a target, or NULL
+    float* gain;             // [M] the factor of P W^T in dx
+    const float* ref;        // [M] P's reference (bf16) ...
+    float* next_ref;         // ... or that of the P to come (fp16)
+};
+__global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
     __shared__ float2 sv[16][17];
     const int i = (int)threadIdx.x & 15, g = (int)threadIdx.x >> 4;
     const int m = (int)blockIdx.x * 16 + i;
+    const int M = a.M;
     const int mc = m < M ? m : M - 1;
-    float2 v = make_float2(-INFINITY, 0.f);
-    for (int t = g; t < tiles; t += 16) {
-        const float2 o = part[(size_t)t * M + mc];
+    auto join = [](float2 v, float2 o) {
         const float top = fmaxf(v.x, o.x);
-        if (top != -INFINITY) v = make_float2(top, v.y * __expf(v.x - top) + o.y * __expf(o.x - top));
+        return top == -INFINITY ? v : make_float2(top, v.y * __expf(v.x - top) + o.y * __expf(o.x - top));
+    };
+    float2 v = make_float2(-INFINITY, 0.f);
+    for (int t0 = g; t0 < a.tiles; t0 += 128) {           // 8 loads in flight
+        float2 o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int t = t0 + 16 * k;
+            o[k] = t < a.tiles ? a.part[(size_t)t * M + mc] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v = join(v, o[k]);
     }
     sv[g][i] = v;
     __syncthreads();
     v = sv[0][i];
-    for (int k = 1; k < 16; ++k) {
-        const float2 o = sv[k][i];
-        const float top = fmaxf(v.x, o.x);
-        if (top != -INFINITY) v = make_float2(top, v.y * __expf(v.x - top) + o.y * __expf(o.x - top));
-    }
+    for (int k = 1; k < 16; ++k) v = join(v, sv[k][i]);
     const float lse = v.x + logf(v.y);
     __syncthreads();
     float sum = 0.f, mass = 0.f;
-    for (int j = g; j < T; j += 16) {
-        const int id = ids[(size_t)mc * T + j];
-        if (id < 0 || id >= N) continue;
-        const float p = weight ? weight[(size_t)mc * T + j] : 1.f;
+    for (int j = g; j < a.T; j += 16) {
+        const int id = a.ids[(size_t)mc * a.T + j];
+        if (id < 0 || id >= a.N) continue;
+        const float p = a.weight ? a.weight[(size_t)mc * a.T + j] : 1.f;
         if (p == 0.f) continue;
-        sum += p * (lse - zsel[(size_t)mc * T + j]);
+        sum += p * (lse - a.zsel[(size_t)mc * a.T + j]);
         mass += p;
     }
     sv[g][i] = make_float2(sum, mass);
@@ -273,11 +385,78 @@ __global__ __launch_bounds__(256) void rows_kernel(const float2* __restrict__ pa
             mass += sv[k][i].y;
         }
         const bool live = mass != 0.f;
-        if (ent) sum += ent[m];
-        loss[m] = live ? tau * tau * sum : 0.f;
-        lse_out[m] = lse;
-        if (coef) coef[m] = live ? tau * (dloss ? dloss[m] : 1.f) : 0.f;
+        if (a.ent) sum += a.ent[m];
+        a.loss[m] = live ? a.tau * a.tau * sum : 0.f;
+        a.lse[m] = lse;
+        if (a.coef) {
+            const float cf = live ? a.tau * (a.dloss ? a.dloss[m] : 1.f) : 0.f;
+            a.coef[m] = cf;
+            a.gain[m] = a.next_ref ? cf * (1.f / (1 << kShiftBits)) : cf * __expf(a.ref[m] - lse);
+            if (a.next_ref) a.next_ref[m] = lse - kShiftBits * 0.6931471806f;
+        }
     }
+}
+
+// dx[m] = gain[m] sum_s part[s][m] + sum_j coef[m] (q_j - p_j) W[:, id_j], one rounding. A
+// workgroup takes 2048 elements of a row, 8 a thread: one code word per target.
+struct FinishArgs {
+    const float* part;
+    int splits, M, K, N, T, UW, sub;
+    const uint8_t* packed;
+    const float *coef, *gain, *lse, *zsel, *weight;
+    const int32_t* ids;
+    uint16_t* dx;
+};
+template <bool kBF16>
+__global__ __launch_bounds__(256) void finish_kernel(const FinishArgs a) {
+    __shared__ int sid[kMaxTargets];
+    __shared__ float sc[kMaxTargets];
+    const int m = (int)blockIdx.x, tid = (int)threadIdx.x;
+    const int k0 = 8 * ((int)blockIdx.y * 256 + tid);
+    const float coef = a.coef[m], gain = a.gain[m];
+    for (int j = tid; j < a.T; j += 256) {
+        const int id = a.ids[(size_t)m * a.T + j];
+        const bool ok = id >= 0 && id < a.N;
+        sid[j] = ok ? id : 0;
+        sc[j] = ok ? coef * (__expf(a.zsel[(size_t)m * a.T + j] - a.lse[m]) - (a.weight ? a.weight[(size_t)m * a.T + j] : 1.f))
+                   : 0.f;
+    }
+    __syncthreads();
+    if (k0 >= a.K) return;
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    if (coef != 0.f) {
+        f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+        const size_t MK = (size_t)a.M * a.K;
+        const float* p = a.part + (size_t)m * a.K + k0;
+        for (int s = 0; s < a.splits; ++s, p += MK) {
+            s0 += *reinterpret_cast<const f32x4*>(p);
+            s1 += *reinterpret_cast<const f32x4*>(p + 4);
+        }
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = s0[e] * gain;
+            v[e + 4] = s1[e] * gain;
+        }
+        const int KB = a.K / kRowsPerBlock, kb = k0 / kRowsPerBlock, i = (k0 >> 5) & 3, h = (k0 >> 3) & 3;
+        const uint8_t* codes = a.packed + (size_t)kb * kBlockBytes + 256 * h + 4 * i;
+        const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.packed + (size_t)a.K * padded_cols(a.N) / 2) + kb * a.sub +
+                               ((i * a.sub) >> 2);
+#pragma unroll 4
+        for (int j = 0; j < a.T; ++j) {
+            const int id = sid[j];
+            const float cf = sc[j];
+            const uint32_t d = *reinterpret_cast<const uint32_t*>(codes + (size_t)(id >> 4) * KB * kBlockBytes + 16 * (id & 15));
+            const uint32_t md = meta[(size_t)id * a.UW];
+            const float s = cf * half_bits_to_f32<kBF16>(md & 0xFFFFu);
+            const float z = (float)((md >> 16) & 0xFu);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[tile_row_of_slot(e)] = fmaf((float)((d >> (4 * e)) & 0xFu) - z, s, v[tile_row_of_slot(e)]);
+        }
+        o = make_uint4(pack2_rne<kBF16>(v[0], v[1]), pack2_rne<kBF16>(v[2], v[3]), pack2_rne<kBF16>(v[4], v[5]),
+                       pack2_rne<kBF16>(v[6], v[7]));
+    }
+    *reinterpret_cast<uint4*>(a.dx + (size_t)m * a.K + k0) = o;
 }
 
 template <bool kBF16, int MR, int CBW, int kSub, bool kProb>
@@ -316,15 +495,18 @@ struct LossLayout {
     ProductPlan stats, prob;
     GradPlan grad;
     int64_t piece, pieces;
-    size_t partials, part, zsel, ids, weight, ent, coef, lse, q, gpart, end;
+    size_t partials, part, zsel, ids, weight, ent, coef, gain, ref, hot, factor, before, q, gpart, end;
 };
 
-LossLayout loss_layout(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bool distill, bool grad) {
+int64_t tile_columns(const ProductPlan& p) { return 128 * p.cbw; }
+
+LossLayout loss_layout(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bool bf16, bool distill, bool grad) {
     LossLayout l{};
     l.stats = plan_product(M, K, V, G, false);
     size_t partial = l.stats.partial_bytes;
+    int64_t tiles = l.stats.tiles_n;
     if (grad) {
-        // pieces of the vocabulary: q of a piece takes at most 256 MiB (it then stays in
+        // pieces of the vocabulary: P of a piece takes at most 256 MiB (it then stays in
         // the last-level cache between the two products)
         int64_t most = kPieceBytes / (2 * M) / 512 * 512;
         if (most < 512) most = 512;
@@ -336,6 +518,7 @@ LossLayout loss_layout(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bo
         const ProductPlan tail = plan_product(M, K, last, G, false);
         if (l.prob.partial_bytes > partial) partial = l.prob.partial_bytes;
         if (tail.partial_bytes > partial) partial = tail.partial_bytes;
+        if (bf16) tiles = (l.pieces - 1) * l.prob.tiles_n + tail.tiles_n;
         l.grad = plan_grad(M, K, l.pieces > 1 ? l.piece : last, true);
     }
     size_t at = kSplitCounterBytes;
@@ -345,12 +528,17 @@ LossLayout loss_layout(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bo
         return here;
     };
     l.partials = take(partial);
-    l.part = take((size_t)l.stats.tiles_n * M * 8);
+    l.part = take((size_t)tiles * M * 8);
     l.zsel = take((size_t)M * T * 4);
     l.ids = take(distill ? (size_t)M * T * 4 : 0);
     l.weight = take(distill ? (size_t)M * T * 4 : 0);
     l.ent = take(distill ? (size_t)M * 4 : 0);
     l.coef = take((size_t)M * 4);
+    l.gain = take((size_t)M * 4);
+    l.ref = take((size_t)M * 4);
+    l.hot = take(4);
+    l.factor = take(grad && bf16 ? (size_t)l.prob.tiles_n * M * 4 : 0);
+    l.before = take(grad && bf16 ? (size_t)M * 4 : 0);
     l.q = take(grad ? (size_t)M * l.piece * 2 : 0);
     l.gpart = take(grad ? l.grad.part_bytes : 0);
     l.end = at;
@@ -363,10 +551,14 @@ int max_loss_targets() { return kMaxTargets; }
 
 size_t loss_workspace(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bool distill, bool grad) {
     const int64_t full = M < kRowsPerPass ? M : kRowsPerPass;
-    size_t need = loss_layout(full, K, V, G, T, distill, grad).end;
-    if (M > full && M % full) {
-        const size_t tail = loss_layout(M % full, K, V, G, T, distill, grad).end;
-        if (tail > need) need = tail;
+    size_t need = 0;
+    for (const bool bf16 : {false, true}) {       // one size for both types
+        size_t n = loss_layout(full, K, V, G, T, bf16, distill, grad).end;
+        if (n > need) need = n;
+        if (M > full && M % full) {
+            n = loss_layout(M % full, K, V, G, T, bf16, distill, grad).end;
+            if (n > need) need = n;
+        }
     }
     return need;
 }
@@ -375,66 +567,110 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
     uint8_t* ws = static_cast<uint8_t*>(q.workspace);
     const bool distill = q.top != nullptr;
     const bool grad = q.dx != nullptr;
+    const bool sums_first = !grad || !q.bf16;
     for (int64_t r0 = 0; r0 < q.M; r0 += kRowsPerPass) {
         const int64_t M = q.M - r0 < kRowsPerPass ? q.M - r0 : kRowsPerPass;
-        const LossLayout l = loss_layout(M, q.K, q.V, q.G, q.T, distill, grad);
+        const LossLayout l = loss_layout(M, q.K, q.V, q.G, q.T, q.bf16, distill, grad);
+        auto floats = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+        float2* part = reinterpret_cast<float2*>(ws + l.part);
+        int* hot = grad && q.bf16 ? reinterpret_cast<int*>(ws + l.hot) : nullptr;
+        float* ref = floats(l.ref);
+        const int32_t* ids = q.ids + r0 * q.T;
+
+        TargetArgs t{};
+        t.x = q.x + r0 * q.K;
+        t.packed = q.packed;
+        t.ids = ids;
+        t.M = (int)M;
+        t.K = (int)q.K;
+        t.N = (int)q.V;
+        t.T = (int)q.T;
+        t.UW = (int)padded_units(q.K, q.G);
+        t.sub = units_per_block(q.G);
+        t.inv_tau = 1.f / q.tau;
+        t.zsel = floats(l.zsel);
+        t.ref = ref;
+        t.hot = hot;
+        if (distill) {
+            t.top = q.top + r0 * q.T;
+            t.out_ids = reinterpret_cast<int32_t*>(ws + l.ids);
+            t.weight = floats(l.weight);
+            t.ent = floats(l.ent);
+            if (q.bf16) hipLaunchKernelGGL((targets_kernel<true>), dim3((unsigned)M), dim3(256), 0, stream, t);
+            else hipLaunchKernelGGL((targets_kernel<false>), dim3((unsigned)M), dim3(256), 0, stream, t);
+            ids = t.out_ids;
+        } else {
+            const dim3 grid((unsigned)((M + 3) / 4));
+            if (q.bf16) hipLaunchKernelGGL((label_kernel<true>), grid, dim3(256), 0, stream, t);
+            else hipLaunchKernelGGL((label_kernel<false>), grid, dim3(256), 0, stream, t);
+        }
+
         LossArgs a{};
-        a.p.x = q.x + r0 * q.K;
+        a.p.x = t.x;
         a.p.packed = q.packed;
         a.p.M = (int)M;
         a.p.K = (int)q.K;
         a.p.N = (int)q.V;
-        a.p.n_begin = 0;
-        a.p.n_end = (int)q.V;
         a.p.counters = static_cast<uint32_t*>(q.workspace);
-        a.p.partials = reinterpret_cast<float*>(ws + l.partials);
-        a.inv_tau = 1.f / q.tau;
-        a.T = (int)q.T;
-        a.zsel = reinterpret_cast<float*>(ws + l.zsel);
-        a.part = reinterpret_cast<float2*>(ws + l.part);
-        float* coef = reinterpret_cast<float*>(ws + l.coef);
-        const float* ent = nullptr;
-        if (distill) {
-            int32_t* ids = reinterpret_cast<int32_t*>(ws + l.ids);
-            float* weight = reinterpret_cast<float*>(ws + l.weight);
-            float* e = reinterpret_cast<float*>(ws + l.ent);
-            hipLaunchKernelGGL(targets_kernel, dim3((unsigned)M), dim3(64), 0, stream, q.ids + r0 * q.T, q.top + r0 * q.T,
-                               (int)M, (int)q.T, (int)q.V, a.inv_tau, ids, weight, e);
-            a.ids = ids;
-            a.weight = weight;
-            ent = e;
-        } else {
-            a.ids = q.ids + r0 * q.T;
-        }
-        a.p.tiles_m = l.stats.tiles_m;
-        a.p.tiles_n = l.stats.tiles_n;
-        a.p.splits = l.stats.splits;
-        launch_any(l.stats, a, q.bf16, false, stream);
-        float* lse = q.lse + r0;
-        hipLaunchKernelGGL(rows_kernel, dim3((unsigned)((M + 15) / 16)), dim3(256), 0, stream, a.part, l.stats.tiles_n, (int)M,
-                           (int)q.V, (int)q.T, a.ids, a.weight, ent, a.zsel, q.tau, q.dloss ? q.dloss + r0 : nullptr,
-                           q.loss + r0, lse, grad ? coef : nullptr);
-        hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
-        if (!grad) continue;
-        a.lse = lse;
-        a.coef = coef;
-        a.q = reinterpret_cast<uint16_t*>(ws + l.q);
-        a.ldq = (int)l.piece;
-        for (int64_t n0 = 0; n0 < q.V; n0 += l.piece) {
-            const int64_t n = q.V - n0 < l.piece ? q.V - n0 : l.piece;
-            const ProductPlan p = n == l.piece ? l.prob : plan_product(M, q.K, n, q.G, false);
+        a.p.partials = floats(l.partials);
+        a.inv_tau = t.inv_tau;
+        a.ref = ref;
+        a.hot = hot;
+        auto product = [&](const ProductPlan& p, int64_t n0, int64_t n, bool prob) {
             a.p.n_begin = (int)n0;
             a.p.n_end = (int)(n0 + n);
             a.p.tiles_m = p.tiles_m;
             a.p.tiles_n = p.tiles_n;
             a.p.splits = p.splits;
-            launch_any(p, a, q.bf16, true, stream);
+            launch_any(p, a, q.bf16, prob, stream);
+        };
+        RowArgs rows{};
+        rows.part = part;
+        rows.M = (int)M;
+        rows.N = (int)q.V;
+        rows.T = (int)q.T;
+        rows.ids = ids;
+        rows.weight = t.weight;
+        rows.ent = t.ent;
+        rows.zsel = t.zsel;
+        rows.tau = q.tau;
+        rows.dloss = q.dloss ? q.dloss + r0 : nullptr;
+        rows.loss = q.loss + r0;
+        rows.lse = q.lse + r0;
+        if (grad) {
+            rows.coef = floats(l.coef);
+            rows.gain = floats(l.gain);
+            rows.ref = ref;
+            if (!q.bf16) rows.next_ref = ref;
+        }
+        const dim3 rows_grid((unsigned)((M + 15) / 16));
+        if (sums_first) {
+            a.part = part;
+            product(l.stats, 0, q.V, false);
+            rows.tiles = l.stats.tiles_n;
+            hipLaunchKernelGGL(rows_kernel, rows_grid, dim3(256), 0, stream, rows);
+        }
+        hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        if (!grad) continue;
+
+        a.q = reinterpret_cast<uint16_t*>(ws + l.q);
+        a.ldq = (int)l.piece;
+        int tiles = 0;
+        for (int64_t n0 = 0; n0 < q.V; n0 += l.piece) {
+            const int64_t n = q.V - n0 < l.piece ? q.V - n0 : l.piece;
+            const ProductPlan p = n == l.piece ? l.prob : plan_product(M, q.K, n, q.G, false);
+            a.part = part + (size_t)tiles * M;
+            product(p, n0, n, true);
+            hipLaunchKernelGGL(settle_kernel, dim3((unsigned)((M * q.T + 255) / 256)), dim3(256), 0, stream, ids, (int)M, (int)q.T,
+                               (int)q.V, (int)n0, (int)n, a.q, a.ldq, hot, a.part, p.tiles_n, ref, floats(l.factor),
+                               floats(l.before));
+            tiles += p.tiles_n;
             GradCall g{};
             g.d = a.q;
             g.ld = l.piece;
             g.packed = q.packed;
-            g.part = reinterpret_cast<float*>(ws + l.gpart);
+            g.part = floats(l.gpart);
             g.add = n0 > 0;
             g.M = M;
             g.K = q.K;
@@ -442,13 +678,39 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
             g.G = q.G;
             g.n0 = n0;
             g.n = n;
-            g.op_bf16 = true;
-            g.scale_bf16 = q.bf16;
+            g.op_bf16 = g.scale_bf16 = q.bf16;
+            g.hot = hot;
+            g.factor = floats(l.factor);
+            g.before = floats(l.before);
+            g.factor_columns = (int)tile_columns(p);
             err = launch_grad(l.grad, g, stream);
             if (err != hipSuccess) return err;
         }
-        err = launch_grad_finish(reinterpret_cast<const float*>(ws + l.gpart), l.grad.splits, M, q.K, coef, q.dx + r0 * q.K,
-                                 q.bf16, stream);
+        if (!sums_first) {
+            rows.tiles = tiles;
+            hipLaunchKernelGGL(rows_kernel, rows_grid, dim3(256), 0, stream, rows);
+        }
+        FinishArgs f{};
+        f.part = floats(l.gpart);
+        f.splits = l.grad.splits;
+        f.M = (int)M;
+        f.K = (int)q.K;
+        f.N = (int)q.V;
+        f.T = (int)q.T;
+        f.UW = t.UW;
+        f.sub = t.sub;
+        f.packed = q.packed;
+        f.coef = rows.coef;
+        f.gain = rows.gain;
+        f.lse = rows.lse;
+        f.zsel = t.zsel;
+        f.weight = t.weight;
+        f.ids = ids;
+        f.dx = q.dx + r0 * q.K;
+        const dim3 finish_grid((unsigned)M, (unsigned)((q.K + 2047) / 2048));
+        if (q.bf16) hipLaunchKernelGGL((finish_kernel<true>), finish_grid, dim3(256), 0, stream, f);
+        else hipLaunchKernelGGL((finish_kernel<false>), finish_grid, dim3(256), 0, stream, f);
+        err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
     return hipSuccess;
