@@ -43,6 +43,7 @@ library's error, raised here as W4A16Error.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -562,13 +563,30 @@ def _result(t, name, shape, dtype, device):
     return t
 
 
-def _space(workspace, need, device, stream):
+def _raw_stream(stream, device):
+    """The hipStream_t of `stream`, or of the device's current stream, as an integer."""
+    if stream is None:
+        if device.type == "cuda":
+            return torch._C._cuda_getCurrentRawStream(device.index)
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream
+
+
+def _space(workspace, need, device, stream, raw):
     """(pointer, bytes) of the caller's workspace, or of the (device, stream)'s own."""
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = _default_workspace(device, need, stream)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        workspace = _workspaces.get((device.index, raw))
+        if workspace is None or workspace.numel() < need:
+            workspace = _default_workspace(device, need, stream)
+    return workspace.data_ptr(), workspace.nbytes
+
+
+@functools.lru_cache(maxsize=4096)
+def _need(name, *shape):
+    """A workspace_bytes function's answer: it depends on the shape alone."""
+    return getattr(_load(), name)(*shape)
 
 
 def w4a16_gemm_grad(dy, packed, K, group_size=128, dx=None, workspace=None, stream=None):
@@ -577,10 +595,11 @@ def w4a16_gemm_grad(dy, packed, K, group_size=128, dx=None, workspace=None, stre
     M, N = _rows(dy, "dy")
     h = _load()
     dx = _result(dx, "dx", (M, K), dy.dtype, dy.device)
-    ws, ws_bytes = _space(workspace, h.w4a16_gemm_grad_workspace_bytes(M, K, N, group_size), dy.device, stream)
-    _check(h.w4a16_gemm_grad(dy.data_ptr(), packed.data_ptr(), packed.numel() * packed.element_size(),
+    raw = _raw_stream(stream, dy.device)
+    ws, ws_bytes = _space(workspace, _need("w4a16_gemm_grad_workspace_bytes", M, K, N, group_size), dy.device, stream, raw)
+    _check(h.w4a16_gemm_grad(dy.data_ptr(), packed.data_ptr(), packed.nbytes,
                              _dtype_code(dy.dtype), dx.data_ptr(), M, K, N, group_size, ws, ws_bytes,
-                             _stream(stream, dy.device)), "w4a16_gemm_grad")
+                             raw), "w4a16_gemm_grad")
     return dx
 
 
@@ -596,10 +615,11 @@ def w4a16_gated(x, packed, F, group_size=128, act="silu", h=None, workspace=None
     M, K = _rows(x, "x")
     lib = _load()
     h = _result(h, "h", (M, F), x.dtype, x.device)
-    ws, ws_bytes = _space(workspace, lib.w4a16_gated_workspace_bytes(M, K, F, group_size, 0), x.device, stream)
-    _check(lib.w4a16_gated(x.data_ptr(), packed.data_ptr(), packed.numel() * packed.element_size(),
+    raw = _raw_stream(stream, x.device)
+    ws, ws_bytes = _space(workspace, _need("w4a16_gated_workspace_bytes", M, K, F, group_size, 0), x.device, stream, raw)
+    _check(lib.w4a16_gated(x.data_ptr(), packed.data_ptr(), packed.nbytes,
                            _dtype_code(x.dtype), h.data_ptr(), M, K, F, group_size, _act_code(act), ws, ws_bytes,
-                           _stream(stream, x.device)), "w4a16_gated")
+                           raw), "w4a16_gated")
     return h
 
 
@@ -611,10 +631,11 @@ def w4a16_gated_grad(x, dh, packed, F, group_size=128, act="silu", dx=None, work
         raise ValueError("dh must be a contiguous [M, F] tensor of x's dtype")
     lib = _load()
     dx = _result(dx, "dx", (M, K), x.dtype, x.device)
-    ws, ws_bytes = _space(workspace, lib.w4a16_gated_workspace_bytes(M, K, F, group_size, 1), x.device, stream)
-    _check(lib.w4a16_gated_grad(x.data_ptr(), dh.data_ptr(), packed.data_ptr(), packed.numel() * packed.element_size(),
+    raw = _raw_stream(stream, x.device)
+    ws, ws_bytes = _space(workspace, _need("w4a16_gated_workspace_bytes", M, K, F, group_size, 1), x.device, stream, raw)
+    _check(lib.w4a16_gated_grad(x.data_ptr(), dh.data_ptr(), packed.data_ptr(), packed.nbytes,
                                 _dtype_code(x.dtype), dx.data_ptr(), M, K, F, group_size, _act_code(act), ws, ws_bytes,
-                                _stream(stream, x.device)), "w4a16_gated_grad")
+                                raw), "w4a16_gated_grad")
     return dx
 
 
@@ -641,12 +662,13 @@ def w4a16_cross_entropy(x, labels, packed, V, group_size=128, dloss=None, grad=F
     if tuple(labels.shape) != (M,) or labels.dtype != torch.int32 or not labels.is_contiguous():
         raise ValueError("labels must be a contiguous int32 [M] tensor")
     h = _load()
-    ws, ws_bytes = _space(workspace, h.w4a16_cross_entropy_workspace_bytes(M, K, V, group_size, 1 if grad else 0),
-                          x.device, stream)
+    raw = _raw_stream(stream, x.device)
+    ws, ws_bytes = _space(workspace, _need("w4a16_cross_entropy_workspace_bytes", M, K, V, group_size, 1 if grad else 0),
+                          x.device, stream, raw)
     _check(h.w4a16_cross_entropy(x.data_ptr(), labels.data_ptr(), packed.data_ptr(),
-                                 packed.numel() * packed.element_size(), _dtype_code(x.dtype), M, K, V, group_size,
+                                 packed.nbytes, _dtype_code(x.dtype), M, K, V, group_size,
                                  None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(),
-                                 dx.data_ptr() if grad else None, ws, ws_bytes, _stream(stream, x.device)),
+                                 dx.data_ptr() if grad else None, ws, ws_bytes, raw),
            "w4a16_cross_entropy")
     return (loss, lse, dx) if grad else (loss, lse)
 
@@ -664,12 +686,13 @@ def w4a16_distill(x, top_ids, top_logits, packed, V, group_size=128, temperature
     if _rows(top_logits, "top_logits") != (M, T) or top_logits.dtype != torch.float32:
         raise ValueError("top_logits must be a float32 [M, T] tensor")
     h = _load()
-    ws, ws_bytes = _space(workspace, h.w4a16_distill_workspace_bytes(M, K, V, group_size, T, 1 if grad else 0),
-                          x.device, stream)
+    raw = _raw_stream(stream, x.device)
+    ws, ws_bytes = _space(workspace, _need("w4a16_distill_workspace_bytes", M, K, V, group_size, T, 1 if grad else 0),
+                          x.device, stream, raw)
     _check(h.w4a16_distill(x.data_ptr(), top_ids.data_ptr(), top_logits.data_ptr(), packed.data_ptr(),
-                           packed.numel() * packed.element_size(), _dtype_code(x.dtype), M, K, V, group_size, T,
+                           packed.nbytes, _dtype_code(x.dtype), M, K, V, group_size, T,
                            temperature, None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(),
-                           dx.data_ptr() if grad else None, ws, ws_bytes, _stream(stream, x.device)), "w4a16_distill")
+                           dx.data_ptr() if grad else None, ws, ws_bytes, raw), "w4a16_distill")
     return (loss, lse, dx) if grad else (loss, lse)
 
 

@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "libw4a16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.hip", "repack.hip", "gemv.hip", "gemv_strip.hip", "gemv_small.hip", "gemm.hip", "embedding.hip", "w4a8.hip", "measure.hip",
-           "api_train.hip", "gated.hip", "gemm_grad.hip", "loss.hip"]
+           "api_train.hip", "gated.hip", "product_small.hip", "gemm_grad.hip", "loss.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -11,6 +11,7 @@
 // workspace in bf16, whatever the dtype - their range is the gradients', which fp16 does
 // not hold without a scale chosen for them - and one product with W^T follows.
 #include "device_common.h"
+#include "gate.h"
 #include "launch.h"
 #include "tile_product.h"
 
@@ -18,26 +19,6 @@ namespace w4a16 {
 namespace {
 
 constexpr int kTargetWorkgroups = 256;      // one per compute unit
-
-// a(g) and a'(g) in fp32. kAct: 0 silu g/(1 + e^-g); 1 gelu g Phi(g); 2 gelu's tanh form,
-// 0.5 (1 + tanh y) = 1/(1 + e^-2y). The polynomial's argument is clamped at +-30, where
-// its logistic is 0 or 1 exactly, so that no infinity meets a zero.
-template <int kAct>
-__device__ __forceinline__ float gate_prob(float g, float* slope) {
-    if constexpr (kAct == 0) {
-        const float e = __builtin_amdgcn_rcpf(1.f + __expf(-g));
-        *slope = e * (1.f - e);
-        return e;
-    } else if constexpr (kAct == 1) {
-        *slope = 0.3989422804f * __expf(-0.5f * g * g);
-        return 0.5f * erfcf(-0.7071067812f * g);
-    } else {
-        const float y = fminf(fmaxf(g, -30.f), 30.f);
-        const float e = __builtin_amdgcn_rcpf(1.f + __expf(-1.5957691216f * y * (1.f + 0.044715f * y * y)));
-        *slope = e * (1.f - e) * 1.5957691216f * (1.f + 0.134145f * y * y);
-        return e;
-    }
-}
 
 struct GatedArgs {
     ProductArgs p;
@@ -161,6 +142,7 @@ void launch_typed(const ProductPlan& p, GatedArgs& a, hipStream_t s) {
 // K over workgroups, at least 4 row blocks each.
 ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gated) {
     ProductPlan p{};
+    if (gated && small_product(M, K)) return p;          // no tiles, no workspace
     p.sub = units_per_block(G);
     const int64_t KB = K / kRowsPerBlock;
     struct Shape { int mr, cbw; double rate; };
@@ -201,6 +183,7 @@ ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gat
 }
 
 hipError_t launch_gated(const GatedCall& q, hipStream_t stream) {
+    if (small_product(q.M, q.K)) return launch_gated_small(q, stream);
     const ProductPlan p = plan_product(q.M, q.K, 2 * q.F, q.G, true);
     GatedArgs a{};
     a.p.x = q.x;

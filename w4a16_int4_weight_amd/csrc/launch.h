@@ -135,6 +135,15 @@ struct GatedCall {
 };
 hipError_t launch_gated(const GatedCall& call, hipStream_t stream);
 
+// Up to 16 rows (csrc/product_small.hip): the gated block, and the head's statistics for
+// cross entropy: the labels' logits and (max, sum) per row and workgroup, part
+// [small_workgroups][M] pairs. No workspace besides.
+bool small_product(int64_t M, int64_t K);
+int small_workgroups(int64_t units);
+hipError_t launch_gated_small(const GatedCall& call, hipStream_t stream);
+hipError_t launch_ce_small(const uint16_t* x, const int32_t* labels, const uint8_t* packed, int64_t M, int64_t K, int64_t V,
+                           int64_t G, bool bf16, float* zsel, float* part, hipStream_t stream);
+
 // dx = coef . (D W^T): D [M, columns n0 .. n0 + n) of the weight, row stride ld, operands
 // bf16 (op_bf16) or fp16; out 16-bit of out_bf16. The sum over columns is split over
 // `splits` workgroups and may be cut into calls: with `part` set, partial tiles

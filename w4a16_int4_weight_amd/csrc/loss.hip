@@ -495,6 +495,7 @@ struct LossLayout {
     ProductPlan stats, prob;
     GradPlan grad;
     int64_t piece, pieces;
+    bool small;              // up to 16 rows without a gradient: one kernel before the rows'
     size_t partials, part, zsel, ids, weight, ent, coef, gain, ref, hot, factor, before, q, gpart, end;
 };
 
@@ -502,9 +503,10 @@ int64_t tile_columns(const ProductPlan& p) { return 128 * p.cbw; }
 
 LossLayout loss_layout(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bool bf16, bool distill, bool grad) {
     LossLayout l{};
-    l.stats = plan_product(M, K, V, G, false);
+    l.small = !distill && !grad && small_product(M, K);
+    if (!l.small) l.stats = plan_product(M, K, V, G, false);
     size_t partial = l.stats.partial_bytes;
-    int64_t tiles = l.stats.tiles_n;
+    int64_t tiles = l.small ? small_workgroups(padded_cols(V) / kColsPerBlock) : l.stats.tiles_n;
     if (grad) {
         // pieces of the vocabulary: P of a piece takes at most 256 MiB (it then stays in
         // the last-level cache between the two products)
@@ -599,7 +601,7 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
             if (q.bf16) hipLaunchKernelGGL((targets_kernel<true>), dim3((unsigned)M), dim3(256), 0, stream, t);
             else hipLaunchKernelGGL((targets_kernel<false>), dim3((unsigned)M), dim3(256), 0, stream, t);
             ids = t.out_ids;
-        } else {
+        } else if (!l.small) {
             const dim3 grid((unsigned)((M + 3) / 4));
             if (q.bf16) hipLaunchKernelGGL((label_kernel<true>), grid, dim3(256), 0, stream, t);
             else hipLaunchKernelGGL((label_kernel<false>), grid, dim3(256), 0, stream, t);
@@ -646,8 +648,14 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
         const dim3 rows_grid((unsigned)((M + 15) / 16));
         if (sums_first) {
             a.part = part;
-            product(l.stats, 0, q.V, false);
-            rows.tiles = l.stats.tiles_n;
+            if (l.small) {
+                const hipError_t e = launch_ce_small(t.x, ids, q.packed, M, q.K, q.V, q.G, q.bf16, t.zsel, floats(l.part), stream);
+                if (e != hipSuccess) return e;
+                rows.tiles = small_workgroups(padded_cols(q.V) / kColsPerBlock);
+            } else {
+                product(l.stats, 0, q.V, false);
+                rows.tiles = l.stats.tiles_n;
+            }
             hipLaunchKernelGGL(rows_kernel, rows_grid, dim3(256), 0, stream, rows);
         }
         hipError_t err = hipGetLastError();
