@@ -18,7 +18,7 @@ using w4a16::kMaxMK;
 using w4a16::packed_size;
 
 constexpr int64_t kMaxRowElements = int64_t(1) << 22;     // a 256-row tile is addressed in 32 bits
-constexpr int64_t kGatedRowsPerPass = 8192;
+constexpr int64_t kGatedRowsPerPass = 8192;            // of a backward: 8 F bytes a row
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -63,10 +63,10 @@ w4a16_status check_gated(int64_t M, int64_t K, int64_t F, int64_t group_size, in
 }
 
 struct GatedLayout {
-    size_t partials, d, gpart, end;
+    size_t partials, tops, rowmax, scale_max, d, gpart, end;
 };
 
-// one pass over M rows: the forward's K-split partials and, for the gradient, dg | du and
+// one pass over M rows: the forward's K-split partials and, for the gradient, dg | du in fp32 and
 // the transposed product's partials
 GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) {
     GatedLayout l{};
@@ -74,8 +74,14 @@ GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) 
     l.partials = w4a16::kSplitCounterBytes;
     size_t at = l.partials + round256(partial);
     if (grad) {
+        l.tops = at;
+        at += round256((size_t)w4a16::gated_tiles(M, K, F, G) * M * 4);
+        l.rowmax = at;
+        at += round256((size_t)M * 4);
+        l.scale_max = at;
+        at += round256(w4a16::kScaleParts * 4);
         l.d = at;
-        at += round256((size_t)M * 4 * F);
+        at += round256((size_t)M * 8 * F);
         l.gpart = at;
         at += round256(w4a16::plan_grad(M, K, 2 * F, false).part_bytes);
     } else if (partial == 0) {
@@ -187,11 +193,11 @@ w4a16_status w4a16_gemm_grad(const void* dy, const void* packed, size_t packed_b
     q.G = G;
     q.n0 = 0;
     q.n = N;
-    q.op_bf16 = q.scale_bf16 = bf16;
+    q.bf16 = bf16;
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err = w4a16::launch_grad(plan, q, s);
     if (err == hipSuccess && part)
-        err = w4a16::launch_grad_finish(part, plan.splits, M, K, static_cast<uint16_t*>(dx), bf16, s);
+        err = w4a16::launch_grad_finish(part, plan.splits, M, K, static_cast<uint16_t*>(dx), bf16, nullptr, nullptr, s);
     return from_hip(err);
 }
 
@@ -260,7 +266,10 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         q.x = static_cast<const uint16_t*>(x) + r0 * K;
         q.dh = static_cast<const uint16_t*>(dh) + r0 * F;
         q.packed = static_cast<const uint8_t*>(packed);
-        q.d = reinterpret_cast<uint16_t*>(ws + l.d);
+        q.d = reinterpret_cast<float*>(ws + l.d);
+        q.tops = reinterpret_cast<float*>(ws + l.tops);
+        float* rowmax = reinterpret_cast<float*>(ws + l.rowmax);
+        float* scale_max = reinterpret_cast<float*>(ws + l.scale_max);
         q.M = rows;
         q.K = K;
         q.F = F;
@@ -270,12 +279,17 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         q.counters = reinterpret_cast<uint32_t*>(ws);
         q.partials = reinterpret_cast<float*>(ws + l.partials);
         hipError_t err = w4a16::launch_gated(q, s);
+        if (err == hipSuccess)
+            err = w4a16::launch_gated_tops(q.tops, w4a16::gated_tiles(rows, K, F, G), q.packed, rows, K, 2 * F, G, bf16, rowmax,
+                                           scale_max, s);
         if (err != hipSuccess) return W4A16_ERR_HIP;
         const w4a16::GradPlan plan = w4a16::plan_grad(rows, K, 2 * F, false);
         float* part = plan.part_bytes ? reinterpret_cast<float*>(ws + l.gpart) : nullptr;
         uint16_t* out = static_cast<uint16_t*>(dx) + r0 * K;
         w4a16::GradCall g{};
-        g.d = q.d;
+        g.d32 = q.d;
+        g.rowmax = rowmax;
+        g.scale_max = scale_max;
         g.ld = 2 * F;
         g.packed = q.packed;
         g.dx = part ? nullptr : out;
@@ -285,10 +299,9 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         g.N = 2 * F;
         g.G = G;
         g.n = 2 * F;
-        g.op_bf16 = true;
-        g.scale_bf16 = bf16;
+        g.bf16 = bf16;
         err = w4a16::launch_grad(plan, g, s);
-        if (err == hipSuccess && part) err = w4a16::launch_grad_finish(part, plan.splits, rows, K, out, bf16, s);
+        if (err == hipSuccess && part) err = w4a16::launch_grad_finish(part, plan.splits, rows, K, out, bf16, rowmax, scale_max, s);
         if (err != hipSuccess) return W4A16_ERR_HIP;
     }
     return W4A16_OK;

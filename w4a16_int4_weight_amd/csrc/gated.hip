@@ -8,8 +8,9 @@
 // blocks and the HB matching up blocks, so g and u never leave its registers and the
 // block costs one product and one pass over x. The backward recomputes them (keeping
 // them would take 4 F bytes a token and round them to 16 bits), writes dg and du to the
-// workspace in bf16, whatever the dtype - their range is the gradients', which fp16 does
-// not hold without a scale chosen for them - and one product with W^T follows.
+// workspace in fp32 with their rows' largest values, and one product with W^T follows, which
+// takes them in fp16 scaled row by row (gemm_grad.hip): rounded to bf16 they would be off by
+// as much as the result's own rounding.
 #include "device_common.h"
 #include "gate.h"
 #include "launch.h"
@@ -24,17 +25,21 @@ struct GatedArgs {
     ProductArgs p;
     uint16_t* h;            // forward: [M, F]
     const uint16_t* dh;     // backward: [M, F]
-    uint16_t* d;            // backward: [M, 2F] bf16, dg then du
+    float* d;               // backward: [M, 2F], dg then du
+    float* tops;            // [column tiles][M] largest |d| of a row
     int act;
 };
 
+// The tile's results go through LDS and leave as whole rows. (Stored from the lanes, 64
+// bytes a row and instruction, a backward's two fp32 tiles took 12 us of a 47 us tile.)
 template <class P, bool kGrad, int kAct>
 __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::Shared& sh, int m0, int f0,
                                                f32x4 (&acc)[P::MR][P::CBW]) {
     constexpr int BM = P::BM, BN = P::BN, HB = P::HB;
-    constexpr int kRow = BN * 2 + 16;                        // bytes of a tile row, padded
-    constexpr int kChunks = BN / 8;
-    static_assert((kGrad ? 2 : 1) * BM * kRow <= (int)sizeof(typename P::Shared), "the output tiles fit in LDS");
+    constexpr int kSize = kGrad ? 4 : 2;                     // bytes of an output
+    constexpr int kRow = BN * kSize + 16;                    // bytes of a tile row, padded
+    constexpr int kChunks = BN * kSize / 16;
+    static_assert((kGrad ? 2 : 1) * BM * kRow + P::W * BM * 4 <= (int)sizeof(typename P::Shared), "the output tiles fit in LDS");
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lane = tid & 63;
@@ -42,25 +47,26 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::S
     const int M = a.p.M, F = a.p.F;
     uint8_t* t0 = reinterpret_cast<uint8_t*>(&sh);
     uint8_t* t1 = t0 + BM * kRow;
+    float* red = reinterpret_cast<float*>(t1 + BM * kRow);   // backward: [W][BM]
+    [[maybe_unused]] uint2 dv[P::MR][HB];
     if constexpr (kGrad) {
-        // dh's tile through LDS: whole 16-byte chunks (F % 8 == 0), zero outside
-        for (int q = tid; q < BM * kChunks; q += P::kThreads) {
-            const int row = q / kChunks, ch = q % kChunks;
-            const int m = m0 + row, f = f0 + 8 * ch;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (m < M && f < F) v = *reinterpret_cast<const uint4*>(a.dh + (size_t)m * F + f);
-            *reinterpret_cast<uint4*>(t0 + row * kRow + 16 * ch) = v;
-        }
-        __syncthreads();
+        // dh of the lane's 4 columns, which lie wholly inside or outside (F % 8 == 0)
+#pragma unroll
+        for (int r = 0; r < P::MR; ++r)
+#pragma unroll
+            for (int j = 0; j < HB; ++j) {
+                const int m = m0 + 16 * r + c, f = f0 + 16 * (w * HB + j) + 4 * h;
+                const uint2 v = *reinterpret_cast<const uint2*>(a.dh + (size_t)(m < M ? m : M - 1) * F + (f < F ? f : F - 4));
+                dv[r][j] = m < M && f < F ? v : make_uint2(0u, 0u);
+            }
     }
 #pragma unroll
     for (int r = 0; r < P::MR; ++r) {
+        [[maybe_unused]] float top = 0.f;
 #pragma unroll
         for (int j = 0; j < HB; ++j) {
-            const int at = (16 * r + c) * kRow + 2 * (16 * (w * HB + j) + 4 * h);      // 4 columns of a row
-            float o0[4], o1[4];
-            uint2 dv = make_uint2(0u, 0u);
-            if constexpr (kGrad) dv = *reinterpret_cast<const uint2*>(t0 + at);
+            const int at = (16 * r + c) * kRow + kSize * (16 * (w * HB + j) + 4 * h);      // 4 columns of a row
+            f32x4 o0, o1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float g = acc[r][j][e], u = acc[r][j + HB][e];
@@ -69,30 +75,44 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::S
                 if constexpr (!kGrad) {
                     o0[e] = g * pr * u;
                 } else {
-                    const uint32_t dw = e < 2 ? dv.x : dv.y;
+                    const uint32_t dw = e < 2 ? dv[r][j].x : dv[r][j].y;
                     const float d = half_bits_to_f32<P::kBF16>(e & 1 ? dw >> 16 : dw & 0xFFFFu);
                     o0[e] = d * u * fmaf(g, slope, pr);
                     o1[e] = d * (g * pr);
+                    top = fmaxf(top, fmaxf(fabsf(o0[e]), fabsf(o1[e])));
                 }
             }
-            constexpr bool kOut = kGrad || P::kBF16;
-            *reinterpret_cast<uint2*>(t0 + at) = make_uint2(pack2_rne<kOut>(o0[0], o0[1]), pack2_rne<kOut>(o0[2], o0[3]));
-            if constexpr (kGrad)
-                *reinterpret_cast<uint2*>(t1 + at) = make_uint2(pack2_rne<true>(o1[0], o1[1]), pack2_rne<true>(o1[2], o1[3]));
+            if constexpr (!kGrad) {
+                *reinterpret_cast<uint2*>(t0 + at) =
+                    make_uint2(pack2_rne<P::kBF16>(o0[0], o0[1]), pack2_rne<P::kBF16>(o0[2], o0[3]));
+            } else {
+                *reinterpret_cast<f32x4*>(t0 + at) = o0;
+                *reinterpret_cast<f32x4*>(t1 + at) = o1;
+            }
+        }
+        if constexpr (kGrad) {
+            top = quarter_max(top);
+            if (h == 0) red[w * BM + 16 * r + c] = top;
         }
     }
     __syncthreads();
     for (int q = tid; q < BM * kChunks; q += P::kThreads) {
         const int row = q / kChunks, ch = q % kChunks;
-        const int m = m0 + row, f = f0 + 8 * ch;
+        const int m = m0 + row, f = f0 + 16 / kSize * ch;
         if (m >= M || f >= F) continue;
         const uint4 v = *reinterpret_cast<const uint4*>(t0 + row * kRow + 16 * ch);
         if constexpr (!kGrad) {
             *reinterpret_cast<uint4*>(a.h + (size_t)m * F + f) = v;
         } else {
             *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + f) = v;
-            *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + F + f) =
-                *reinterpret_cast<const uint4*>(t1 + row * kRow + 16 * ch);
+            *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + F + f) = *reinterpret_cast<const uint4*>(t1 + row * kRow + 16 * ch);
+        }
+    }
+    if constexpr (kGrad) {
+        if (tid < BM && m0 + tid < M) {
+            float top = red[tid];
+            for (int i = 1; i < P::W; ++i) top = fmaxf(top, red[i * BM + tid]);
+            a.tops[(size_t)(f0 / BN) * M + m0 + tid] = top;
         }
     }
 }
@@ -111,6 +131,41 @@ __global__ __launch_bounds__(P::kThreads) void gated_kernel(const GatedArgs a) {
     if (a.act == 0) gated_epilogue<P, kGrad, 0>(a, sh, m0, f0, acc);
     else if (a.act == 1) gated_epilogue<P, kGrad, 1>(a, sh, m0, f0, acc);
     else gated_epilogue<P, kGrad, 2>(a, sh, m0, f0, acc);
+}
+
+// Workgroups 0 .. kScaleParts - 1: the weight's largest |scale|, a part each. The others: 16
+// rows each, 16 threads a row, their largest |d| over the column tiles.
+template <bool kBF16>
+__global__ __launch_bounds__(256) void tops_kernel(const float* __restrict__ tops, int tiles, const uint32_t* __restrict__ meta,
+                                                   int64_t words, int M, float* __restrict__ rowmax,
+                                                   float* __restrict__ scale_max) {
+    __shared__ float red[16][17];
+    const int tid = (int)threadIdx.x, i = tid & 15, g = tid >> 4;
+    float top = 0.f;
+    if ((int)blockIdx.x < kScaleParts) {
+#pragma unroll 4
+        for (int64_t k = (int64_t)blockIdx.x * 256 + tid; 4 * k < words; k += kScaleParts * 256) {
+            const uint4 v = *reinterpret_cast<const uint4*>(meta + 4 * k);
+            for (const uint32_t q : {v.x, v.y, v.z, v.w}) top = fmaxf(top, fabsf(half_bits_to_f32<kBF16>(q & 0xFFFFu)));
+        }
+    } else {
+        const int m = ((int)blockIdx.x - kScaleParts) * 16 + i;
+#pragma unroll 4
+        for (int t = g; t < tiles; t += 16) top = fmaxf(top, tops[(size_t)t * M + (m < M ? m : M - 1)]);
+    }
+    red[g][i] = top;
+    __syncthreads();
+    if ((int)blockIdx.x < kScaleParts) {
+        if (g == 0) {
+            for (int k = 1; k < 16; ++k) top = fmaxf(top, red[k][i]);
+            for (int s = 1; s < 16; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
+            if (i == 0) scale_max[blockIdx.x] = top;
+        }
+    } else if (g == 0) {
+        const int m = ((int)blockIdx.x - kScaleParts) * 16 + i;
+        for (int k = 1; k < 16; ++k) top = fmaxf(top, red[k][i]);
+        if (m < M) rowmax[m] = top;
+    }
 }
 
 template <bool kBF16, int MR, int CBW, int kSub, bool kGrad>
@@ -182,6 +237,20 @@ ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gat
     return p;
 }
 
+int gated_tiles(int64_t M, int64_t K, int64_t F, int64_t G) {
+    return small_product(M, K) ? small_workgroups(F / 8) : plan_product(M, K, 2 * F, G, true).tiles_n;
+}
+
+hipError_t launch_gated_tops(const float* tops, int tiles, const uint8_t* packed, int64_t M, int64_t K, int64_t N, int64_t G,
+                             bool bf16, float* rowmax, float* scale_max, hipStream_t stream) {
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(packed + (size_t)K * padded_cols(N) / 2);
+    const int64_t words = padded_cols(N) * padded_units(K, G);
+    const dim3 grid((unsigned)(kScaleParts + (M + 15) / 16)), block(256);
+    if (bf16) hipLaunchKernelGGL((tops_kernel<true>), grid, block, 0, stream, tops, tiles, meta, words, (int)M, rowmax, scale_max);
+    else hipLaunchKernelGGL((tops_kernel<false>), grid, block, 0, stream, tops, tiles, meta, words, (int)M, rowmax, scale_max);
+    return hipGetLastError();
+}
+
 hipError_t launch_gated(const GatedCall& q, hipStream_t stream) {
     if (small_product(q.M, q.K)) return launch_gated_small(q, stream);
     const ProductPlan p = plan_product(q.M, q.K, 2 * q.F, q.G, true);
@@ -200,6 +269,7 @@ hipError_t launch_gated(const GatedCall& q, hipStream_t stream) {
     a.h = q.h;
     a.dh = q.dh;
     a.d = q.d;
+    a.tops = q.tops;
     a.act = q.act;
     if (q.d) {
         if (q.bf16) launch_typed<true, true>(p, a, stream);

@@ -44,18 +44,38 @@ struct GradArgs {
     const float* factor;
     const float* before;
     int factor_stages;      // stages of one column of `factor`
+    const float* d32;
+    const float* rowmax;
+    const float* scale_max;
 };
+
+// Powers of two that bring fp32 gradients and the weights into fp16 (24 binades above the
+// last that is normal and 24 below its first value keep 11 bits of everything that counts
+// in a row): a row's largest |d| goes to [2^4, 2^5), the weight's largest |scale| to
+// [2^6, 2^7), so that 15 times it stays below 2^11. Exact, and taken off the result again.
+__device__ __forceinline__ int scale_exponent(float top, int to) {
+    if (!(top > 0.f) || top > 3e38f) return 0;
+    int e = to - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
+    return e < -100 ? -100 : e > 100 ? 100 : e;
+}
+__device__ __forceinline__ int row_exponent(const float* rowmax, int m) { return scale_exponent(rowmax[m], 4); }
+__device__ __forceinline__ int weight_exponent(const float* scale_max) {       // by every lane of a wave
+    float top = scale_max[threadIdx.x & 63];
+    for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+    return scale_exponent(top, 6);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // 8 codes -> 8 operand values (q - z) s in row order
 template <bool kOpBF16, bool kScaleBF16>
 struct Decode {
+    static_assert(kOpBF16 && kScaleBF16, "bf16 operands from bf16 scales");
     float s, nzs;
     __device__ __forceinline__ explicit Decode(uint32_t md) {
         s = half_bits_to_f32<kScaleBF16>(md & 0xFFFFu);
         nzs = -(float)((md >> 16) & 0xFu) * s;
     }
     __device__ __forceinline__ uint4 operator()(uint32_t d) const {
-        static_assert(kOpBF16, "fp16 operands decode in packed fp16");
         uint32_t lo = d & 0x0F0F0F0Fu, hi = (d >> 4) & 0x0F0F0F0Fu;    // rows 0,4,1,5 / 2,6,3,7
         asm volatile("" : "+v"(lo), "+v"(hi));
         const float r0 = fmaf((float)(lo & 0xFFu), s, nzs), r4 = fmaf((float)((lo >> 8) & 0xFFu), s, nzs);
@@ -71,13 +91,24 @@ struct Decode<false, false> : Dequant<false> {
     __device__ __forceinline__ explicit Decode(uint32_t md) : Dequant<false>(md) {}
 };
 
+// codes -> fp16 (q - z) (s 2^e), s of either type
+template <bool kScaleBF16>
+struct DecodeScaled : Dequant<false> {
+    __device__ __forceinline__ DecodeScaled(uint32_t md, float by) {
+        const _Float16 zb = (_Float16)(1024.0f + (float)((md >> 16) & 0xFu));
+        const _Float16 s = (_Float16)(half_bits_to_f32<kScaleBF16>(md & 0xFFFFu) * by);
+        zz = f16x2{zb, zb};
+        ss = f16x2{s, s};
+    }
+};
+
 // One stage: D rows [BM][8 chunks of 16 bytes], chunk j of row r at j ^ (r % 8); W rows
 // [64 n][32 chunks of 8 k], chunk j of row n at j ^ swz(n). swz spreads the 8 lanes of a
 // write (8 consecutive n, one chunk) over 8 chunks and the 16 rows of a transposing read
 // (n % 8 in a half, all n / 8) evenly over 4 chunk pairs.
 __device__ __forceinline__ int swz(int n) { return (n & 7) ^ (2 * ((n >> 3) & 3)); }
 
-template <bool kOpBF16, bool kScaleBF16, int MR, int WM, int CK, int kSub>
+template <bool kOpBF16, bool kScaleBF16, int MR, int WM, int CK, int kSub, bool kD32>
 __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     constexpr int WK = 8 / WM;
     constexpr int BM = 16 * MR * WM;
@@ -118,6 +149,12 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     const int NB = Np / kColsPerBlock;
     const uint8_t* meta = a.packed + (size_t)a.K * Np / 2;
 
+    [[maybe_unused]] int we = 0;
+    [[maybe_unused]] float wscale = 1.f;
+    if constexpr (kD32) {
+        we = weight_exponent(a.scale_max);
+        wscale = power_of_two(we);
+    }
     uint4 code;
     uint32_t md[kSub];
     auto load_codes = [&](int t) {
@@ -135,9 +172,11 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         const int row = 16 * nbi + cc;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const Decode<kOpBF16, kScaleBF16> dq(md[(i * kSub) / 4]);
             const uint32_t d = i == 0 ? code.x : i == 1 ? code.y : i == 2 ? code.z : code.w;
-            ring[slot].w[row * 32 + ((16 * kbi + 4 * i + hh) ^ swz(row))] = dq(d);
+            uint4 v;
+            if constexpr (kD32) v = DecodeScaled<kScaleBF16>(md[(i * kSub) / 4], wscale)(d);
+            else v = Decode<kOpBF16, kScaleBF16>(md[(i * kSub) / 4])(d);
+            ring[slot].w[row * 32 + ((16 * kbi + 4 * i + hh) ^ swz(row))] = v;
         }
     };
     // D rows m0 + 8 slab + lane / 8, 16-byte chunk (lane % 8) ^ (row % 8). Rows past M read
@@ -168,6 +207,43 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         }
     };
 
+    // D in fp32: chunk q = tid + 512 i of the stage (row q / 8, 8 columns) through registers,
+    // one stage ahead, scaled by its row's power of two and rounded to fp16
+    constexpr int kChunks = kD32 ? (BM * 8 + 511) / 512 : 1;
+    [[maybe_unused]] f32x4 dv[kChunks][2];
+    [[maybe_unused]] float dscale[kChunks];
+    [[maybe_unused]] const float* drow[kChunks];
+    if constexpr (kD32) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int row = ((tid + 512 * i) >> 3) % BM;
+            const int m = m0 + row < a.M ? m0 + row : a.M - 1;
+            dscale[i] = power_of_two(row_exponent(a.rowmax, m));
+            drow[i] = a.d32 + (size_t)m * a.ld + 8 * (tid & 7);
+        }
+    }
+    auto load_d = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int n = t * kStageN + 8 * (tid & 7);
+            // columns past the last (n % 8 == 0) read the last and weigh zero: their weights do
+            const float* p = drow[i] + (n < a.n ? t * kStageN : a.n - 8 - 8 * (tid & 7));
+            dv[i][0] = *reinterpret_cast<const f32x4*>(p);
+            dv[i][1] = *reinterpret_cast<const f32x4*>(p + 4);
+        }
+    };
+    auto store_d = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int q = tid + 512 * i;
+            if (BM * 8 % 512 != 0 && q >= BM * 8) break;
+            const int row = q >> 3, ch = q & 7;
+            const f32x4 lo = dv[i][0] * dscale[i], hi = dv[i][1] * dscale[i];
+            ring[slot].d[row * 8 + (ch ^ (row & 7))] = make_uint4(pack2_rne<false>(lo[0], lo[1]), pack2_rne<false>(lo[2], lo[3]),
+                                                                  pack2_rne<false>(hi[0], hi[1]), pack2_rne<false>(hi[2], hi[3]));
+        }
+    };
+
     f32x4 acc[MR][CK];
 #pragma unroll
     for (int r = 0; r < MR; ++r)
@@ -177,9 +253,17 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     const bool hot = a.hot && *a.hot != 0;
     if (st_lo < st_hi) {
         load_codes(st_lo);
-        issue_d(0, st_lo);
+        if constexpr (kD32) {
+            load_d(st_lo);
+            store_d(0);
+        } else {
+            issue_d(0, st_lo);
+        }
         store_codes(0);
-        if (st_lo + 1 < st_hi) load_codes(st_lo + 1);
+        if (st_lo + 1 < st_hi) {
+            load_codes(st_lo + 1);
+            if constexpr (kD32) load_d(st_lo + 1);
+        }
     }
     for (int t = st_lo; t < st_hi; ++t) {
         const int slot = (t - st_lo) & 1;
@@ -202,10 +286,14 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
             }
         }
         if (t + 1 < st_hi) {
-            issue_d(slot ^ 1, t + 1);
+            if constexpr (kD32) store_d(slot ^ 1);
+            else issue_d(slot ^ 1, t + 1);
             store_codes(slot ^ 1);
         }
-        if (t + 2 < st_hi) load_codes(t + 2);
+        if (t + 2 < st_hi) {
+            load_codes(t + 2);
+            if constexpr (kD32) load_d(t + 2);
+        }
         const Stage& st = ring[slot];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -253,6 +341,10 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
                 if (a.add) v += hot ? *o * a.before[m] : *o;
                 *o = v;
             } else {
+                if constexpr (kD32) {
+                    v *= power_of_two(-row_exponent(a.rowmax, m));
+                    v *= power_of_two(-we);
+                }
                 const uint2 o = make_uint2(pack2_rne<kScaleBF16>(v[0], v[1]), pack2_rne<kScaleBF16>(v[2], v[3]));
                 *reinterpret_cast<uint2*>(a.dx + (size_t)m * a.K + k) = o;
             }
@@ -262,9 +354,11 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
 
 // dx = sum_s part[s], 8 values a thread; bandwidth-bound over the partials
 template <bool kBF16>
-__global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restrict__ part, int splits, int64_t MK,
-                                                          uint16_t* __restrict__ dx) {
+__global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restrict__ part, int splits, int64_t MK, int K,
+                                                          const float* __restrict__ rowmax,
+                                                          const float* __restrict__ scale_max, uint16_t* __restrict__ dx) {
     const int64_t at = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    const int we = rowmax ? weight_exponent(scale_max) : 0;
     if (at >= MK) return;
     f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
 #pragma unroll 4
@@ -273,25 +367,32 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restric
         s0 += p[0];
         s1 += p[1];
     }
+    if (rowmax) {
+        const float by = power_of_two(-row_exponent(rowmax, (int)(at / K))), by2 = power_of_two(-we);
+        s0 = s0 * by * by2;
+        s1 = s1 * by * by2;
+    }
     *reinterpret_cast<uint4*>(dx + at) = make_uint4(pack2_rne<kBF16>(s0[0], s0[1]), pack2_rne<kBF16>(s0[2], s0[3]),
                                                     pack2_rne<kBF16>(s1[0], s1[1]), pack2_rne<kBF16>(s1[2], s1[3]));
 }
 
-template <bool kOp, bool kSc, int kSub>
+template <bool kOp, bool kSc, int kSub, bool kD32>
 void launch_sub(int bm, const GradArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.tiles_m * a.tiles_k * a.splits)), block(512);
-    if (bm == 16) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 1, 1, 2, kSub>), grid, block, 0, s, a);
-    else if (bm == 32) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 2, 1, 2, kSub>), grid, block, 0, s, a);
-    else if (bm == 64) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 1, 2, kSub>), grid, block, 0, s, a);
-    else if (bm == 128) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 2, 4, kSub>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((grad_kernel<kOp, kSc, 8, 2, 4, kSub>), grid, block, 0, s, a);
+    if (bm == 16) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 1, 1, 2, kSub, kD32>), grid, block, 0, s, a);
+    else if (bm == 32) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 2, 1, 2, kSub, kD32>), grid, block, 0, s, a);
+    else if (bm == 64) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 1, 2, kSub, kD32>), grid, block, 0, s, a);
+    else if (bm == 128) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 2, 4, kSub, kD32>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((grad_kernel<kOp, kSc, 8, 2, 4, kSub, kD32>), grid, block, 0, s, a);
 }
 
-template <bool kOp, bool kSc>
+// operands: bf16 or fp16 as the scales, or fp16 from fp32
+template <bool kSc, bool kD32>
 void launch_typed(int bm, int sub, const GradArgs& a, hipStream_t s) {
-    if (sub == 4) launch_sub<kOp, kSc, 4>(bm, a, s);
-    else if (sub == 2) launch_sub<kOp, kSc, 2>(bm, a, s);
-    else launch_sub<kOp, kSc, 1>(bm, a, s);
+    constexpr bool kOp = kSc && !kD32;
+    if (sub == 4) launch_sub<kOp, kSc, 4, kD32>(bm, a, s);
+    else if (sub == 2) launch_sub<kOp, kSc, 2, kD32>(bm, a, s);
+    else launch_sub<kOp, kSc, 1, kD32>(bm, a, s);
 }
 
 }  // namespace
@@ -347,22 +448,26 @@ hipError_t launch_grad(const GradPlan& plan, const GradCall& q, hipStream_t stre
     a.before = q.before;
     a.factor_stages = q.factor_columns / kStageN;
     if ((plan.splits > 1 || !q.dx) && !q.part) return hipErrorInvalidValue;
+    a.d32 = q.d32;
+    a.rowmax = q.rowmax;
+    a.scale_max = q.scale_max;
     const int sub = units_per_block(q.G);
-    if (q.op_bf16) {
-        if (q.scale_bf16) launch_typed<true, true>(plan.bm, sub, a, stream);
-        else launch_typed<true, false>(plan.bm, sub, a, stream);
+    if (q.d32) {
+        if (q.bf16) launch_typed<true, true>(plan.bm, sub, a, stream);
+        else launch_typed<false, true>(plan.bm, sub, a, stream);
     } else {
-        launch_typed<false, false>(plan.bm, sub, a, stream);
+        if (q.bf16) launch_typed<true, false>(plan.bm, sub, a, stream);
+        else launch_typed<false, false>(plan.bm, sub, a, stream);
     }
     return hipGetLastError();
 }
 
 hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, uint16_t* dx, bool bf16,
-                              hipStream_t stream) {
+                              const float* rowmax, const float* scale_max, hipStream_t stream) {
     const int64_t MK = M * K;
     const dim3 grid((unsigned)((MK / 8 + 255) / 256)), block(256);
-    if (bf16) hipLaunchKernelGGL((grad_finish_kernel<true>), grid, block, 0, stream, part, splits, MK, dx);
-    else hipLaunchKernelGGL((grad_finish_kernel<false>), grid, block, 0, stream, part, splits, MK, dx);
+    if (bf16) hipLaunchKernelGGL((grad_finish_kernel<true>), grid, block, 0, stream, part, splits, MK, (int)K, rowmax, scale_max, dx);
+    else hipLaunchKernelGGL((grad_finish_kernel<false>), grid, block, 0, stream, part, splits, MK, (int)K, rowmax, scale_max, dx);
     return hipGetLastError();
 }
 

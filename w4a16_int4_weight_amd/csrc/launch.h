@@ -119,14 +119,15 @@ struct ProductPlan {
 };
 ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gated);
 
-// Gated block: h = a(x Wg) (x Wu) when d is NULL; else d = [dg, du] bf16 [M, 2F] from dh.
+// Gated block: h = a(x Wg) (x Wu) when d is NULL; else d = [dg, du] fp32 [M, 2F] from dh.
 // act: 0 silu, 1 gelu, 2 gelu's tanh form. counters / partials as plan_product asks.
 struct GatedCall {
     const uint16_t* x;
     const uint16_t* dh;
     const uint8_t* packed;
     uint16_t* h;
-    uint16_t* d;
+    float* d;
+    float* tops;           // [gated_tiles(...)][M] largest |d| of a row in each share of the columns
     int64_t M, K, F, G;
     int act;
     bool bf16;
@@ -134,6 +135,12 @@ struct GatedCall {
     float* partials;
 };
 hipError_t launch_gated(const GatedCall& call, hipStream_t stream);
+int gated_tiles(int64_t M, int64_t K, int64_t F, int64_t G);
+// Between a backward's products: the rows' largest |d| from `tops`, and the largest |scale|
+// of the weight in kScaleParts parts.
+constexpr int kScaleParts = 64;
+hipError_t launch_gated_tops(const float* tops, int tiles, const uint8_t* packed, int64_t M, int64_t K, int64_t N, int64_t G,
+                             bool bf16, float* rowmax, float* scale_max, hipStream_t stream);
 
 // Up to 16 rows (csrc/product_small.hip): the gated block, and the head's statistics for
 // cross entropy: the labels' logits and (max, sum) per row and workgroup, part
@@ -144,8 +151,7 @@ hipError_t launch_gated_small(const GatedCall& call, hipStream_t stream);
 hipError_t launch_ce_small(const uint16_t* x, const int32_t* labels, const uint8_t* packed, int64_t M, int64_t K, int64_t V,
                            int64_t G, bool bf16, float* zsel, float* part, hipStream_t stream);
 
-// dx = coef . (D W^T): D [M, columns n0 .. n0 + n) of the weight, row stride ld, operands
-// bf16 (op_bf16) or fp16; out 16-bit of out_bf16. The sum over columns is split over
+// dx = D W^T: D [M, columns n0 .. n0 + n) of the weight, row stride ld, of the weight's type. The sum over columns is split over
 // `splits` workgroups and may be cut into calls: with `part` set, partial tiles
 // [splits][M][K] fp32 are written (or, with `add`, added to); grad_finish sums them.
 struct GradCall {
@@ -157,13 +163,18 @@ struct GradCall {
     bool add;
     int64_t M, K, N, G;    // N: columns of the weight
     int64_t n0, n;         // n0 % 64 == 0
-    bool op_bf16, scale_bf16;
+    bool bf16;
     // when *hot is set: D's rows are multiplied by factor[tile][M], tile of factor_columns
     // columns from n0, and what `add` adds to by before[M]. hot may be NULL.
     const int* hot;
     const float* factor;
     const float* before;
     int factor_columns;
+    // D in fp32 instead (d NULL, ld = n): its rows, scaled by powers of two from their
+    // largest values, and the weights, from the largest scale, both enter in fp16
+    const float* d32;
+    const float* rowmax;
+    const float* scale_max;
 };
 struct GradPlan {
     int bm;                // rows of a tile: 16, 32, 64, 128 or 256
@@ -174,9 +185,9 @@ struct GradPlan {
 // `forced`: the sum comes in several calls, so partials are needed at any split.
 GradPlan plan_grad(int64_t M, int64_t K, int64_t n, bool forced);
 hipError_t launch_grad(const GradPlan& plan, const GradCall& call, hipStream_t stream);
-// dx[m, k] = sum_s part[s][m][k], rounded once
+// dx[m, k] = sum_s part[s][m][k], rounded once (rowmax, scale_max: of a product with d32)
 hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, uint16_t* dx, bool bf16,
-                              hipStream_t stream);
+                              const float* rowmax, const float* scale_max, hipStream_t stream);
 
 // Cross entropy (top NULL, T = 1) or distillation over the packed head. lse and loss
 // [M] fp32; dx (or NULL) with dloss (or NULL: 1). The workspace holds loss_workspace(...)

@@ -686,7 +686,7 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
             g.G = q.G;
             g.n0 = n0;
             g.n = n;
-            g.op_bf16 = g.scale_bf16 = q.bf16;
+            g.bf16 = q.bf16;
             g.hot = hot;
             g.factor = floats(l.factor);
             g.before = floats(l.before);

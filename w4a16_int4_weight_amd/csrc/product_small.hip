@@ -35,7 +35,8 @@ struct SmallArgs {
     // gated
     uint16_t* h;
     const uint16_t* dh;
-    uint16_t* d;
+    float* d;
+    float* tops;            // [workgroups][M]
     int act;
     // cross entropy
     const int32_t* labels;
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
     constexpr int kRowStep = kThreads / (kCols * S);       // rows met at a time
     constexpr int kSlots = kGated || kRowStep >= 16 ? 1 : 16 / kRowStep;
     const int oc = tid % kCols, os = tid / kCols % S, om = tid / (kCols * S);
-    [[maybe_unused]] float top[kSlots], sum[kSlots];
+    [[maybe_unused]] float top[kSlots], sum[kSlots], most = 0.f;
     [[maybe_unused]] int label[kSlots];
     if constexpr (!kGated) {
 #pragma unroll
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
         __syncthreads();
         const int u = u0 + os;
         if constexpr (kGated) {
-            for (int m = om; m < M; m += kRowStep) {
+            for (int m = om; m < M; m += kRowStep) {              // one row a thread: M <= 16 <= kRowStep
                 if (u >= hi) continue;
                 const float gv = total(buf, os, m, oc), uv = total(buf, os, m, oc + 8);
                 const size_t f = (size_t)8 * u + oc;
@@ -193,8 +194,10 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
                 const float pr = a.act == 0 ? gate_prob<0>(gv, &slope) : a.act == 1 ? gate_prob<1>(gv, &slope) : gate_prob<2>(gv, &slope);
                 if (a.d) {
                     const float dv = half_bits_to_f32<kBF16>(a.dh[(size_t)m * a.F + f]);
-                    a.d[(size_t)m * 2 * a.F + f] = f32_to_half_bits<true>(dv * uv * fmaf(gv, slope, pr));
-                    a.d[(size_t)m * 2 * a.F + a.F + f] = f32_to_half_bits<true>(dv * (gv * pr));
+                    const float dg = dv * uv * fmaf(gv, slope, pr), du = dv * (gv * pr);
+                    a.d[(size_t)m * 2 * a.F + f] = dg;
+                    a.d[(size_t)m * 2 * a.F + a.F + f] = du;
+                    most = fmaxf(most, fmaxf(fabsf(dg), fabsf(du)));
                 } else {
                     a.h[(size_t)m * a.F + f] = f32_to_half_bits<kBF16>(gv * pr * uv);
                 }
@@ -218,6 +221,14 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
     for (int u0 = lo; u0 < hi; u0 += 2 * S) {
         turn(b0, b1, u0, 0);
         if (u0 + S < hi) turn(b1, b0, u0 + S, 1);
+    }
+    if constexpr (kGated) {
+        static_assert(kRowStep >= 16, "a thread meets one row");
+        if (a.d) {
+#pragma unroll
+            for (int s = 1; s < kCols * S; s *= 2) most = fmaxf(most, __shfl_xor(most, s));
+            if (oc == 0 && os == 0 && om < M) a.tops[(size_t)g * M + om] = most;
+        }
     }
     if constexpr (!kGated) {
         // a row's kCols S threads are neighbours in one wave
@@ -276,6 +287,7 @@ hipError_t launch_gated_small(const GatedCall& q, hipStream_t stream) {
     a.h = q.h;
     a.dh = q.dh;
     a.d = q.d;
+    a.tops = q.tops;
     a.act = q.act;
     launch_any<true>(a, units_per_block(q.G), q.bf16, small_workgroups(a.U), stream);
     return hipGetLastError();
