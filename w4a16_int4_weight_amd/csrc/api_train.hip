@@ -18,7 +18,7 @@ using w4a16::kMaxMK;
 using w4a16::packed_size;
 
 constexpr int64_t kMaxRowElements = int64_t(1) << 22;     // a 256-row tile is addressed in 32 bits
-constexpr int64_t kGatedRowsPerPass = 8192;            // of a backward: 8 F bytes a row
+constexpr int64_t kGatedRowsPerPass = 8192;            // of a backward: 4 F bytes a row
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -63,10 +63,10 @@ w4a16_status check_gated(int64_t M, int64_t K, int64_t F, int64_t group_size, in
 }
 
 struct GatedLayout {
-    size_t partials, tops, rowmax, scale_max, d, gpart, end;
+    size_t partials, tops, rowmax, factor, scale_max, d, d32, gpart, end;
 };
 
-// one pass over M rows: the forward's K-split partials and, for the gradient, dg | du in fp32 and
+// one pass over M rows: the forward's K-split partials and, for the gradient, dg | du and
 // the transposed product's partials
 GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) {
     GatedLayout l{};
@@ -78,10 +78,14 @@ GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) 
         at += round256((size_t)w4a16::gated_tiles(M, K, F, G) * M * 4);
         l.rowmax = at;
         at += round256((size_t)M * 4);
+        l.factor = at;
+        at += round256((size_t)w4a16::gated_tiles(M, K, F, G) * M * 4);
         l.scale_max = at;
         at += round256(w4a16::kScaleParts * 4);
         l.d = at;
-        at += round256((size_t)M * 8 * F);
+        at += round256((size_t)M * 4 * F);
+        l.d32 = at;
+        if (w4a16::small_product(M, K)) at += round256((size_t)M * 8 * F);
         l.gpart = at;
         at += round256(w4a16::plan_grad(M, K, 2 * F, false).part_bytes);
     } else if (partial == 0) {
@@ -266,7 +270,8 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         q.x = static_cast<const uint16_t*>(x) + r0 * K;
         q.dh = static_cast<const uint16_t*>(dh) + r0 * F;
         q.packed = static_cast<const uint8_t*>(packed);
-        q.d = reinterpret_cast<float*>(ws + l.d);
+        q.d = reinterpret_cast<uint16_t*>(ws + l.d);
+        q.d32 = reinterpret_cast<float*>(ws + l.d32);
         q.tops = reinterpret_cast<float*>(ws + l.tops);
         float* rowmax = reinterpret_cast<float*>(ws + l.rowmax);
         float* scale_max = reinterpret_cast<float*>(ws + l.scale_max);
@@ -280,15 +285,17 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         q.partials = reinterpret_cast<float*>(ws + l.partials);
         hipError_t err = w4a16::launch_gated(q, s);
         if (err == hipSuccess)
-            err = w4a16::launch_gated_tops(q.tops, w4a16::gated_tiles(rows, K, F, G), q.packed, rows, K, 2 * F, G, bf16, rowmax,
-                                           scale_max, s);
+            err = w4a16::launch_gated_tops(q, rowmax, reinterpret_cast<uint32_t*>(ws + l.factor), scale_max, s);
         if (err != hipSuccess) return W4A16_ERR_HIP;
         const w4a16::GradPlan plan = w4a16::plan_grad(rows, K, 2 * F, false);
         float* part = plan.part_bytes ? reinterpret_cast<float*>(ws + l.gpart) : nullptr;
         uint16_t* out = static_cast<uint16_t*>(dx) + r0 * K;
         w4a16::GradCall g{};
-        g.d32 = q.d;
+        g.d = q.d;
+        g.scaled = true;
         g.rowmax = rowmax;
+        g.tile_columns = w4a16::gated_tile_columns(rows, K, F, G);
+        g.tile_factor = g.tile_columns ? reinterpret_cast<uint32_t*>(ws + l.factor) : nullptr;
         g.scale_max = scale_max;
         g.ld = 2 * F;
         g.packed = q.packed;

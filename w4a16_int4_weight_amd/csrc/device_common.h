@@ -159,6 +159,18 @@ template <> struct Dequant<false> {
     }
 };
 
+// Powers of two that bring fp32 gradients and the weights into fp16, whose first 24 binades
+// from the top keep 11 bits: a set of gradients' largest magnitude goes to [2^4, 2^5), the
+// weight's largest |scale| to [2^6, 2^7), so that 15 times it stays below 2^11. Exact, and
+// taken off the result again. (Zero, infinite or no number: 0.)
+constexpr int kGradTop = 4, kScaleTop = 6;
+__device__ __forceinline__ int scale_exponent(float top, int to) {
+    if (!(top > 0.f) || top > 3e38f) return 0;
+    const int e = to - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
+    return e < -100 ? -100 : e > 100 ? 100 : e;
+}
+__device__ __forceinline__ float power_of_two(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // Direct global -> LDS copies (global_load_lds): each lane's 4 or 16 bytes land at
 // M0 + 4*lane or M0 + 16*lane, M0 being uniform over the wave. They count in vmcnt
 // like loads but occupy no registers, so several k blocks can be in flight. They are

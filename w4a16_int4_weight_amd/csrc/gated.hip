@@ -8,9 +8,9 @@
 // blocks and the HB matching up blocks, so g and u never leave its registers and the
 // block costs one product and one pass over x. The backward recomputes them (keeping
 // them would take 4 F bytes a token and round them to 16 bits), writes dg and du to the
-// workspace in fp32 with their rows' largest values, and one product with W^T follows, which
-// takes them in fp16 scaled row by row (gemm_grad.hip): rounded to bf16 they would be off by
-// as much as the result's own rounding.
+// workspace in fp16, scaled by a power of two for each row of a tile, and one product with
+// W^T follows, which brings a row's tiles to one scale (gemm_grad.hip): rounded to bf16 they
+// would be off by as much as the result's own rounding, and fp32 took 8 F bytes a row.
 #include "device_common.h"
 #include "gate.h"
 #include "launch.h"
@@ -25,20 +25,20 @@ struct GatedArgs {
     ProductArgs p;
     uint16_t* h;            // forward: [M, F]
     const uint16_t* dh;     // backward: [M, F]
-    float* d;               // backward: [M, 2F], dg then du
+    uint16_t* d;            // backward: [M, 2F] fp16, dg then du
     float* tops;            // [column tiles][M] largest |d| of a row
     int act;
 };
 
-// The tile's results go through LDS and leave as whole rows. (Stored from the lanes, 64
-// bytes a row and instruction, a backward's two fp32 tiles took 12 us of a 47 us tile.)
+// The tile's results go through LDS and leave as whole rows. A backward forms dg and du in
+// the accumulators, takes each row's largest over the workgroup's columns, and rounds them
+// once, scaled by its power of two.
 template <class P, bool kGrad, int kAct>
 __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::Shared& sh, int m0, int f0,
                                                f32x4 (&acc)[P::MR][P::CBW]) {
     constexpr int BM = P::BM, BN = P::BN, HB = P::HB;
-    constexpr int kSize = kGrad ? 4 : 2;                     // bytes of an output
-    constexpr int kRow = BN * kSize + 16;                    // bytes of a tile row, padded
-    constexpr int kChunks = BN * kSize / 16;
+    constexpr int kRow = BN * 2 + 16;                        // bytes of a tile row, padded
+    constexpr int kChunks = BN / 8;
     static_assert((kGrad ? 2 : 1) * BM * kRow + P::W * BM * 4 <= (int)sizeof(typename P::Shared), "the output tiles fit in LDS");
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -48,9 +48,24 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::S
     uint8_t* t0 = reinterpret_cast<uint8_t*>(&sh);
     uint8_t* t1 = t0 + BM * kRow;
     float* red = reinterpret_cast<float*>(t1 + BM * kRow);   // backward: [W][BM]
-    [[maybe_unused]] uint2 dv[P::MR][HB];
-    if constexpr (kGrad) {
+    auto place = [&](int r, int j) { return (16 * r + c) * kRow + 2 * (16 * (w * HB + j) + 4 * h); };     // 4 columns of a row
+    if constexpr (!kGrad) {
+#pragma unroll
+        for (int r = 0; r < P::MR; ++r)
+#pragma unroll
+            for (int j = 0; j < HB; ++j) {
+                float o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float g = acc[r][j][e];
+                    float slope;
+                    o[e] = g * gate_prob<kAct>(g, &slope) * acc[r][j + HB][e];
+                }
+                *reinterpret_cast<uint2*>(t0 + place(r, j)) = make_uint2(pack2_rne<P::kBF16>(o[0], o[1]), pack2_rne<P::kBF16>(o[2], o[3]));
+            }
+    } else {
         // dh of the lane's 4 columns, which lie wholly inside or outside (F % 8 == 0)
+        uint2 dv[P::MR][HB];
 #pragma unroll
         for (int r = 0; r < P::MR; ++r)
 #pragma unroll
@@ -59,46 +74,46 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::S
                 const uint2 v = *reinterpret_cast<const uint2*>(a.dh + (size_t)(m < M ? m : M - 1) * F + (f < F ? f : F - 4));
                 dv[r][j] = m < M && f < F ? v : make_uint2(0u, 0u);
             }
-    }
 #pragma unroll
-    for (int r = 0; r < P::MR; ++r) {
-        [[maybe_unused]] float top = 0.f;
+        for (int r = 0; r < P::MR; ++r) {
+            float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < HB; ++j) {
-            const int at = (16 * r + c) * kRow + kSize * (16 * (w * HB + j) + 4 * h);      // 4 columns of a row
-            f32x4 o0, o1;
+            for (int j = 0; j < HB; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float g = acc[r][j][e], u = acc[r][j + HB][e];
-                float slope;
-                const float pr = gate_prob<kAct>(g, &slope);
-                if constexpr (!kGrad) {
-                    o0[e] = g * pr * u;
-                } else {
+                for (int e = 0; e < 4; ++e) {
+                    const float g = acc[r][j][e], u = acc[r][j + HB][e];
                     const uint32_t dw = e < 2 ? dv[r][j].x : dv[r][j].y;
                     const float d = half_bits_to_f32<P::kBF16>(e & 1 ? dw >> 16 : dw & 0xFFFFu);
-                    o0[e] = d * u * fmaf(g, slope, pr);
-                    o1[e] = d * (g * pr);
-                    top = fmaxf(top, fmaxf(fabsf(o0[e]), fabsf(o1[e])));
+                    float slope;
+                    const float pr = gate_prob<kAct>(g, &slope);
+                    acc[r][j][e] = d * u * fmaf(g, slope, pr);
+                    acc[r][j + HB][e] = d * (g * pr);
+                    top = fmaxf(top, fmaxf(fabsf(acc[r][j][e]), fabsf(acc[r][j + HB][e])));
                 }
-            }
-            if constexpr (!kGrad) {
-                *reinterpret_cast<uint2*>(t0 + at) =
-                    make_uint2(pack2_rne<P::kBF16>(o0[0], o0[1]), pack2_rne<P::kBF16>(o0[2], o0[3]));
-            } else {
-                *reinterpret_cast<f32x4*>(t0 + at) = o0;
-                *reinterpret_cast<f32x4*>(t1 + at) = o1;
-            }
-        }
-        if constexpr (kGrad) {
             top = quarter_max(top);
             if (h == 0) red[w * BM + 16 * r + c] = top;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < P::MR; ++r) {
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < P::W; ++i) top = fmaxf(top, red[i * BM + 16 * r + c]);
+            const int m = m0 + 16 * r + c;
+            if (w == 0 && h == 0 && m < M) a.tops[(size_t)(f0 / BN) * M + m] = top;
+            const float by = power_of_two(scale_exponent(top, kGradTop));
+#pragma unroll
+            for (int j = 0; j < HB; ++j) {
+                const f32x4 o0 = acc[r][j] * by, o1 = acc[r][j + HB] * by;
+                *reinterpret_cast<uint2*>(t0 + place(r, j)) = make_uint2(pack2_rne<false>(o0[0], o0[1]), pack2_rne<false>(o0[2], o0[3]));
+                *reinterpret_cast<uint2*>(t1 + place(r, j)) = make_uint2(pack2_rne<false>(o1[0], o1[1]), pack2_rne<false>(o1[2], o1[3]));
+            }
         }
     }
     __syncthreads();
     for (int q = tid; q < BM * kChunks; q += P::kThreads) {
         const int row = q / kChunks, ch = q % kChunks;
-        const int m = m0 + row, f = f0 + 16 / kSize * ch;
+        const int m = m0 + row, f = f0 + 8 * ch;
         if (m >= M || f >= F) continue;
         const uint4 v = *reinterpret_cast<const uint4*>(t0 + row * kRow + 16 * ch);
         if constexpr (!kGrad) {
@@ -106,13 +121,6 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::S
         } else {
             *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + f) = v;
             *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + F + f) = *reinterpret_cast<const uint4*>(t1 + row * kRow + 16 * ch);
-        }
-    }
-    if constexpr (kGrad) {
-        if (tid < BM && m0 + tid < M) {
-            float top = red[tid];
-            for (int i = 1; i < P::W; ++i) top = fmaxf(top, red[i * BM + tid]);
-            a.tops[(size_t)(f0 / BN) * M + m0 + tid] = top;
         }
     }
 }
@@ -134,38 +142,75 @@ __global__ __launch_bounds__(P::kThreads) void gated_kernel(const GatedArgs a) {
 }
 
 // Workgroups 0 .. kScaleParts - 1: the weight's largest |scale|, a part each. The others: 16
-// rows each, 16 threads a row, their largest |d| over the column tiles.
+// rows each, 16 threads a row: their largest |d| over the column tiles, and what brings each
+// tile's values to the row's scale, two fp16 of one power of two.
+template <bool kBF16>
+__device__ __forceinline__ void scale_part(const uint32_t* __restrict__ meta, int64_t words, float* __restrict__ scale_max) {
+    __shared__ float wave_top[4];
+    const int tid = (int)threadIdx.x;
+    float top = 0.f;
+#pragma unroll 4
+    for (int64_t k = (int64_t)blockIdx.x * 256 + tid; 4 * k < words; k += kScaleParts * 256) {
+        const uint4 v = *reinterpret_cast<const uint4*>(meta + 4 * k);
+        for (const uint32_t q : {v.x, v.y, v.z, v.w}) top = fmaxf(top, fabsf(half_bits_to_f32<kBF16>(q & 0xFFFFu)));
+    }
+    for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+    if ((tid & 63) == 0) wave_top[tid >> 6] = top;
+    __syncthreads();
+    if (tid == 0) scale_max[blockIdx.x] = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+}
 template <bool kBF16>
 __global__ __launch_bounds__(256) void tops_kernel(const float* __restrict__ tops, int tiles, const uint32_t* __restrict__ meta,
                                                    int64_t words, int M, float* __restrict__ rowmax,
-                                                   float* __restrict__ scale_max) {
+                                                   uint32_t* __restrict__ factor, float* __restrict__ scale_max) {
+    if ((int)blockIdx.x < kScaleParts) {
+        scale_part<kBF16>(meta, words, scale_max);
+        return;
+    }
     __shared__ float red[16][17];
     const int tid = (int)threadIdx.x, i = tid & 15, g = tid >> 4;
+    const int m = ((int)blockIdx.x - kScaleParts) * 16 + i, mc = m < M ? m : M - 1;
     float top = 0.f;
-    if ((int)blockIdx.x < kScaleParts) {
 #pragma unroll 4
-        for (int64_t k = (int64_t)blockIdx.x * 256 + tid; 4 * k < words; k += kScaleParts * 256) {
-            const uint4 v = *reinterpret_cast<const uint4*>(meta + 4 * k);
-            for (const uint32_t q : {v.x, v.y, v.z, v.w}) top = fmaxf(top, fabsf(half_bits_to_f32<kBF16>(q & 0xFFFFu)));
-        }
-    } else {
-        const int m = ((int)blockIdx.x - kScaleParts) * 16 + i;
-#pragma unroll 4
-        for (int t = g; t < tiles; t += 16) top = fmaxf(top, tops[(size_t)t * M + (m < M ? m : M - 1)]);
-    }
+    for (int t = g; t < tiles; t += 16) top = fmaxf(top, tops[(size_t)t * M + mc]);
     red[g][i] = top;
     __syncthreads();
-    if ((int)blockIdx.x < kScaleParts) {
-        if (g == 0) {
-            for (int k = 1; k < 16; ++k) top = fmaxf(top, red[k][i]);
-            for (int s = 1; s < 16; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
-            if (i == 0) scale_max[blockIdx.x] = top;
-        }
-    } else if (g == 0) {
-        const int m = ((int)blockIdx.x - kScaleParts) * 16 + i;
-        for (int k = 1; k < 16; ++k) top = fmaxf(top, red[k][i]);
-        if (m < M) rowmax[m] = top;
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, red[k][i]);
+    if (m >= M) return;
+    if (g == 0) rowmax[m] = top;
+    const int row = scale_exponent(top, kGradTop);
+    for (int t = g; t < tiles; t += 16) {
+        const float own = tops[(size_t)t * M + m];
+        factor[(size_t)t * M + m] = own > 0.f ? 0x10001u * f32_to_half_bits<false>(power_of_two(row - scale_exponent(own, kGradTop))) : 0u;
     }
+}
+
+// The same after the small product, whose d is fp32: one row and 2048 of its values a
+// workgroup, rounded to fp16 at the row's scale.
+template <bool kBF16>
+__global__ __launch_bounds__(256) void convert_kernel(const float* __restrict__ tops, int tiles, const uint32_t* __restrict__ meta,
+                                                      int64_t words, int M, int N, const float* __restrict__ d32,
+                                                      float* __restrict__ rowmax, uint16_t* __restrict__ d,
+                                                      float* __restrict__ scale_max) {
+    if ((int)blockIdx.x < kScaleParts) {
+        scale_part<kBF16>(meta, words, scale_max);
+        return;
+    }
+    __shared__ float wave_top[4];
+    const int tid = (int)threadIdx.x;
+    const int m = ((int)blockIdx.x - kScaleParts) % M, n = 8 * ((((int)blockIdx.x - kScaleParts) / M) * 256 + tid);
+    float top = tid < tiles ? tops[(size_t)tid * M + m] : 0.f;            // tiles <= 256
+    for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+    if ((tid & 63) == 0) wave_top[tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+    if (tid == 0) rowmax[m] = top;
+    if (n >= N) return;
+    const float by = power_of_two(scale_exponent(top, kGradTop));
+    const f32x4* p = reinterpret_cast<const f32x4*>(d32 + (size_t)m * N + n);
+    const f32x4 lo = p[0] * by, hi = p[1] * by;
+    *reinterpret_cast<uint4*>(d + (size_t)m * N + n) = make_uint4(pack2_rne<false>(lo[0], lo[1]), pack2_rne<false>(lo[2], lo[3]),
+                                                                 pack2_rne<false>(hi[0], hi[1]), pack2_rne<false>(hi[2], hi[3]));
 }
 
 template <bool kBF16, int MR, int CBW, int kSub, bool kGrad>
@@ -241,13 +286,25 @@ int gated_tiles(int64_t M, int64_t K, int64_t F, int64_t G) {
     return small_product(M, K) ? small_workgroups(F / 8) : plan_product(M, K, 2 * F, G, true).tiles_n;
 }
 
-hipError_t launch_gated_tops(const float* tops, int tiles, const uint8_t* packed, int64_t M, int64_t K, int64_t N, int64_t G,
-                             bool bf16, float* rowmax, float* scale_max, hipStream_t stream) {
-    const uint32_t* meta = reinterpret_cast<const uint32_t*>(packed + (size_t)K * padded_cols(N) / 2);
-    const int64_t words = padded_cols(N) * padded_units(K, G);
-    const dim3 grid((unsigned)(kScaleParts + (M + 15) / 16)), block(256);
-    if (bf16) hipLaunchKernelGGL((tops_kernel<true>), grid, block, 0, stream, tops, tiles, meta, words, (int)M, rowmax, scale_max);
-    else hipLaunchKernelGGL((tops_kernel<false>), grid, block, 0, stream, tops, tiles, meta, words, (int)M, rowmax, scale_max);
+int gated_tile_columns(int64_t M, int64_t K, int64_t F, int64_t G) {
+    return small_product(M, K) ? 0 : 64 * plan_product(M, K, 2 * F, G, true).cbw;
+}
+
+hipError_t launch_gated_tops(const GatedCall& q, float* rowmax, uint32_t* factor, float* scale_max, hipStream_t stream) {
+    const int64_t N = 2 * q.F;
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(q.packed + (size_t)q.K * padded_cols(N) / 2);
+    const int64_t words = padded_cols(N) * padded_units(q.K, q.G);
+    const int tiles = gated_tiles(q.M, q.K, q.F, q.G);
+    const dim3 block(256);
+    if (small_product(q.M, q.K)) {
+        const dim3 grid((unsigned)(kScaleParts + q.M * ((N + 2047) / 2048)));
+        if (q.bf16) hipLaunchKernelGGL((convert_kernel<true>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, (int)N, q.d32, rowmax, q.d, scale_max);
+        else hipLaunchKernelGGL((convert_kernel<false>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, (int)N, q.d32, rowmax, q.d, scale_max);
+    } else {
+        const dim3 grid((unsigned)(kScaleParts + (q.M + 15) / 16));
+        if (q.bf16) hipLaunchKernelGGL((tops_kernel<true>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, rowmax, factor, scale_max);
+        else hipLaunchKernelGGL((tops_kernel<false>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, rowmax, factor, scale_max);
+    }
     return hipGetLastError();
 }
 

@@ -44,27 +44,18 @@ struct GradArgs {
     const float* factor;
     const float* before;
     int factor_stages;      // stages of one column of `factor`
-    const float* d32;
     const float* rowmax;
+    const uint32_t* tile_factor;
+    int tile_columns;
     const float* scale_max;
 };
 
-// Powers of two that bring fp32 gradients and the weights into fp16 (24 binades above the
-// last that is normal and 24 below its first value keep 11 bits of everything that counts
-// in a row): a row's largest |d| goes to [2^4, 2^5), the weight's largest |scale| to
-// [2^6, 2^7), so that 15 times it stays below 2^11. Exact, and taken off the result again.
-__device__ __forceinline__ int scale_exponent(float top, int to) {
-    if (!(top > 0.f) || top > 3e38f) return 0;
-    int e = to - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
-    return e < -100 ? -100 : e > 100 ? 100 : e;
-}
-__device__ __forceinline__ int row_exponent(const float* rowmax, int m) { return scale_exponent(rowmax[m], 4); }
+
 __device__ __forceinline__ int weight_exponent(const float* scale_max) {       // by every lane of a wave
     float top = scale_max[threadIdx.x & 63];
     for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-    return scale_exponent(top, 6);
+    return scale_exponent(top, kScaleTop);
 }
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // 8 codes -> 8 operand values (q - z) s in row order
 template <bool kOpBF16, bool kScaleBF16>
@@ -108,7 +99,7 @@ struct DecodeScaled : Dequant<false> {
 // (n % 8 in a half, all n / 8) evenly over 4 chunk pairs.
 __device__ __forceinline__ int swz(int n) { return (n & 7) ^ (2 * ((n >> 3) & 3)); }
 
-template <bool kOpBF16, bool kScaleBF16, int MR, int WM, int CK, int kSub, bool kD32>
+template <bool kOpBF16, bool kScaleBF16, int MR, int WM, int CK, int kSub, bool kScaled>
 __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     constexpr int WK = 8 / WM;
     constexpr int BM = 16 * MR * WM;
@@ -151,7 +142,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
 
     [[maybe_unused]] int we = 0;
     [[maybe_unused]] float wscale = 1.f;
-    if constexpr (kD32) {
+    if constexpr (kScaled) {
         we = weight_exponent(a.scale_max);
         wscale = power_of_two(we);
     }
@@ -174,7 +165,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         for (int i = 0; i < 4; ++i) {
             const uint32_t d = i == 0 ? code.x : i == 1 ? code.y : i == 2 ? code.z : code.w;
             uint4 v;
-            if constexpr (kD32) v = DecodeScaled<kScaleBF16>(md[(i * kSub) / 4], wscale)(d);
+            if constexpr (kScaled) v = DecodeScaled<kScaleBF16>(md[(i * kSub) / 4], wscale)(d);
             else v = Decode<kOpBF16, kScaleBF16>(md[(i * kSub) / 4])(d);
             ring[slot].w[row * 32 + ((16 * kbi + 4 * i + hh) ^ swz(row))] = v;
         }
@@ -207,29 +198,29 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         }
     };
 
-    // D in fp32: chunk q = tid + 512 i of the stage (row q / 8, 8 columns) through registers,
-    // one stage ahead, scaled by its row's power of two and rounded to fp16
-    constexpr int kChunks = kD32 ? (BM * 8 + 511) / 512 : 1;
-    [[maybe_unused]] f32x4 dv[kChunks][2];
-    [[maybe_unused]] float dscale[kChunks];
-    [[maybe_unused]] const float* drow[kChunks];
-    if constexpr (kD32) {
+    // Scaled D: chunk q = tid + 512 i of the stage (row q / 8, 8 columns) through registers,
+    // one stage ahead, times its tile's factor (a power of two, exact but for what falls
+    // below fp16's last place at the row's scale)
+    constexpr int kChunks = kScaled ? (BM * 8 + 511) / 512 : 1;
+    [[maybe_unused]] uint4 dv[kChunks];
+    [[maybe_unused]] uint32_t df[kChunks];
+    [[maybe_unused]] uint32_t drow[kChunks];
+    if constexpr (kScaled) {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             const int row = ((tid + 512 * i) >> 3) % BM;
-            const int m = m0 + row < a.M ? m0 + row : a.M - 1;
-            dscale[i] = power_of_two(row_exponent(a.rowmax, m));
-            drow[i] = a.d32 + (size_t)m * a.ld + 8 * (tid & 7);
+            drow[i] = (uint32_t)(m0 + row < a.M ? row : a.M - 1 - m0);
         }
     }
     auto load_d = [&](int t) {
+        // columns past the last (n % 8 == 0) read the last: their weights are zero
+        const int n = t * kStageN + 8 * (tid & 7) < a.n ? t * kStageN + 8 * (tid & 7) : a.n - 8;
+        const uint32_t* fac = nullptr;
+        if (a.tile_factor) fac = a.tile_factor + (size_t)((n < a.n / 2 ? n : n - a.n / 2) / a.tile_columns) * a.M + m0;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int n = t * kStageN + 8 * (tid & 7);
-            // columns past the last (n % 8 == 0) read the last and weigh zero: their weights do
-            const float* p = drow[i] + (n < a.n ? t * kStageN : a.n - 8 - 8 * (tid & 7));
-            dv[i][0] = *reinterpret_cast<const f32x4*>(p);
-            dv[i][1] = *reinterpret_cast<const f32x4*>(p + 4);
+            dv[i] = *reinterpret_cast<const uint4*>(dbase + 2 * ((size_t)drow[i] * a.ld + n));
+            df[i] = fac ? fac[drow[i]] : 0x3C003C00u;
         }
     };
     auto store_d = [&](int slot) {
@@ -238,9 +229,9 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
             const int q = tid + 512 * i;
             if (BM * 8 % 512 != 0 && q >= BM * 8) break;
             const int row = q >> 3, ch = q & 7;
-            const f32x4 lo = dv[i][0] * dscale[i], hi = dv[i][1] * dscale[i];
-            ring[slot].d[row * 8 + (ch ^ (row & 7))] = make_uint4(pack2_rne<false>(lo[0], lo[1]), pack2_rne<false>(lo[2], lo[3]),
-                                                                  pack2_rne<false>(hi[0], hi[1]), pack2_rne<false>(hi[2], hi[3]));
+            const f16x2 by = __builtin_bit_cast(f16x2, df[i]);
+            auto times = [&](uint32_t v) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) * by); };
+            ring[slot].d[row * 8 + (ch ^ (row & 7))] = make_uint4(times(dv[i].x), times(dv[i].y), times(dv[i].z), times(dv[i].w));
         }
     };
 
@@ -253,7 +244,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     const bool hot = a.hot && *a.hot != 0;
     if (st_lo < st_hi) {
         load_codes(st_lo);
-        if constexpr (kD32) {
+        if constexpr (kScaled) {
             load_d(st_lo);
             store_d(0);
         } else {
@@ -262,7 +253,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         store_codes(0);
         if (st_lo + 1 < st_hi) {
             load_codes(st_lo + 1);
-            if constexpr (kD32) load_d(st_lo + 1);
+            if constexpr (kScaled) load_d(st_lo + 1);
         }
     }
     for (int t = st_lo; t < st_hi; ++t) {
@@ -286,13 +277,13 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
             }
         }
         if (t + 1 < st_hi) {
-            if constexpr (kD32) store_d(slot ^ 1);
+            if constexpr (kScaled) store_d(slot ^ 1);
             else issue_d(slot ^ 1, t + 1);
             store_codes(slot ^ 1);
         }
         if (t + 2 < st_hi) {
             load_codes(t + 2);
-            if constexpr (kD32) load_d(t + 2);
+            if constexpr (kScaled) load_d(t + 2);
         }
         const Stage& st = ring[slot];
 #pragma unroll
@@ -341,8 +332,8 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
                 if (a.add) v += hot ? *o * a.before[m] : *o;
                 *o = v;
             } else {
-                if constexpr (kD32) {
-                    v *= power_of_two(-row_exponent(a.rowmax, m));
+                if constexpr (kScaled) {
+                    v *= power_of_two(-scale_exponent(a.rowmax[m], kGradTop));
                     v *= power_of_two(-we);
                 }
                 const uint2 o = make_uint2(pack2_rne<kScaleBF16>(v[0], v[1]), pack2_rne<kScaleBF16>(v[2], v[3]));
@@ -368,7 +359,7 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restric
         s1 += p[1];
     }
     if (rowmax) {
-        const float by = power_of_two(-row_exponent(rowmax, (int)(at / K))), by2 = power_of_two(-we);
+        const float by = power_of_two(-scale_exponent(rowmax[at / K], kGradTop)), by2 = power_of_two(-we);
         s0 = s0 * by * by2;
         s1 = s1 * by * by2;
     }
@@ -376,23 +367,23 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restric
                                                     pack2_rne<kBF16>(s1[0], s1[1]), pack2_rne<kBF16>(s1[2], s1[3]));
 }
 
-template <bool kOp, bool kSc, int kSub, bool kD32>
+template <bool kOp, bool kSc, int kSub, bool kScaled>
 void launch_sub(int bm, const GradArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.tiles_m * a.tiles_k * a.splits)), block(512);
-    if (bm == 16) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 1, 1, 2, kSub, kD32>), grid, block, 0, s, a);
-    else if (bm == 32) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 2, 1, 2, kSub, kD32>), grid, block, 0, s, a);
-    else if (bm == 64) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 1, 2, kSub, kD32>), grid, block, 0, s, a);
-    else if (bm == 128) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 2, 4, kSub, kD32>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((grad_kernel<kOp, kSc, 8, 2, 4, kSub, kD32>), grid, block, 0, s, a);
+    if (bm == 16) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 1, 1, 2, kSub, kScaled>), grid, block, 0, s, a);
+    else if (bm == 32) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 2, 1, 2, kSub, kScaled>), grid, block, 0, s, a);
+    else if (bm == 64) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 1, 2, kSub, kScaled>), grid, block, 0, s, a);
+    else if (bm == 128) hipLaunchKernelGGL((grad_kernel<kOp, kSc, 4, 2, 4, kSub, kScaled>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((grad_kernel<kOp, kSc, 8, 2, 4, kSub, kScaled>), grid, block, 0, s, a);
 }
 
-// operands: bf16 or fp16 as the scales, or fp16 from fp32
-template <bool kSc, bool kD32>
+// operands: bf16 or fp16 as the scales, or scaled fp16
+template <bool kSc, bool kScaled>
 void launch_typed(int bm, int sub, const GradArgs& a, hipStream_t s) {
-    constexpr bool kOp = kSc && !kD32;
-    if (sub == 4) launch_sub<kOp, kSc, 4, kD32>(bm, a, s);
-    else if (sub == 2) launch_sub<kOp, kSc, 2, kD32>(bm, a, s);
-    else launch_sub<kOp, kSc, 1, kD32>(bm, a, s);
+    constexpr bool kOp = kSc && !kScaled;
+    if (sub == 4) launch_sub<kOp, kSc, 4, kScaled>(bm, a, s);
+    else if (sub == 2) launch_sub<kOp, kSc, 2, kScaled>(bm, a, s);
+    else launch_sub<kOp, kSc, 1, kScaled>(bm, a, s);
 }
 
 }  // namespace
@@ -448,11 +439,12 @@ hipError_t launch_grad(const GradPlan& plan, const GradCall& q, hipStream_t stre
     a.before = q.before;
     a.factor_stages = q.factor_columns / kStageN;
     if ((plan.splits > 1 || !q.dx) && !q.part) return hipErrorInvalidValue;
-    a.d32 = q.d32;
     a.rowmax = q.rowmax;
+    a.tile_factor = q.tile_factor;
+    a.tile_columns = q.tile_columns;
     a.scale_max = q.scale_max;
     const int sub = units_per_block(q.G);
-    if (q.d32) {
+    if (q.scaled) {
         if (q.bf16) launch_typed<true, true>(plan.bm, sub, a, stream);
         else launch_typed<false, true>(plan.bm, sub, a, stream);
     } else {

@@ -119,14 +119,16 @@ struct ProductPlan {
 };
 ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gated);
 
-// Gated block: h = a(x Wg) (x Wu) when d is NULL; else d = [dg, du] fp32 [M, 2F] from dh.
+// Gated block: h = a(x Wg) (x Wu) when d is NULL; else d = [dg, du] [M, 2F] from dh, fp16,
+// each row of a column tile scaled by the power of two of its `tops`.
 // act: 0 silu, 1 gelu, 2 gelu's tanh form. counters / partials as plan_product asks.
 struct GatedCall {
     const uint16_t* x;
     const uint16_t* dh;
     const uint8_t* packed;
     uint16_t* h;
-    float* d;
+    uint16_t* d;
+    float* d32;            // what small_product shapes write instead
     float* tops;           // [gated_tiles(...)][M] largest |d| of a row in each share of the columns
     int64_t M, K, F, G;
     int act;
@@ -136,11 +138,12 @@ struct GatedCall {
 };
 hipError_t launch_gated(const GatedCall& call, hipStream_t stream);
 int gated_tiles(int64_t M, int64_t K, int64_t F, int64_t G);
-// Between a backward's products: the rows' largest |d| from `tops`, and the largest |scale|
-// of the weight in kScaleParts parts.
+int gated_tile_columns(int64_t M, int64_t K, int64_t F, int64_t G);       // 0: d's rows have one scale
+// Between a backward's products: the rows' largest |d| from `tops`, the factors [tile][M] (two
+// fp16) that bring the tiles to their row's scale, and the largest |scale| of the weight in
+// kScaleParts parts.
 constexpr int kScaleParts = 64;
-hipError_t launch_gated_tops(const float* tops, int tiles, const uint8_t* packed, int64_t M, int64_t K, int64_t N, int64_t G,
-                             bool bf16, float* rowmax, float* scale_max, hipStream_t stream);
+hipError_t launch_gated_tops(const GatedCall& call, float* rowmax, uint32_t* factor, float* scale_max, hipStream_t stream);
 
 // Up to 16 rows (csrc/product_small.hip): the gated block, and the head's statistics for
 // cross entropy: the labels' logits and (max, sum) per row and workgroup, part
@@ -170,10 +173,13 @@ struct GradCall {
     const float* factor;
     const float* before;
     int factor_columns;
-    // D in fp32 instead (d NULL, ld = n): its rows, scaled by powers of two from their
-    // largest values, and the weights, from the largest scale, both enter in fp16
-    const float* d32;
+    // `scaled`: D is fp16 at its rows' scales (rowmax), times tile_factor[tile][M] where that
+    // is not NULL, tile of tile_columns columns from 0 and from N / 2; the weights are taken
+    // in fp16, scaled from the largest |scale| (scale_max)
+    bool scaled;
     const float* rowmax;
+    const uint32_t* tile_factor;
+    int tile_columns;
     const float* scale_max;
 };
 struct GradPlan {
@@ -185,7 +191,7 @@ struct GradPlan {
 // `forced`: the sum comes in several calls, so partials are needed at any split.
 GradPlan plan_grad(int64_t M, int64_t K, int64_t n, bool forced);
 hipError_t launch_grad(const GradPlan& plan, const GradCall& call, hipStream_t stream);
-// dx[m, k] = sum_s part[s][m][k], rounded once (rowmax, scale_max: of a product with d32)
+// dx[m, k] = sum_s part[s][m][k], rounded once (rowmax, scale_max: of a `scaled` product)
 hipError_t launch_grad_finish(const float* part, int splits, int64_t M, int64_t K, uint16_t* dx, bool bf16,
                               const float* rowmax, const float* scale_max, hipStream_t stream);
 

@@ -35,7 +35,7 @@ struct SmallArgs {
     // gated
     uint16_t* h;
     const uint16_t* dh;
-    float* d;
+    float* d32;
     float* tops;            // [workgroups][M]
     int act;
     // cross entropy
@@ -192,11 +192,11 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
                 const size_t f = (size_t)8 * u + oc;
                 float slope;
                 const float pr = a.act == 0 ? gate_prob<0>(gv, &slope) : a.act == 1 ? gate_prob<1>(gv, &slope) : gate_prob<2>(gv, &slope);
-                if (a.d) {
+                if (a.d32) {
                     const float dv = half_bits_to_f32<kBF16>(a.dh[(size_t)m * a.F + f]);
                     const float dg = dv * uv * fmaf(gv, slope, pr), du = dv * (gv * pr);
-                    a.d[(size_t)m * 2 * a.F + f] = dg;
-                    a.d[(size_t)m * 2 * a.F + a.F + f] = du;
+                    a.d32[(size_t)m * 2 * a.F + f] = dg;
+                    a.d32[(size_t)m * 2 * a.F + a.F + f] = du;
                     most = fmaxf(most, fmaxf(fabsf(dg), fabsf(du)));
                 } else {
                     a.h[(size_t)m * a.F + f] = f32_to_half_bits<kBF16>(gv * pr * uv);
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
     }
     if constexpr (kGated) {
         static_assert(kRowStep >= 16, "a thread meets one row");
-        if (a.d) {
+        if (a.d32) {
 #pragma unroll
             for (int s = 1; s < kCols * S; s *= 2) most = fmaxf(most, __shfl_xor(most, s));
             if (oc == 0 && os == 0 && om < M) a.tops[(size_t)g * M + om] = most;
@@ -286,7 +286,7 @@ hipError_t launch_gated_small(const GatedCall& q, hipStream_t stream) {
     a.U = (int)(q.F / 8);
     a.h = q.h;
     a.dh = q.dh;
-    a.d = q.d;
+    a.d32 = q.d ? q.d32 : nullptr;
     a.tops = q.tops;
     a.act = q.act;
     launch_any<true>(a, units_per_block(q.G), q.bf16, small_workgroups(a.U), stream);
