@@ -52,8 +52,9 @@ typedef enum {
  * An unknown activation gives W4A16_ERR_PATH. x, h 16-byte aligned, not overlapping.
  *
  * w4a16_gated_grad is its backward to x: it forms both projections again from x and
- * returns dx = dg Wg^T + du Wu^T, dg = dh u a'(g), du = dh a(g); dg and du enter the
- * second product in bf16 for either dtype (fp16 has not their range). dh [M, F]. */
+ * returns dx = dg Wg^T + du Wu^T, dg = dh u a'(g), du = dh a(g). dg and du are rounded once
+ * to fp16 at a power of two of their row's largest value, and so are the weights at one of
+ * the largest scale. dh [M, F]. 8192 rows at a time. */
 size_t w4a16_gated_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t group_size, int grad);
 w4a16_status w4a16_gated(const void* x, const void* packed, size_t packed_bytes, w4a16_dtype dtype, void* h, int64_t M,
                          int64_t K, int64_t F, int64_t group_size, w4a16_act act, void* workspace,
@@ -69,8 +70,9 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
  *   dloss   fp32 [M] or NULL (1). Read only when dx is given.
  *   loss, lse  fp32 [M], written in full.
  *   dx      [M, K] `dtype`, written in full, or NULL: no gradient. 16-byte aligned.
- * The vocabulary is taken in pieces: the largest buffer is q - p of one piece (at most
- * 256 MiB, 4096 rows at a time). No pointer may overlap another that is written. */
+ * The vocabulary is taken in pieces: the largest buffer holds the unnormalised
+ * probabilities of one piece (`dtype`, at most 256 MiB, 4096 rows at a time). The target
+ * columns' part of dx is taken in fp32. No pointer may overlap another that is written. */
 size_t w4a16_cross_entropy_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t group_size, int grad);
 w4a16_status w4a16_cross_entropy(const void* x, const int32_t* labels, const void* packed, size_t packed_bytes,
                                  w4a16_dtype dtype, int64_t M, int64_t K, int64_t V, int64_t group_size,

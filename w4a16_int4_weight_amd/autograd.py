@@ -1,0 +1,105 @@
+"""The operators on frozen packed int4 weights as differentiable torch operations.
+
+  linear(x, packed, N, group_size, bias)                    -> y = x W (+ bias)
+  gated(x, packed, F, group_size, act)                      -> h = a(x Wg) * (x Wu)
+  cross_entropy(x, labels, packed, V, group_size, weights)  -> weights[m] * loss[m]
+  distill(x, top_ids, top_logits, packed, V, group_size, temperature, weights)
+
+Gradients go to x alone: the weights, a bias and a teacher's logits are constants. x is
+fp16 or bf16, [..., K]; a dimension of any size is met as rows. Each call runs on the
+current stream, like the functions it is made of.
+
+The losses form x's gradient in the forward pass, where the head is read for the loss
+anyway, scaled by `weights` (float32 per row; None: 1). Give the rows' weights there
+(1 / count for a mean, a loss scale for fp16) and sum what comes back: the backward pass
+then multiplies by one, which is exact. Another factor on a row is one more rounding.
+"""
+
+import torch
+
+from . import w4a16_cross_entropy, w4a16_distill, w4a16_gated, w4a16_gated_grad, w4a16_gemm, w4a16_gemm_grad
+
+__all__ = ["linear", "gated", "cross_entropy", "distill"]
+
+
+def _flat(x):
+    return x.reshape(-1, x.shape[-1]).contiguous()
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, packed, N, group_size, bias):
+        ctx.save_for_backward(packed)
+        ctx.shape, ctx.group_size = x.shape, group_size
+        return w4a16_gemm(_flat(x), packed, N, group_size, bias=bias).view(*x.shape[:-1], N)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        packed, = ctx.saved_tensors
+        dx = w4a16_gemm_grad(_flat(dy), packed, ctx.shape[-1], ctx.group_size)
+        return dx.view(ctx.shape), None, None, None, None
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, packed, F, group_size, act):
+        flat = _flat(x)
+        ctx.save_for_backward(flat, packed)
+        ctx.shape, ctx.args = x.shape, (F, group_size, act)
+        return w4a16_gated(flat, packed, F, group_size, act=act).view(*x.shape[:-1], F)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        flat, packed = ctx.saved_tensors
+        F, group_size, act = ctx.args
+        dx = w4a16_gated_grad(flat, _flat(dh), packed, F, group_size, act=act)
+        return dx.view(ctx.shape), None, None, None, None
+
+
+class _Loss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weights, call):
+        flat = _flat(x)
+        grad = ctx.needs_input_grad[0]
+        if weights is not None:
+            weights = weights.reshape(-1).contiguous()
+        out = call(flat, grad, weights if grad else None)
+        ctx.shape = x.shape
+        if grad:
+            ctx.save_for_backward(out[2])
+        loss = out[0] if weights is None else out[0] * weights
+        return loss.view(x.shape[:-1])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        dx, = ctx.saved_tensors
+        return (dx.float() * g.reshape(-1, 1)).to(dx.dtype).view(ctx.shape), None, None
+
+
+def linear(x, packed, N, group_size=128, bias=None):
+    """w4a16_gemm, with w4a16_gemm_grad as its backward pass."""
+    return _Linear.apply(x, packed, N, group_size, bias)
+
+
+def gated(x, packed, F, group_size=128, act="silu"):
+    """w4a16_gated, with w4a16_gated_grad as its backward pass (x is kept, not g and u)."""
+    return _Gated.apply(x, packed, F, group_size, act)
+
+
+def cross_entropy(x, labels, packed, V, group_size=128, weights=None):
+    """w4a16_cross_entropy: weights[m] * loss[m], float32, shaped like labels. labels int32;
+    a label outside [0, V) has loss and gradient 0."""
+    def call(flat, grad, dloss):
+        return w4a16_cross_entropy(flat, labels.reshape(-1).contiguous(), packed, V, group_size, dloss=dloss, grad=grad)
+    return _Loss.apply(x, weights, call)
+
+
+def distill(x, top_ids, top_logits, packed, V, group_size=128, temperature=1.0, weights=None):
+    """w4a16_distill: weights[m] * loss[m], float32. top_ids, top_logits [..., T]."""
+    def call(flat, grad, dloss):
+        return w4a16_distill(flat, _flat(top_ids), _flat(top_logits), packed, V, group_size, temperature=temperature,
+                             dloss=dloss, grad=grad)
+    return _Loss.apply(x, weights, call)
