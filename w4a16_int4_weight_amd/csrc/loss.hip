@@ -162,36 +162,59 @@ __global__ __launch_bounds__(P::kThreads) void loss_kernel(const LossArgs a) {
     loss_epilogue<P, P::kBF16 || !kProb, kProb>(a, sh, m_tile * P::BM, n_tile, acc);
 }
 
-// One wave: x . W_id in fp32, (q - z) s exactly. Lane: row block lane / 4 (+ 16, ...), rows
-// 8 (lane % 4) + 32 i of it.
-template <bool kBF16>
-__device__ __forceinline__ float column_dot(const uint16_t* __restrict__ x, const uint8_t* __restrict__ packed, int K, int Np,
-                                            int UW, int sub, int id, int lane) {
+// One wave: x . W_id of kCols columns in fp32, (q - z) s exactly. Lane: row block lane / 4
+// (+ 16, ...), rows 8 (lane % 4) + 32 i of it. Several columns at a time share the loads of
+// x and hide each other's latency.
+template <bool kBF16, int kCols>
+__device__ __forceinline__ void column_dots(const uint16_t* __restrict__ x, const uint8_t* __restrict__ packed, int K, int Np,
+                                            int UW, int sub, const int (&id)[kCols], int lane, float (&total)[kCols]) {
     const int KB = K / kRowsPerBlock;
     const int h = lane & 3;
-    const uint8_t* codes = packed + (size_t)(id >> 4) * KB * kBlockBytes + 16 * (16 * h + (id & 15));
-    const uint32_t* meta = reinterpret_cast<const uint32_t*>(packed + (size_t)K * Np / 2) + (size_t)id * UW;
-    float total = 0.f;
+    const uint8_t* codes[kCols];
+    const uint32_t* meta[kCols];
+#pragma unroll
+    for (int n = 0; n < kCols; ++n) {
+        codes[n] = packed + (size_t)(id[n] >> 4) * KB * kBlockBytes + 16 * (16 * h + (id[n] & 15));
+        meta[n] = reinterpret_cast<const uint32_t*>(packed + (size_t)K * Np / 2) + (size_t)id[n] * UW;
+        total[n] = 0.f;
+    }
     for (int kb = lane >> 2; kb < KB; kb += 16) {
-        const uint4 q = *reinterpret_cast<const uint4*>(codes + (size_t)kb * kBlockBytes);
+        uint4 q[kCols];
+        uint32_t md[kCols][4];
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) {
+            q[n] = *reinterpret_cast<const uint4*>(codes[n] + (size_t)kb * kBlockBytes);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) md[n][i] = meta[n][kb * sub + ((i * sub) >> 2)];
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t md = meta[kb * sub + ((i * sub) >> 2)];
             const uint4 xv = *reinterpret_cast<const uint4*>(x + (size_t)kb * kRowsPerBlock + 32 * i + 8 * h);
-            const uint32_t d = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
-            const float z = (float)((md >> 16) & 0xFu);
-            float a = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t xp = e == 0 ? xv.x : e == 1 ? xv.y : e == 2 ? xv.z : xv.w;
-                a = fmaf(half_bits_to_f32<kBF16>(xp & 0xFFFFu), (float)((d >> (4 * e)) & 0xFu) - z, a);
-                a = fmaf(half_bits_to_f32<kBF16>(xp >> 16), (float)((d >> (4 * e + 16)) & 0xFu) - z, a);
+            for (int n = 0; n < kCols; ++n) {
+                const uint32_t d = i == 0 ? q[n].x : i == 1 ? q[n].y : i == 2 ? q[n].z : q[n].w;
+                const float z = (float)((md[n][i] >> 16) & 0xFu);
+                float a = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t xp = e == 0 ? xv.x : e == 1 ? xv.y : e == 2 ? xv.z : xv.w;
+                    a = fmaf(half_bits_to_f32<kBF16>(xp & 0xFFFFu), (float)((d >> (4 * e)) & 0xFu) - z, a);
+                    a = fmaf(half_bits_to_f32<kBF16>(xp >> 16), (float)((d >> (4 * e + 16)) & 0xFu) - z, a);
+                }
+                total[n] = fmaf(half_bits_to_f32<kBF16>(md[n][i] & 0xFFFFu), a, total[n]);
             }
-            total = fmaf(half_bits_to_f32<kBF16>(md & 0xFFFFu), a, total);
         }
     }
-    for (int s = 32; s > 0; s >>= 1) total += __shfl_xor(total, s);
-    return total;
+    for (int s = 32; s > 0; s >>= 1)
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) total[n] += __shfl_xor(total[n], s);
+}
+template <bool kBF16>
+__device__ __forceinline__ float column_dot(const uint16_t* x, const uint8_t* packed, int K, int Np, int UW, int sub, int id, int lane) {
+    const int ids[1] = {id};
+    float total[1];
+    column_dots<kBF16, 1>(x, packed, K, Np, UW, sub, ids, lane, total);
+    return total[0];
 }
 
 constexpr int kMaxTargets = 256;
@@ -282,12 +305,19 @@ __global__ __launch_bounds__(256) void targets_kernel(const TargetArgs a) {
     __syncthreads();
     const uint16_t* x = a.x + (size_t)m * a.K;
     float top = -INFINITY;
-    for (int j = w; j < T; j += 4) {
-        const int id = first_id[j];
-        if (id < 0) continue;
-        const float z = a.inv_tau * column_dot<kBF16>(x, a.packed, a.K, (int)padded_cols(a.N), a.UW, a.sub, id, lane);
-        if (lane == 0) a.zsel[(size_t)m * T + j] = z;
-        top = fmaxf(top, z);
+    for (int j0 = 4 * w; j0 < T; j0 += 16) {
+        int id[4];
+        float z[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) id[n] = j0 + n < T && first_id[j0 + n] >= 0 ? first_id[j0 + n] : 0;
+        column_dots<kBF16, 4>(x, a.packed, a.K, (int)padded_cols(a.N), a.UW, a.sub, id, lane, z);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if (j0 + n >= T || first_id[j0 + n] < 0) continue;
+            z[n] *= a.inv_tau;
+            if (lane == 0) a.zsel[(size_t)m * T + j0 + n] = z[n];
+            top = fmaxf(top, z[n]);
+        }
     }
     if (lane == 0) wave_top[w] = top;
     __syncthreads();
@@ -398,7 +428,8 @@ __global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
 }
 
 // dx[m] = gain[m] sum_s part[s][m] + sum_j coef[m] (q_j - p_j) W[:, id_j], one rounding. A
-// workgroup takes 2048 elements of a row, 8 a thread: one code word per target.
+// thread takes 8 elements of a row (one code word per target); where there are many splits
+// and targets, kShare threads share them and their sums meet in LDS, in a fixed order.
 struct FinishArgs {
     const float* part;
     int splits, M, K, N, T, UW, sub;
@@ -407,12 +438,15 @@ struct FinishArgs {
     const int32_t* ids;
     uint16_t* dx;
 };
-template <bool kBF16>
+template <bool kBF16, int kShare>
 __global__ __launch_bounds__(256) void finish_kernel(const FinishArgs a) {
+    constexpr int kWide = 256 / kShare;                    // threads along a row
     __shared__ int sid[kMaxTargets];
     __shared__ float sc[kMaxTargets];
+    __shared__ float sums[kShare > 1 ? kShare : 1][kShare > 1 ? kWide * 8 + 4 : 1];
     const int m = (int)blockIdx.x, tid = (int)threadIdx.x;
-    const int k0 = 8 * ((int)blockIdx.y * 256 + tid);
+    const int g = tid / kWide, at = tid % kWide;
+    const int k0 = 8 * ((int)blockIdx.y * kWide + at);
     const float coef = a.coef[m], gain = a.gain[m];
     for (int j = tid; j < a.T; j += 256) {
         const int id = a.ids[(size_t)m * a.T + j];
@@ -422,17 +456,16 @@ __global__ __launch_bounds__(256) void finish_kernel(const FinishArgs a) {
                    : 0.f;
     }
     __syncthreads();
-    if (k0 >= a.K) return;
-    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-    if (coef != 0.f) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (k0 < a.K && coef != 0.f) {
         f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
         const size_t MK = (size_t)a.M * a.K;
         const float* p = a.part + (size_t)m * a.K + k0;
-        for (int s = 0; s < a.splits; ++s, p += MK) {
-            s0 += *reinterpret_cast<const f32x4*>(p);
-            s1 += *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll 4
+        for (int s = g; s < a.splits; s += kShare) {
+            s0 += *reinterpret_cast<const f32x4*>(p + s * MK);
+            s1 += *reinterpret_cast<const f32x4*>(p + s * MK + 4);
         }
-        float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[e] = s0[e] * gain;
@@ -442,8 +475,8 @@ __global__ __launch_bounds__(256) void finish_kernel(const FinishArgs a) {
         const uint8_t* codes = a.packed + (size_t)kb * kBlockBytes + 256 * h + 4 * i;
         const uint32_t* meta = reinterpret_cast<const uint32_t*>(a.packed + (size_t)a.K * padded_cols(a.N) / 2) + kb * a.sub +
                                ((i * a.sub) >> 2);
-#pragma unroll 4
-        for (int j = 0; j < a.T; ++j) {
+#pragma unroll 8
+        for (int j = g; j < a.T; j += kShare) {
             const int id = sid[j];
             const float cf = sc[j];
             const uint32_t d = *reinterpret_cast<const uint32_t*>(codes + (size_t)(id >> 4) * KB * kBlockBytes + 16 * (id & 15));
@@ -453,10 +486,22 @@ __global__ __launch_bounds__(256) void finish_kernel(const FinishArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[tile_row_of_slot(e)] = fmaf((float)((d >> (4 * e)) & 0xFu) - z, s, v[tile_row_of_slot(e)]);
         }
-        o = make_uint4(pack2_rne<kBF16>(v[0], v[1]), pack2_rne<kBF16>(v[2], v[3]), pack2_rne<kBF16>(v[4], v[5]),
+    }
+    if constexpr (kShare > 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[g][8 * at + e] = v[e];
+        __syncthreads();
+        static_assert(kShare == 8, "a thread sums one element");
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) t += sums[i][tid];
+        const int k = (int)blockIdx.y * kWide * 8 + tid;
+        if (k < a.K) a.dx[(size_t)m * a.K + k] = f32_to_half_bits<kBF16>(t);
+    } else if (k0 < a.K) {
+        *reinterpret_cast<uint4*>(a.dx + (size_t)m * a.K + k0) =
+            make_uint4(pack2_rne<kBF16>(v[0], v[1]), pack2_rne<kBF16>(v[2], v[3]), pack2_rne<kBF16>(v[4], v[5]),
                        pack2_rne<kBF16>(v[6], v[7]));
     }
-    *reinterpret_cast<uint4*>(a.dx + (size_t)m * a.K + k0) = o;
 }
 
 template <bool kBF16, int MR, int CBW, int kSub, bool kProb>
@@ -715,9 +760,18 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
         f.weight = t.weight;
         f.ids = ids;
         f.dx = q.dx + r0 * q.K;
-        const dim3 finish_grid((unsigned)M, (unsigned)((q.K + 2047) / 2048));
-        if (q.bf16) hipLaunchKernelGGL((finish_kernel<true>), finish_grid, dim3(256), 0, stream, f);
-        else hipLaunchKernelGGL((finish_kernel<false>), finish_grid, dim3(256), 0, stream, f);
+        // shared where a thread alone would meet 16 loads or more (65 rows, 20 targets, 64
+        // splits: 24 -> 6.6 us; 1024 rows, 64 targets: 83 -> 80 us, bound by the lines the
+        // columns' codes lie in), else one thread each (4096 rows, 1 target, 2 splits: 18 us)
+        const bool share = f.splits + f.T >= 16;
+        const dim3 finish_grid((unsigned)M, (unsigned)(share ? (q.K + 255) / 256 : (q.K + 2047) / 2048));
+        if (q.bf16) {
+            if (share) hipLaunchKernelGGL((finish_kernel<true, 8>), finish_grid, dim3(256), 0, stream, f);
+            else hipLaunchKernelGGL((finish_kernel<true, 1>), finish_grid, dim3(256), 0, stream, f);
+        } else {
+            if (share) hipLaunchKernelGGL((finish_kernel<false, 8>), finish_grid, dim3(256), 0, stream, f);
+            else hipLaunchKernelGGL((finish_kernel<false, 1>), finish_grid, dim3(256), 0, stream, f);
+        }
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
