@@ -15,7 +15,9 @@
 // Workgroup: a tile of BM rows x 256 columns of dx, 8 waves as WM x WK. A stage is 64
 // columns of W: D's rows by direct global -> LDS copies (16-byte chunks XOR-swizzled by
 // row), the codes through registers one stage ahead; two stages alternate, and the next
-// one is decoded between the products of the current one. Small M, or few tiles: the sum
+// one is decoded between the products of the current one. Tiles of up to 128 rows, which
+// run few stages, take both through registers and four stages ahead, so that a memory
+// latency is paid once and not each stage. Small M, or few tiles: the sum
 // is split over workgroups into fp32 partial tiles, added in split order by a second
 // kernel (the result does not depend on the order of arrival).
 #include "device_common.h"
@@ -105,6 +107,9 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     constexpr int BM = 16 * MR * WM;
     static_assert(16 * CK * WK == kTileK, "the waves cover the tile's columns");
     constexpr int kSlabs = BM / 8;                    // 1 KiB slabs (8 rows) of the D stage
+    // D through registers (else by direct copies), and stages on their way in registers
+    constexpr bool kRegs = kScaled || BM <= 128;
+    constexpr int kDepth = BM <= 128 ? 4 : 1;
     struct Stage {
         uint4 d[BM * 8];
         uint4 w[kStageN * 32];
@@ -147,31 +152,36 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         we = weight_exponent(a.scale_max);
         wscale = power_of_two(we);
     }
-    uint4 code;
-    uint32_t md[kSub];
-    auto load_codes = [&](int t) {
+    constexpr int kChunks = kRegs ? (BM * 8 + 511) / 512 : 1;
+    struct Fetch {                                    // what a thread holds of a stage
+        uint4 code;
+        uint32_t md[kSub];
+        uint4 dv[kChunks];                            // chunk tid + 512 i of D (row / 8, 8 columns)
+        uint32_t df[kChunks];
+    };
+    Fetch fetch[kDepth];
+    auto load_codes = [&](Fetch& x, int t) {
         const int n = a.n0 + t * kStageN + 16 * nbi + cc;
         const int nb = n / kColsPerBlock < NB ? n / kColsPerBlock : NB - 1;
-        code = *reinterpret_cast<const uint4*>(a.packed + ((size_t)nb * a.KB + kbc) * kBlockBytes + 16 * (16 * hh + cc));
+        x.code = *reinterpret_cast<const uint4*>(a.packed + ((size_t)nb * a.KB + kbc) * kBlockBytes + 16 * (16 * hh + cc));
 #pragma unroll
-        for (int u = 0; u < kSub; ++u) {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(
-                meta + 4 * ((size_t)(nb * kColsPerBlock + cc) * a.UW + kbc * kSub + u));
-            md[u] = n < a.n0 + a.n ? v : 0u;          // columns past the call's weigh zero
-        }
+        for (int u = 0; u < kSub; ++u)
+            x.md[u] = *reinterpret_cast<const uint32_t*>(meta + 4 * ((size_t)(nb * kColsPerBlock + cc) * a.UW + kbc * kSub + u));
     };
-    auto store_codes = [&](int slot) {
+    auto store_codes = [&](const Fetch& x, int slot, int t) {
         const int row = 16 * nbi + cc;
+        const bool in = t * kStageN + row < a.n;      // columns past the call's weigh zero
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t d = i == 0 ? code.x : i == 1 ? code.y : i == 2 ? code.z : code.w;
+            const uint32_t d = i == 0 ? x.code.x : i == 1 ? x.code.y : i == 2 ? x.code.z : x.code.w;
+            const uint32_t md = in ? x.md[(i * kSub) / 4] : 0u;
             uint4 v;
-            if constexpr (kScaled) v = DecodeScaled<kScaleBF16>(md[(i * kSub) / 4], wscale)(d);
-            else v = Decode<kOpBF16, kScaleBF16>(md[(i * kSub) / 4])(d);
+            if constexpr (kScaled) v = DecodeScaled<kScaleBF16>(md, wscale)(d);
+            else v = Decode<kOpBF16, kScaleBF16>(md)(d);
             ring[slot].w[row * 32 + ((16 * kbi + 4 * i + hh) ^ swz(row))] = v;
         }
     };
-    // D rows m0 + 8 slab + lane / 8, 16-byte chunk (lane % 8) ^ (row % 8). Rows past M read
+    // Direct copies: D rows m0 + 8 slab + lane / 8, 16-byte chunk (lane % 8) ^ (row % 8). Rows past M read
     // row M - 1. A stage that ends past the call's columns is read with a test per chunk
     // instead (n % 8 == 0), zero outside: what lies there may be no number.
     const uint8_t* dbase = uniform_ptr(a.d + (size_t)m0 * a.ld);
@@ -199,40 +209,51 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         }
     };
 
-    // Scaled D: chunk q = tid + 512 i of the stage (row q / 8, 8 columns) through registers,
-    // one stage ahead, times its tile's factor (a power of two, exact but for what falls
-    // below fp16's last place at the row's scale)
-    constexpr int kChunks = kScaled ? (BM * 8 + 511) / 512 : 1;
-    [[maybe_unused]] uint4 dv[kChunks];
-    [[maybe_unused]] uint32_t df[kChunks];
+    // Through registers. Scaled D is multiplied by its tile's factor on the way (a power of
+    // two, exact but for what falls below fp16's last place at the row's scale).
     [[maybe_unused]] uint32_t drow[kChunks];
-    if constexpr (kScaled) {
+    if constexpr (kRegs) {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             const int row = ((tid + 512 * i) >> 3) % BM;
             drow[i] = (uint32_t)(m0 + row < a.M ? row : a.M - 1 - m0);
         }
     }
-    auto load_d = [&](int t) {
-        // columns past the last (n % 8 == 0) read the last: their weights are zero
-        const int n = t * kStageN + 8 * (tid & 7) < a.n ? t * kStageN + 8 * (tid & 7) : a.n - 8;
+    const bool hot = a.hot && *a.hot != 0;
+    auto load_d = [&](Fetch& x, int t) {
+        const int n = t * kStageN + 8 * (tid & 7) < a.n ? t * kStageN + 8 * (tid & 7) : a.n - 8;      // n % 8 == 0
         const uint32_t* fac = nullptr;
-        if (a.tile_factor) fac = a.tile_factor + (size_t)((n < a.n / 2 ? n : n - a.n / 2) / a.tile_columns) * a.M + m0;
+        if constexpr (kScaled) {
+            if (a.tile_factor) fac = a.tile_factor + (size_t)((n < a.n / 2 ? n : n - a.n / 2) / a.tile_columns) * a.M + m0;
+        }
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            dv[i] = *reinterpret_cast<const uint4*>(dbase + 2 * ((size_t)drow[i] * a.ld + n));
-            df[i] = fac ? fac[drow[i]] : 0x3C003C00u;
+            x.dv[i] = *reinterpret_cast<const uint4*>(dbase + 2 * ((size_t)drow[i] * a.ld + n));
+            if constexpr (kScaled) x.df[i] = fac ? fac[drow[i]] : 0x3C003C00u;
         }
     };
-    auto store_d = [&](int slot) {
+    auto bf16_times = [](uint32_t p, float by) {
+        return pack2_rne<true>(bf16_bits_to_f32(p & 0xFFFFu) * by, bf16_bits_to_f32(p >> 16) * by);
+    };
+    auto store_d = [&](const Fetch& x, int slot, int t) {
+        const bool in = t * kStageN + 8 * (tid & 7) < a.n;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             const int q = tid + 512 * i;
             if (BM * 8 % 512 != 0 && q >= BM * 8) break;
             const int row = q >> 3, ch = q & 7;
-            const f16x2 by = __builtin_bit_cast(f16x2, df[i]);
-            auto times = [&](uint32_t v) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) * by); };
-            ring[slot].d[row * 8 + (ch ^ (row & 7))] = make_uint4(times(dv[i].x), times(dv[i].y), times(dv[i].z), times(dv[i].w));
+            uint4 v = x.dv[i];
+            if constexpr (kScaled) {
+                const f16x2 by = __builtin_bit_cast(f16x2, x.df[i]);
+                auto times = [&](uint32_t p) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) * by); };
+                v = make_uint4(times(v.x), times(v.y), times(v.z), times(v.w));
+            } else if constexpr (kOpBF16) {
+                if (hot) {
+                    const float by = a.factor[(size_t)(t / a.factor_stages) * a.M + m0 + drow[i]];
+                    v = make_uint4(bf16_times(v.x, by), bf16_times(v.y, by), bf16_times(v.z, by), bf16_times(v.w, by));
+                }
+            }
+            ring[slot].d[row * 8 + (ch ^ (row & 7))] = in ? v : make_uint4(0u, 0u, 0u, 0u);
         }
     };
 
@@ -242,50 +263,35 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
 #pragma unroll
         for (int j = 0; j < CK; ++j) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const bool hot = a.hot && *a.hot != 0;
-    if (st_lo < st_hi) {
-        load_codes(st_lo);
-        if constexpr (kScaled) {
-            load_d(st_lo);
-            store_d(0);
-        } else {
-            issue_d(0, st_lo);
-        }
-        store_codes(0);
-        if (st_lo + 1 < st_hi) {
-            load_codes(st_lo + 1);
-            if constexpr (kScaled) load_d(st_lo + 1);
-        }
-    }
-    for (int t = st_lo; t < st_hi; ++t) {
+    auto load = [&](Fetch& x, int t) {
+        load_codes(x, t);
+        if constexpr (kRegs) load_d(x, t);
+    };
+    auto store = [&](const Fetch& x, int slot, int t) {
+        if constexpr (kRegs) store_d(x, slot, t);
+        else issue_d(slot, t);
+        store_codes(x, slot, t);
+    };
+    // one stage; `next` holds stage t + 1 and takes stage t + 1 + kDepth
+    auto stage = [&](int t, Fetch& next) {
         const int slot = (t - st_lo) & 1;
-        wait_vmcnt<0>();                  // this wave's copies of stage t, and its codes of t + 1
+        if constexpr (!kRegs) wait_vmcnt<0>();        // this wave's copies of stage t
         wait_lgkmcnt0();                  // its decoded rows of stage t are written
         lds_barrier();                    // everyone's; and everyone has read stage t - 1
-        if constexpr (kOpBF16) {
+        if constexpr (kOpBF16 && !kRegs) {
             if (hot) {
                 const float* fac = a.factor + (size_t)(t / a.factor_stages) * a.M;
                 for (int q = tid; q < BM * 8; q += 512) {
                     const int row = q >> 3;
-                    const float fr = fac[m0 + row < a.M ? m0 + row : a.M - 1];
-                    uint4 v = ring[slot].d[q];
-                    auto times = [&](uint32_t p) {
-                        return pack2_rne<true>(bf16_bits_to_f32(p & 0xFFFFu) * fr, bf16_bits_to_f32(p >> 16) * fr);
-                    };
-                    ring[slot].d[q] = make_uint4(times(v.x), times(v.y), times(v.z), times(v.w));
+                    const float by = fac[m0 + row < a.M ? m0 + row : a.M - 1];
+                    const uint4 v = ring[slot].d[q];
+                    ring[slot].d[q] = make_uint4(bf16_times(v.x, by), bf16_times(v.y, by), bf16_times(v.z, by), bf16_times(v.w, by));
                 }
                 __syncthreads();
             }
         }
-        if (t + 1 < st_hi) {
-            if constexpr (kScaled) store_d(slot ^ 1);
-            else issue_d(slot ^ 1, t + 1);
-            store_codes(slot ^ 1);
-        }
-        if (t + 2 < st_hi) {
-            load_codes(t + 2);
-            if constexpr (kScaled) load_d(t + 2);
-        }
+        if (t + 1 < st_hi) store(next, slot ^ 1, t + 1);
+        if (t + 1 + kDepth < st_hi) load(next, t + 1 + kDepth);
         const Stage& st = ring[slot];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -317,6 +323,18 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
 #pragma unroll
                 for (int j = 0; j < CK; ++j) acc[r][j] = mfma16x16x32<kOpBF16>(b[j], f[r], acc[r][j]);
         }
+    };
+    if (st_lo < st_hi) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u)
+            if (st_lo + u < st_hi) load(fetch[u], st_lo + u);
+        store(fetch[0], 0, st_lo);
+        if (st_lo + kDepth < st_hi) load(fetch[0], st_lo + kDepth);
+    }
+    for (int t = st_lo; t < st_hi; t += kDepth) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u)
+            if (t + u < st_hi) stage(t + u, fetch[(u + 1) % kDepth]);
     }
 
 #pragma unroll
