@@ -63,7 +63,7 @@ w4a16_status check_gated(int64_t M, int64_t K, int64_t F, int64_t group_size, in
 }
 
 struct GatedLayout {
-    size_t partials, tops, rowmax, factor, scale_max, d, d32, gpart, end;
+    size_t partials, tops, rowmax, factor, scale_max, d, d_rest, d32, gpart, end;
 };
 
 // one pass over M rows: the forward's K-split partials and, for the gradient, dg | du and
@@ -84,6 +84,8 @@ GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) 
         at += round256(w4a16::kScaleParts * 4);
         l.d = at;
         at += round256((size_t)M * 4 * F);
+        l.d_rest = at;                    // (fp16; one size for both types)
+        if (w4a16::grad_takes_rest(w4a16::plan_grad(M, K, 2 * F, false), false)) at += round256((size_t)M * 4 * F);
         l.d32 = at;
         if (w4a16::small_product(M, K)) at += round256((size_t)M * 8 * F);
         l.gpart = at;
@@ -271,6 +273,8 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         q.dh = static_cast<const uint16_t*>(dh) + r0 * F;
         q.packed = static_cast<const uint8_t*>(packed);
         q.d = reinterpret_cast<uint16_t*>(ws + l.d);
+        const w4a16::GradPlan plan = w4a16::plan_grad(rows, K, 2 * F, false);
+        if (w4a16::grad_takes_rest(plan, bf16)) q.d_rest = reinterpret_cast<uint16_t*>(ws + l.d_rest);
         q.d32 = reinterpret_cast<float*>(ws + l.d32);
         q.tops = reinterpret_cast<float*>(ws + l.tops);
         float* rowmax = reinterpret_cast<float*>(ws + l.rowmax);
@@ -287,12 +291,12 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         if (err == hipSuccess)
             err = w4a16::launch_gated_tops(q, rowmax, reinterpret_cast<uint32_t*>(ws + l.factor), scale_max, s);
         if (err != hipSuccess) return W4A16_ERR_HIP;
-        const w4a16::GradPlan plan = w4a16::plan_grad(rows, K, 2 * F, false);
         float* part = plan.part_bytes ? reinterpret_cast<float*>(ws + l.gpart) : nullptr;
         uint16_t* out = static_cast<uint16_t*>(dx) + r0 * K;
         w4a16::GradCall g{};
         g.d = q.d;
         g.scaled = true;
+        g.d_rest = q.d_rest;
         g.rowmax = rowmax;
         g.tile_columns = w4a16::gated_tile_columns(rows, K, F, G);
         g.tile_factor = g.tile_columns ? reinterpret_cast<uint32_t*>(ws + l.factor) : nullptr;

@@ -160,10 +160,10 @@ template <> struct Dequant<false> {
 };
 
 // Powers of two that bring fp32 gradients and the weights into fp16, whose first 24 binades
-// from the top keep 11 bits: a set of gradients' largest magnitude goes to [2^4, 2^5), the
+// from the top keep 11 bits: a set of gradients' largest magnitude goes to [2^8, 2^9), the
 // weight's largest |scale| to [2^6, 2^7), so that 15 times it stays below 2^11. Exact, and
 // taken off the result again. (Zero, infinite or no number: 0.)
-constexpr int kGradTop = 4, kScaleTop = 6;
+constexpr int kGradTop = 8, kScaleTop = 6;
 __device__ __forceinline__ int scale_exponent(float top, int to) {
     if (!(top > 0.f) || top > 3e38f) return 0;
     const int e = to - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;

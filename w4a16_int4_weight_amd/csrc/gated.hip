@@ -26,6 +26,7 @@ struct GatedArgs {
     uint16_t* h;            // forward: [M, F]
     const uint16_t* dh;     // backward: [M, F]
     uint16_t* d;            // backward: [M, 2F] fp16, dg then du
+    uint16_t* d_rest;       // NULL or what d's rounding leaves
     float* tops;            // [column tiles][M] largest |d| of a row
     int act;
 };
@@ -103,24 +104,38 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, typename P::S
             if (w == 0 && h == 0 && m < M) a.tops[(size_t)(f0 / BN) * M + m] = top;
             const float by = power_of_two(scale_exponent(top, kGradTop));
 #pragma unroll
-            for (int j = 0; j < HB; ++j) {
-                const f32x4 o0 = acc[r][j] * by, o1 = acc[r][j + HB] * by;
-                *reinterpret_cast<uint2*>(t0 + place(r, j)) = make_uint2(pack2_rne<false>(o0[0], o0[1]), pack2_rne<false>(o0[2], o0[3]));
-                *reinterpret_cast<uint2*>(t1 + place(r, j)) = make_uint2(pack2_rne<false>(o1[0], o1[1]), pack2_rne<false>(o1[2], o1[3]));
-            }
+            for (int j = 0; j < P::CBW; ++j) acc[r][j] *= by;
         }
     }
-    __syncthreads();
-    for (int q = tid; q < BM * kChunks; q += P::kThreads) {
-        const int row = q / kChunks, ch = q % kChunks;
-        const int m = m0 + row, f = f0 + 8 * ch;
-        if (m >= M || f >= F) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(t0 + row * kRow + 16 * ch);
-        if constexpr (!kGrad) {
-            *reinterpret_cast<uint4*>(a.h + (size_t)m * F + f) = v;
-        } else {
-            *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + f) = v;
-            *reinterpret_cast<uint4*>(a.d + (size_t)m * 2 * F + F + f) = *reinterpret_cast<const uint4*>(t1 + row * kRow + 16 * ch);
+    // (an fp16 backward's second pass: what the first one's rounding left)
+    constexpr bool kRest = kGrad && !P::kBF16;
+    for (int pass = 0; pass < (kRest && a.d_rest ? 2 : 1); ++pass) {
+        if constexpr (kGrad) {
+            if (pass) __syncthreads();
+#pragma unroll
+            for (int r = 0; r < P::MR; ++r)
+#pragma unroll
+                for (int j = 0; j < P::CBW; ++j) {
+                    const f32x4 v = acc[r][j];
+                    const uint2 o = make_uint2(pack2_rne<false>(v[0], v[1]), pack2_rne<false>(v[2], v[3]));
+                    *reinterpret_cast<uint2*>((j < HB ? t0 : t1) + place(r, j % HB)) = o;
+                    if constexpr (kRest) acc[r][j] = f32x4{v[0] - f16_bits_to_f32(o.x & 0xFFFFu), v[1] - f16_bits_to_f32(o.x >> 16),
+                                      v[2] - f16_bits_to_f32(o.y & 0xFFFFu), v[3] - f16_bits_to_f32(o.y >> 16)};
+                }
+        }
+        __syncthreads();
+        for (int q = tid; q < BM * kChunks; q += P::kThreads) {
+            const int row = q / kChunks, ch = q % kChunks;
+            const int m = m0 + row, f = f0 + 8 * ch;
+            if (m >= M || f >= F) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(t0 + row * kRow + 16 * ch);
+            if constexpr (!kGrad) {
+                *reinterpret_cast<uint4*>(a.h + (size_t)m * F + f) = v;
+            } else {
+                uint16_t* d = pass ? a.d_rest : a.d;
+                *reinterpret_cast<uint4*>(d + (size_t)m * 2 * F + f) = v;
+                *reinterpret_cast<uint4*>(d + (size_t)m * 2 * F + F + f) = *reinterpret_cast<const uint4*>(t1 + row * kRow + 16 * ch);
+            }
         }
     }
 }
@@ -191,7 +206,7 @@ template <bool kBF16>
 __global__ __launch_bounds__(256) void convert_kernel(const float* __restrict__ tops, int tiles, const uint32_t* __restrict__ meta,
                                                       int64_t words, int M, int N, const float* __restrict__ d32,
                                                       float* __restrict__ rowmax, uint16_t* __restrict__ d,
-                                                      float* __restrict__ scale_max) {
+                                                      uint16_t* __restrict__ d_rest, float* __restrict__ scale_max) {
     if ((int)blockIdx.x < kScaleParts) {
         scale_part<kBF16>(meta, words, scale_max);
         return;
@@ -209,8 +224,15 @@ __global__ __launch_bounds__(256) void convert_kernel(const float* __restrict__ 
     const float by = power_of_two(scale_exponent(top, kGradTop));
     const f32x4* p = reinterpret_cast<const f32x4*>(d32 + (size_t)m * N + n);
     const f32x4 lo = p[0] * by, hi = p[1] * by;
-    *reinterpret_cast<uint4*>(d + (size_t)m * N + n) = make_uint4(pack2_rne<false>(lo[0], lo[1]), pack2_rne<false>(lo[2], lo[3]),
-                                                                 pack2_rne<false>(hi[0], hi[1]), pack2_rne<false>(hi[2], hi[3]));
+    const uint4 o = make_uint4(pack2_rne<false>(lo[0], lo[1]), pack2_rne<false>(lo[2], lo[3]), pack2_rne<false>(hi[0], hi[1]),
+                               pack2_rne<false>(hi[2], hi[3]));
+    *reinterpret_cast<uint4*>(d + (size_t)m * N + n) = o;
+    if (!d_rest) return;
+    auto rest = [](float a, float b, uint32_t v) {
+        return pack2_rne<false>(a - f16_bits_to_f32(v & 0xFFFFu), b - f16_bits_to_f32(v >> 16));
+    };
+    *reinterpret_cast<uint4*>(d_rest + (size_t)m * N + n) =
+        make_uint4(rest(lo[0], lo[1], o.x), rest(lo[2], lo[3], o.y), rest(hi[0], hi[1], o.z), rest(hi[2], hi[3], o.w));
 }
 
 template <bool kBF16, int MR, int CBW, int kSub, bool kGrad>
@@ -224,9 +246,11 @@ template <bool kBF16, bool kGrad>
 void launch_typed(const ProductPlan& p, GatedArgs& a, hipStream_t s) {
     if (p.sub == 4) {
         if (p.mr == 1) launch_cfg<kBF16, 1, 2, 4, kGrad>(a, s);
+        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 4, kGrad>(a, s);
         else launch_cfg<kBF16, 4, 2, 4, kGrad>(a, s);
     } else if (p.sub == 2) {
         if (p.mr == 1) launch_cfg<kBF16, 1, 2, 2, kGrad>(a, s);
+        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 2, kGrad>(a, s);
         else launch_cfg<kBF16, 4, 2, 2, kGrad>(a, s);
     } else if (p.mr == 1) launch_cfg<kBF16, 1, 2, 1, kGrad>(a, s);
     else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 1, kGrad>(a, s);
@@ -236,30 +260,39 @@ void launch_typed(const ProductPlan& p, GatedArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Tile shape: rows by M; at more than 64 rows the tile (128 x 256 or 64 x 256
-// columns of the weight) whose rounds over the compute units cost least, by area over the
-// rate each shape was measured at with every compute unit busy. Outputs of few tiles split
-// K over workgroups, at least 4 row blocks each.
+// Tile shape: 128, 64 or 32 rows by 256 columns of the weight, whose rounds over the compute
+// units cost least, by area over the rate each shape was measured at with every compute unit
+// busy (333 rows x 1024 x 5456: 132 tiles of 64 rows 17.0 us, 242 of 32 rows 13.4; 100 rows
+// x 2048 x 13312: 18.6 against 20.8). Outputs of few tiles split K over workgroups, at least
+// 4 row blocks each.
 ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gated) {
     ProductPlan p{};
     if (gated && small_product(M, K)) return p;          // no tiles, no workspace
     p.sub = units_per_block(G);
     const int64_t KB = K / kRowsPerBlock;
+    auto splits_of = [&](int64_t tiles) -> int64_t {
+        if (tiles >= kTargetWorkgroups / 2 || KB < 8) return 1;
+        const int64_t want = kTargetWorkgroups / tiles, most = KB / 4;
+        return want < most ? want : most;
+    };
     struct Shape { int mr, cbw; double rate; };
-    static constexpr Shape kShapes[] = {{8, 2, 0.85}, {4, 2, 0.7}};
-    if (p.sub > 1) {
-        p.mr = M <= 16 ? 1 : 4;
-        p.cbw = 2;
-    } else if (M <= 64) {
-        p.mr = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    // finer groups scale each fragment 2 or 4 times; their 128-row tile does not fit in LDS
+    static constexpr Shape kShapes[] = {{8, 2, 0.85}, {4, 2, 0.7}, {2, 2, 0.5}};
+    if (M <= 16) {
+        p.mr = 1;
         p.cbw = 2;
     } else {
         double best = 0.0;
         for (const Shape& c : kShapes) {
+            if (c.mr == 8 && (p.sub > 1 || M <= 64)) continue;
             const int64_t tm = (M + 16 * c.mr - 1) / (16 * c.mr);
             const int64_t tn = (cols + 128 * c.cbw - 1) / (128 * c.cbw);
-            const int64_t rounds = (tm * tn + kTargetWorkgroups - 1) / kTargetWorkgroups;
-            const double cost = (double)rounds * c.mr * c.cbw / c.rate;
+            const int64_t tiles = tm * tn, rounds = (tiles + kTargetWorkgroups - 1) / kTargetWorkgroups;
+            const int64_t splits = splits_of(tiles);
+            // a 128-row tile takes 2.1 us a row block; a tile's start and end as much as one,
+            // a split's meeting by its partial tiles
+            const double cost = (double)rounds * ((double)KB / (double)splits * c.mr * c.cbw / c.rate + 20.0 +
+                                                  (splits > 1 ? 4.0 * c.mr * (double)splits : 0.0));
             if (best == 0.0 || cost < best) {
                 best = cost;
                 p.mr = c.mr;
@@ -271,13 +304,8 @@ ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gat
     p.tiles_m = (int)((M + 16 * p.mr - 1) / (16 * p.mr));
     p.tiles_n = (int)(gated ? (cols / 2 + width / 2 - 1) / (width / 2) : (cols + width - 1) / width);
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    p.splits = 1;
     static_assert(kTargetWorkgroups / 2 <= kMaxSplitTiles, "split tiles must fit the counter region");
-    if (tiles < kTargetWorkgroups / 2 && KB >= 8) {
-        const int64_t want = kTargetWorkgroups / tiles;
-        const int64_t most = KB / 4;
-        p.splits = (int)(want < most ? want : most);
-    }
+    p.splits = (int)splits_of(tiles);
     p.partial_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)tiles * (size_t)(16 * p.mr) * (size_t)width * 4 : 0;
     return p;
 }
@@ -298,8 +326,8 @@ hipError_t launch_gated_tops(const GatedCall& q, float* rowmax, uint32_t* factor
     const dim3 block(256);
     if (small_product(q.M, q.K)) {
         const dim3 grid((unsigned)(kScaleParts + q.M * ((N + 2047) / 2048)));
-        if (q.bf16) hipLaunchKernelGGL((convert_kernel<true>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, (int)N, q.d32, rowmax, q.d, scale_max);
-        else hipLaunchKernelGGL((convert_kernel<false>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, (int)N, q.d32, rowmax, q.d, scale_max);
+        if (q.bf16) hipLaunchKernelGGL((convert_kernel<true>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, (int)N, q.d32, rowmax, q.d, q.d_rest, scale_max);
+        else hipLaunchKernelGGL((convert_kernel<false>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, (int)N, q.d32, rowmax, q.d, q.d_rest, scale_max);
     } else {
         const dim3 grid((unsigned)(kScaleParts + (q.M + 15) / 16));
         if (q.bf16) hipLaunchKernelGGL((tops_kernel<true>), grid, block, 0, stream, q.tops, tiles, meta, words, (int)q.M, rowmax, factor, scale_max);
@@ -326,6 +354,7 @@ hipError_t launch_gated(const GatedCall& q, hipStream_t stream) {
     a.h = q.h;
     a.dh = q.dh;
     a.d = q.d;
+    a.d_rest = q.d_rest;
     a.tops = q.tops;
     a.act = q.act;
     if (q.d) {

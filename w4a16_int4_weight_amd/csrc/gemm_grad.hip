@@ -46,6 +46,7 @@ struct GradArgs {
     const float* factor;
     const float* before;
     int factor_stages;      // stages of one column of `factor`
+    const uint16_t* d_rest;
     const float* rowmax;
     const uint32_t* tile_factor;
     int tile_columns;
@@ -110,9 +111,14 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     // D through registers (else by direct copies), and stages on their way in registers
     constexpr bool kRegs = kScaled || BM <= 128;
     constexpr int kDepth = BM <= 128 ? 4 : 1;
+    // D as two fp16 values, d + d_rest. One fp16 rounding of D, one of W and the result's own
+    // come to 1.7 times the last; without D's, to 1.4. (bf16's own rounding is 8 times
+    // theirs.) It costs a second MFMA; a 256-row tile has neither the time nor the LDS.
+    constexpr bool kRest = kScaled && !kScaleBF16 && BM <= 128;
     struct Stage {
         uint4 d[BM * 8];
         uint4 w[kStageN * 32];
+        uint4 rest[kRest ? BM * 8 : 1];
     };
     __shared__ Stage ring[2];
 
@@ -157,6 +163,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
         uint4 code;
         uint32_t md[kSub];
         uint4 dv[kChunks];                            // chunk tid + 512 i of D (row / 8, 8 columns)
+        uint4 rest[kRest ? kChunks : 1];
         uint32_t df[kChunks];
     };
     Fetch fetch[kDepth];
@@ -229,6 +236,8 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             x.dv[i] = *reinterpret_cast<const uint4*>(dbase + 2 * ((size_t)drow[i] * a.ld + n));
+            if constexpr (kRest)
+                x.rest[i] = *reinterpret_cast<const uint4*>(a.d_rest + ((size_t)m0 + drow[i]) * a.ld + n);
             if constexpr (kScaled) x.df[i] = fac ? fac[drow[i]] : 0x3C003C00u;
         }
     };
@@ -247,6 +256,11 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
                 const f16x2 by = __builtin_bit_cast(f16x2, x.df[i]);
                 auto times = [&](uint32_t p) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) * by); };
                 v = make_uint4(times(v.x), times(v.y), times(v.z), times(v.w));
+                if constexpr (kRest) {
+                    const uint4 l = x.rest[i];
+                    ring[slot].rest[row * 8 + (ch ^ (row & 7))] =
+                        in ? make_uint4(times(l.x), times(l.y), times(l.z), times(l.w)) : make_uint4(0u, 0u, 0u, 0u);
+                }
             } else if constexpr (kOpBF16) {
                 if (hot) {
                     const float by = a.factor[(size_t)(t / a.factor_stages) * a.M + m0 + drow[i]];
@@ -322,6 +336,15 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
             for (int r = 0; r < MR; ++r)
 #pragma unroll
                 for (int j = 0; j < CK; ++j) acc[r][j] = mfma16x16x32<kOpBF16>(b[j], f[r], acc[r][j]);
+            if constexpr (kRest) {
+#pragma unroll
+                for (int r = 0; r < MR; ++r) {
+                    const int row = 16 * (wm * MR + r) + c;
+                    const uint4 l = st.rest[row * 8 + ((4 * i + h) ^ (row & 7))];
+#pragma unroll
+                    for (int j = 0; j < CK; ++j) acc[r][j] = mfma16x16x32<kOpBF16>(b[j], l, acc[r][j]);
+                }
+            }
         }
     };
     if (st_lo < st_hi) {
@@ -437,6 +460,8 @@ GradPlan plan_grad(int64_t M, int64_t K, int64_t n, bool forced) {
     return p;
 }
 
+bool grad_takes_rest(const GradPlan& plan, bool bf16) { return !bf16 && plan.bm <= 128; }
+
 hipError_t launch_grad(const GradPlan& plan, const GradCall& q, hipStream_t stream) {
     GradArgs a{};
     a.d = q.d;
@@ -460,6 +485,8 @@ hipError_t launch_grad(const GradPlan& plan, const GradCall& q, hipStream_t stre
     a.before = q.before;
     a.factor_stages = q.factor_columns / kStageN;
     if ((plan.splits > 1 || !q.dx) && !q.part) return hipErrorInvalidValue;
+    if (q.scaled && grad_takes_rest(plan, q.bf16) != (q.d_rest != nullptr)) return hipErrorInvalidValue;
+    a.d_rest = q.d_rest;
     a.rowmax = q.rowmax;
     a.tile_factor = q.tile_factor;
     a.tile_columns = q.tile_columns;

@@ -128,6 +128,7 @@ struct GatedCall {
     const uint8_t* packed;
     uint16_t* h;
     uint16_t* d;
+    uint16_t* d_rest;      // NULL, or [M, 2F]: what d's rounding leaves, at the same scales
     float* d32;            // what small_product shapes write instead
     float* tops;           // [gated_tiles(...)][M] largest |d| of a row in each share of the columns
     int64_t M, K, F, G;
@@ -177,6 +178,7 @@ struct GradCall {
     // is not NULL, tile of tile_columns columns from 0 and from N / 2; the weights are taken
     // in fp16, scaled from the largest |scale| (scale_max)
     bool scaled;
+    const uint16_t* d_rest;   // added to d
     const float* rowmax;
     const uint32_t* tile_factor;
     int tile_columns;
@@ -188,6 +190,8 @@ struct GradPlan {
     int splits;
     size_t part_bytes;     // [splits][M][K] fp32 when splits > 1
 };
+// Whether a scaled product of this type takes d_rest: fp16, tiles of up to 128 rows.
+bool grad_takes_rest(const GradPlan& plan, bool bf16);
 // `forced`: the sum comes in several calls, so partials are needed at any split.
 GradPlan plan_grad(int64_t M, int64_t K, int64_t n, bool forced);
 hipError_t launch_grad(const GradPlan& plan, const GradCall& call, hipStream_t stream);

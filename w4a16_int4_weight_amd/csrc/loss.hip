@@ -515,9 +515,11 @@ template <bool kBF16, bool kProb>
 void launch_typed(const ProductPlan& p, LossArgs& a, hipStream_t s) {
     if (p.sub == 4) {
         if (p.mr == 1) launch_cfg<kBF16, 1, 2, 4, kProb>(a, s);
+        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 4, kProb>(a, s);
         else launch_cfg<kBF16, 4, 2, 4, kProb>(a, s);
     } else if (p.sub == 2) {
         if (p.mr == 1) launch_cfg<kBF16, 1, 2, 2, kProb>(a, s);
+        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 2, kProb>(a, s);
         else launch_cfg<kBF16, 4, 2, 2, kProb>(a, s);
     } else if (p.mr == 1) launch_cfg<kBF16, 1, 2, 1, kProb>(a, s);
     else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 1, kProb>(a, s);

@@ -49,24 +49,26 @@ struct ProductArgs {
 
 constexpr int kProductXcds = 8;
 
-// Workgroup id -> tile. Ids id, id + 8, ... run on one XCD: it takes every 8th column
-// tile and walks the row tiles of one in groups of 8, so that its L2 serves the codes of
-// few column tiles and the activations of few row tiles at a time.
+// Workgroup id -> tile. Ids id, id + 8, ... run on one XCD, which takes a contiguous eighth
+// of the tiles in an order that walks 8 row tiles of a column tile, then the next column
+// tile's: its L2 serves the codes of few column tiles and the activations of few row tiles
+// at a time. (Whole column tiles dealt to the XCDs left some with a round more than others:
+// 242 tiles, 22 columns wide, took 25 us, two rounds, against 17.)
 __device__ __forceinline__ bool product_tile(const ProductArgs& a, int id, int* m_tile, int* n_tile, int* split) {
-    const int x = id % kProductXcds;
-    int local = id / kProductXcds;
-    *split = local % a.splits;
-    local /= a.splits;
-    const int per = (a.tiles_n + kProductXcds - 1) / kProductXcds;   // column tiles of an XCD
-    const int chunk = local / (8 * per);
+    const int x = id % kProductXcds, total = a.tiles_m * a.tiles_n * a.splits;
+    const int at = (int)((int64_t)total * x / kProductXcds) + id / kProductXcds;
+    if (at >= (int)((int64_t)total * (x + 1) / kProductXcds)) return false;
+    *split = at % a.splits;
+    const int tile = at / a.splits;
+    const int chunk = tile / (8 * a.tiles_n);
     const int gm = a.tiles_m - 8 * chunk < 8 ? a.tiles_m - 8 * chunk : 8;
-    const int rem = local - chunk * 8 * per;
+    const int rem = tile - chunk * 8 * a.tiles_n;
     *m_tile = 8 * chunk + rem % gm;
-    *n_tile = (rem / gm) * kProductXcds + x;
-    return *n_tile < a.tiles_n;
+    *n_tile = rem / gm;
+    return true;
 }
 inline int64_t product_ids(int tiles_m, int tiles_n, int splits) {
-    return (int64_t)tiles_m * ((tiles_n + kProductXcds - 1) / kProductXcds) * kProductXcds * splits;
+    return ((int64_t)tiles_m * tiles_n * splits + kProductXcds - 1) / kProductXcds * kProductXcds;
 }
 
 template <bool kBF16>
