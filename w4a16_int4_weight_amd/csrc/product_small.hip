@@ -10,10 +10,14 @@
 // one barrier a batch, added in wave order. No K split over workgroups, no partial sums in
 // memory, no atomics: results do not depend on timing.
 //
-// Per metadata unit: s (T - (128 + z) X), as in tile_product.h; X comes from the same MFMAs
-// against ones, once for all units. fp16 takes q - z exactly in 16 bits.
+// Per metadata unit: s (T - (16 + z) X), T = sum x (16 + q) on codes masked into the mantissa
+// of bf16's 16.0 (one shift more per word than 128.0, as tile_product.h has it, and a ninth
+// of what the difference loses; here the shifts hide behind the loads). X comes from the
+// same MFMAs against ones, once for all units. fp16 takes q - z exactly in 16 bits.
 //
-// Measured (2048 x 13312 at one row; 2048 x 131072 at one row): see the table of cases.
+// Measured: 2048 x 13312, one row or 16, 7 us a call (10 us with 16-row tiles and K split over
+// workgroups); 2048 x 131072, one row, 31 us, 4.6 TB/s (36 us). With 512 workgroups instead
+// of 256: 9.0 and 38.7 us a call.
 #include "device_common.h"
 #include "gate.h"
 #include "launch.h"
@@ -135,7 +139,10 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
                 const int u = i * kSub / 4;
                 uint32_t p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ((d >> (4 * e)) & 0x000F000Fu) | Magic<kBF16>::kBase2;
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (kBF16) p[e] = ((e == 0 ? d << 3 : d >> (4 * e - 3)) & 0x00780078u) | 0x41804180u;
+                    else p[e] = ((d >> (4 * e)) & 0x000F000Fu) | Magic<false>::kBase2;
+                }
                 if constexpr (!kBF16) {
                     const _Float16 zb = (_Float16)(1024.0f + (float)((b.md[s][j * kSub + u] >> 16) & 0xFu));
 #pragma unroll
@@ -148,7 +155,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
             for (int u = 0; u < kSub; ++u) {
                 const uint32_t md = b.md[s][j * kSub + u];
                 const float sc = half_bits_to_f32<kBF16>(md & 0xFFFFu);
-                const float zb = 128.f + (float)((md >> 16) & 0xFu);
+                const float zb = 16.f + (float)((md >> 16) & 0xFu);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[e] = fmaf(sc, kBF16 ? fmaf(-zb, X[j][u][e], T[u][e]) : T[u][e], acc[e]);
             }
