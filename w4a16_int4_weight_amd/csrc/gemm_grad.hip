@@ -20,6 +20,11 @@
 // latency is paid once and not each stage. Small M, or few tiles: the sum
 // is split over workgroups into fp32 partial tiles, added in split order by a second
 // kernel (the result does not depend on the order of arrival).
+//
+// Measured with every compute unit busy (4096 x 8192 -> 4096, bf16): 264 us, 1041 TFLOP/s;
+// bound by LDS (writes and reads of a stage take as long as its MFMAs) and the decoding.
+// 4096 x 2048 -> 6656 has 416 tiles for 256 compute units: 144 us, the second round 0.6 full.
+// Few rows are bound by the partial tiles' traffic and the latency of a few stages.
 #include "device_common.h"
 #include "launch.h"
 

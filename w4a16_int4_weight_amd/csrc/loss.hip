@@ -21,6 +21,11 @@
 // is 8 times finer than bf16's rounding).
 // The targets' columns are zero in P and enter at the end in fp32, (q_t - p_t) W_t: for a
 // confident row that difference is small, and of two rounded numbers it would be lost.
+//
+// Roundings: P once and W once, to the operand type; dx once. Measured on 4096 x 2048 x
+// 131072 with its gradient: 9490 us with the tile formed twice and the scheduling left to
+// the compiler, 4700 us so (two products of 2.2 TFLOP, 930 and 980 TFLOP/s); bound by the
+// matrix cores and the vector instructions between their MFMAs.
 #include "device_common.h"
 #include "launch.h"
 #include "tile_product.h"
