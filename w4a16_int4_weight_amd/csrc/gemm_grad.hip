@@ -115,7 +115,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
     constexpr int kSlabs = BM / 8;                    // 1 KiB slabs (8 rows) of the D stage
     // D through registers (else by direct copies), and stages on their way in registers
     constexpr bool kRegs = kScaled || BM <= 128;
-    constexpr int kDepth = BM <= 128 ? 4 : 1;
+    constexpr int kDepth = BM > 128 ? 1 : kScaled && !kScaleBF16 ? 2 : 4;       // (fp16 scaled: twice the D)
     // D as two fp16 values, d + d_rest. One fp16 rounding of D, one of W and the result's own
     // come to 1.7 times the last; without D's, to 1.4. (bf16's own rounding is 8 times
     // theirs.) It costs a second MFMA; a 256-row tile has neither the time nor the LDS.
