@@ -435,32 +435,39 @@ void launch_typed(int bm, int sub, const GradArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Rows of a tile by M; above 128 rows, 256 or 128 by the rounds of tiles over the compute
-// units. The sum is split where the tiles leave compute units idle, at least 4 stages each.
+// Rows of a tile and the split of the sum, by what they cost: rounds of tiles over the
+// compute units times the stages of each (us, measured with every compute unit busy; 4096 x
+// 8192 -> 4096 takes 264 us in 256-row tiles, 376 in 128-row ones), plus a start and an end,
+// plus the partial tiles written and read at 4 TB/s. Lower tiles need fewer splits: 180 x
+// 4000 -> 1024 takes 21.3 us in 128-row tiles, 15.5 in 32-row ones; 64 x 32000 -> 2048, where
+// the stages count, 6.7 us less in 64-row tiles than in 32-row ones. At least 4 stages a
+// split.
 GradPlan plan_grad(int64_t M, int64_t K, int64_t n, bool forced) {
     GradPlan p{};
     p.tiles_k = (int)((K + kTileK - 1) / kTileK);
     const int64_t stages = (n + kStageN - 1) / kStageN;
     const int64_t most = stages / 4 > 1 ? stages / 4 : 1;
-    auto splits_of = [&](int64_t tiles) {
+    struct Shape { int bm; double stage; };
+    static constexpr Shape kShapes[] = {{16, 0.85}, {32, 0.9}, {64, 1.1}, {128, 1.47}, {256, 2.06}};
+    double best = 0.0;
+    for (const Shape& c : kShapes) {
+        if (c.bm > 16 && c.bm / 2 >= M) break;                     // half the rows would do
+        const int64_t tm = (M + c.bm - 1) / c.bm, tiles = tm * p.tiles_k;
         int64_t s = kTargetWorkgroups / tiles;
-        if (s < 1) s = 1;
-        return s < most ? s : most;
-    };
-    p.bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    if (M > 128) {
-        auto cost = [&](int bm, double rate) {
-            const int64_t tiles = (M + bm - 1) / bm * p.tiles_k;
-            const int64_t s = splits_of(tiles);
+        s = s < 1 ? 1 : s < most ? s : most;
+        for (;; s /= 2) {
             const int64_t rounds = (tiles * s + kTargetWorkgroups - 1) / kTargetWorkgroups;
-            return (double)rounds * bm / ((double)s * rate);
-        };
-        // a 128-row tile reaches 0.66 of the 256-row tile's rate (4096 x 8192 -> 4096: 376
-        // against 264 us)
-        if (cost(256, 1.0) <= cost(128, 0.66)) p.bm = 256;
+            const double part = forced || s > 1 ? 8.0e-6 * (double)s * (double)M * (double)K / 4.0 : 0.0;
+            const double cost = (double)rounds * ((double)stages / (double)s * c.stage + 5.0) + part;
+            if (best == 0.0 || cost < best) {
+                best = cost;
+                p.bm = c.bm;
+                p.tiles_m = (int)tm;
+                p.splits = (int)s;
+            }
+            if (s == 1) break;
+        }
     }
-    p.tiles_m = (int)((M + p.bm - 1) / p.bm);
-    p.splits = (int)splits_of((int64_t)p.tiles_m * p.tiles_k);
     p.part_bytes = forced || p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)K * 4 : 0;
     return p;
 }
