@@ -13,7 +13,7 @@
 // would be off by as much as the result's own rounding, and fp32 took 8 F bytes a row.
 //
 // Measured: 512 rows x 2048 x 13312 37 us (757 TFLOP/s; 208 tiles, one round), 4096 rows 247
-// us (903); the backward of 4096 rows 528 us (846 over both products). Bound by the matrix
+// us (903); the backward of 4096 rows 523 us (855 over both products). Bound by the matrix
 // cores and the vector instructions between their MFMAs; a tile's start and end, which no
 // other workgroup of its compute unit covers, take a tenth.
 #include "device_common.h"
