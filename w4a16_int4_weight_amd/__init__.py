@@ -45,6 +45,7 @@ library's error, raised here as W4A16Error.
 import ctypes
 import functools
 import os
+import threading
 
 import torch
 
@@ -389,30 +390,62 @@ def _default_workspace(device, nbytes, stream=None):
     return ws
 
 
-def _gemm_args(x, packed, N, group_size, bias, y, workspace, stream):
+_locks = {}
+
+
+def _raw_stream(stream, device):
+    """The hipStream_t of `stream`, or of the device's current stream, as an integer."""
+    if stream is None:
+        if device.type == "cuda":
+            return torch._C._cuda_getCurrentRawStream(device.index)
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream
+
+
+def _launch(name, args, workspace, need, device, stream, more=()):
+    """The library's `name`(*args, workspace, its bytes, stream, *more), checked. Without a
+    workspace, a call that needs one takes the (device, stream)'s own, which serves one
+    call at a time: most entry points are several launches that meet in it, so the lock is
+    held until a call's last launch is queued, and the launches of another thread's call on
+    that stream stay behind them. (ctypes lets other threads run during the call.)"""
+    fn = getattr(_load(), name)
+    raw = _raw_stream(stream, device)
+    if workspace is None and need > 0:
+        key = (device.index, raw)
+        lock = _locks.get(key) or _locks.setdefault(key, threading.RLock())
+        with lock:
+            ws = _workspaces.get(key)
+            if ws is None or ws.numel() < need:
+                ws = _default_workspace(device, need, stream)
+            code = fn(*args, ws.data_ptr(), ws.nbytes, raw, *more)
+    elif workspace is None:
+        code = fn(*args, None, 0, raw, *more)
+    else:
+        code = fn(*args, workspace.data_ptr(), workspace.nbytes, raw, *more)
+    _check(code, name)
+
+
+def _gemm_args(x, packed, N, group_size, bias, y, workspace):
+    """-> (the library's arguments up to the workspace, the workspace it needs, y)"""
     if x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous [M, K] tensor")
     M, K = x.shape
-    if workspace is None and M > 0:
-        need = w4a16_workspace_bytes(M, K, N, group_size)
-        if need > 0:
-            workspace = _default_workspace(x.device, need, stream)
+    need = w4a16_workspace_bytes(M, K, N, group_size) if workspace is None and M > 0 else 0
     if y is None:
         y = torch.empty((M, N), dtype=x.dtype, device=x.device)
     if tuple(y.shape) != (M, N) or y.dtype != x.dtype or not y.is_contiguous():
         raise ValueError("y must be a contiguous [M, N] tensor of x's dtype")
     if bias is not None and (bias.dtype != x.dtype or tuple(bias.shape) != (N,) or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous [N] tensor of x's dtype")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(x), _ptr(packed), packed.numel() * packed.element_size(), _dtype_code(x.dtype),
-            _ptr(y), M, K, N, group_size, _ptr(bias), _ptr(workspace), ws_bytes, _stream(stream, x.device))
-    return args, y
+            _ptr(y), M, K, N, group_size, _ptr(bias))
+    return args, need, y
 
 
 def w4a16_gemm(x, packed, N, group_size=128, bias=None, y=None, workspace=None, stream=None):
     """x [M, K] (fp16/bf16) times the packed weight (+ bias) -> y [M, N] of x's dtype."""
-    args, y = _gemm_args(x, packed, N, group_size, bias, y, workspace, stream)
-    _check(_load().w4a16_gemm(*args), "w4a16_gemm")
+    args, need, y = _gemm_args(x, packed, N, group_size, bias, y, workspace)
+    _launch("w4a16_gemm", args, workspace, need, x.device, stream)
     return y
 
 
@@ -421,8 +454,8 @@ def w4a16_gemm_ex(x, packed, N, group_size=128, bias=None, y=None, workspace=Non
     """w4a16_gemm with the kernel path forced ("auto", "gemv" or "mfma")."""
     if path not in PATHS:
         raise W4A16Error(9, f"path {path!r}")
-    args, y = _gemm_args(x, packed, N, group_size, bias, y, workspace, stream)
-    _check(_load().w4a16_gemm_ex(*args, PATHS[path], gemv_max_m), "w4a16_gemm_ex")
+    args, need, y = _gemm_args(x, packed, N, group_size, bias, y, workspace)
+    _launch("w4a16_gemm_ex", args, workspace, need, x.device, stream, (PATHS[path], gemv_max_m))
     return y
 
 
@@ -505,21 +538,16 @@ def w4a8_gemm(act, packed, M, K, N, group_size=128, dtype=torch.bfloat16, bias=N
               stream=None):
     """W4A8 activation buffer (from w4a8_quantize) times the packed weight (+ bias)
     -> y [M, N] of `dtype` (the dtype of the weight's scales)."""
-    if workspace is None and M > 0:
-        need = w4a8_workspace_bytes(M, K, N, group_size)
-        if need > 0:
-            workspace = _default_workspace(act.device, need, stream)
+    need = w4a8_workspace_bytes(M, K, N, group_size) if workspace is None and M > 0 else 0
     if y is None:
         y = torch.empty((M, N), dtype=dtype, device=act.device)
     if tuple(y.shape) != (M, N) or y.dtype != dtype or not y.is_contiguous():
         raise ValueError("y must be a contiguous [M, N] tensor of `dtype`")
     if bias is not None and (bias.dtype != dtype or tuple(bias.shape) != (N,) or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous [N] tensor of `dtype`")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    code = _load().w4a8_gemm(_ptr(act), act.numel() * act.element_size(), _ptr(packed),
-                             packed.numel() * packed.element_size(), _dtype_code(dtype), _ptr(y), M, K, N, group_size,
-                             _ptr(bias), _ptr(workspace), ws_bytes, _stream(stream, act.device))
-    _check(code, "w4a8_gemm")
+    args = (_ptr(act), act.numel() * act.element_size(), _ptr(packed), packed.numel() * packed.element_size(),
+            _dtype_code(dtype), _ptr(y), M, K, N, group_size, _ptr(bias))
+    _launch("w4a8_gemm", args, workspace, need, act.device, stream)
     return y
 
 
@@ -563,26 +591,6 @@ def _result(t, name, shape, dtype, device):
     return t
 
 
-def _raw_stream(stream, device):
-    """The hipStream_t of `stream`, or of the device's current stream, as an integer."""
-    if stream is None:
-        if device.type == "cuda":
-            return torch._C._cuda_getCurrentRawStream(device.index)
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream
-
-
-def _space(workspace, need, device, stream, raw):
-    """(pointer, bytes) of the caller's workspace, or of the (device, stream)'s own."""
-    if workspace is None:
-        if need == 0:
-            return None, 0
-        workspace = _workspaces.get((device.index, raw))
-        if workspace is None or workspace.numel() < need:
-            workspace = _default_workspace(device, need, stream)
-    return workspace.data_ptr(), workspace.nbytes
-
-
 @functools.lru_cache(maxsize=4096)
 def _need(name, *shape):
     """A workspace_bytes function's answer: it depends on the shape alone."""
@@ -593,13 +601,10 @@ def w4a16_gemm_grad(dy, packed, K, group_size=128, dx=None, workspace=None, stre
     """dy [M, N] (fp16/bf16) times the transposed packed [K, N] weight -> dx [M, K]: the
     gradient of w4a16_gemm with respect to x."""
     M, N = _rows(dy, "dy")
-    h = _load()
     dx = _result(dx, "dx", (M, K), dy.dtype, dy.device)
-    raw = _raw_stream(stream, dy.device)
-    ws, ws_bytes = _space(workspace, _need("w4a16_gemm_grad_workspace_bytes", M, K, N, group_size), dy.device, stream, raw)
-    _check(h.w4a16_gemm_grad(dy.data_ptr(), packed.data_ptr(), packed.nbytes,
-                             _dtype_code(dy.dtype), dx.data_ptr(), M, K, N, group_size, ws, ws_bytes,
-                             raw), "w4a16_gemm_grad")
+    _launch("w4a16_gemm_grad",
+            (dy.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(dy.dtype), dx.data_ptr(), M, K, N, group_size),
+            workspace, _need("w4a16_gemm_grad_workspace_bytes", M, K, N, group_size), dy.device, stream)
     return dx
 
 
@@ -613,13 +618,10 @@ def w4a16_gated(x, packed, F, group_size=128, act="silu", h=None, workspace=None
     """Gated feed-forward block on one packed [K, 2F] weight (gate columns, then up):
     x [M, K] -> h [M, F] = act(x Wg) * (x Wu). act: "silu", "gelu" or "gelu_tanh"."""
     M, K = _rows(x, "x")
-    lib = _load()
     h = _result(h, "h", (M, F), x.dtype, x.device)
-    raw = _raw_stream(stream, x.device)
-    ws, ws_bytes = _space(workspace, _need("w4a16_gated_workspace_bytes", M, K, F, group_size, 0), x.device, stream, raw)
-    _check(lib.w4a16_gated(x.data_ptr(), packed.data_ptr(), packed.nbytes,
-                           _dtype_code(x.dtype), h.data_ptr(), M, K, F, group_size, _act_code(act), ws, ws_bytes,
-                           raw), "w4a16_gated")
+    _launch("w4a16_gated",
+            (x.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(x.dtype), h.data_ptr(), M, K, F, group_size,
+             _act_code(act)), workspace, _need("w4a16_gated_workspace_bytes", M, K, F, group_size, 0), x.device, stream)
     return h
 
 
@@ -629,13 +631,11 @@ def w4a16_gated_grad(x, dh, packed, F, group_size=128, act="silu", dx=None, work
     M, K = _rows(x, "x")
     if _rows(dh, "dh") != (M, F) or dh.dtype != x.dtype:
         raise ValueError("dh must be a contiguous [M, F] tensor of x's dtype")
-    lib = _load()
     dx = _result(dx, "dx", (M, K), x.dtype, x.device)
-    raw = _raw_stream(stream, x.device)
-    ws, ws_bytes = _space(workspace, _need("w4a16_gated_workspace_bytes", M, K, F, group_size, 1), x.device, stream, raw)
-    _check(lib.w4a16_gated_grad(x.data_ptr(), dh.data_ptr(), packed.data_ptr(), packed.nbytes,
-                                _dtype_code(x.dtype), dx.data_ptr(), M, K, F, group_size, _act_code(act), ws, ws_bytes,
-                                raw), "w4a16_gated_grad")
+    _launch("w4a16_gated_grad",
+            (x.data_ptr(), dh.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(x.dtype), dx.data_ptr(), M, K, F,
+             group_size, _act_code(act)), workspace, _need("w4a16_gated_workspace_bytes", M, K, F, group_size, 1), x.device,
+            stream)
     return dx
 
 
@@ -661,15 +661,10 @@ def w4a16_cross_entropy(x, labels, packed, V, group_size=128, dloss=None, grad=F
     M, K, loss, lse, dx = _loss_args(x, dloss, grad, loss, lse, dx)
     if tuple(labels.shape) != (M,) or labels.dtype != torch.int32 or not labels.is_contiguous():
         raise ValueError("labels must be a contiguous int32 [M] tensor")
-    h = _load()
-    raw = _raw_stream(stream, x.device)
-    ws, ws_bytes = _space(workspace, _need("w4a16_cross_entropy_workspace_bytes", M, K, V, group_size, 1 if grad else 0),
-                          x.device, stream, raw)
-    _check(h.w4a16_cross_entropy(x.data_ptr(), labels.data_ptr(), packed.data_ptr(),
-                                 packed.nbytes, _dtype_code(x.dtype), M, K, V, group_size,
-                                 None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(),
-                                 dx.data_ptr() if grad else None, ws, ws_bytes, raw),
-           "w4a16_cross_entropy")
+    _launch("w4a16_cross_entropy",
+            (x.data_ptr(), labels.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(x.dtype), M, K, V, group_size,
+             None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(), dx.data_ptr() if grad else None),
+            workspace, _need("w4a16_cross_entropy_workspace_bytes", M, K, V, group_size, 1 if grad else 0), x.device, stream)
     return (loss, lse, dx) if grad else (loss, lse)
 
 
@@ -685,14 +680,11 @@ def w4a16_distill(x, top_ids, top_logits, packed, V, group_size=128, temperature
         raise ValueError("top_ids must be an int32 [M, T] tensor")
     if _rows(top_logits, "top_logits") != (M, T) or top_logits.dtype != torch.float32:
         raise ValueError("top_logits must be a float32 [M, T] tensor")
-    h = _load()
-    raw = _raw_stream(stream, x.device)
-    ws, ws_bytes = _space(workspace, _need("w4a16_distill_workspace_bytes", M, K, V, group_size, T, 1 if grad else 0),
-                          x.device, stream, raw)
-    _check(h.w4a16_distill(x.data_ptr(), top_ids.data_ptr(), top_logits.data_ptr(), packed.data_ptr(),
-                           packed.nbytes, _dtype_code(x.dtype), M, K, V, group_size, T,
-                           temperature, None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(),
-                           dx.data_ptr() if grad else None, ws, ws_bytes, raw), "w4a16_distill")
+    _launch("w4a16_distill",
+            (x.data_ptr(), top_ids.data_ptr(), top_logits.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(x.dtype),
+             M, K, V, group_size, T, temperature, None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+             dx.data_ptr() if grad else None),
+            workspace, _need("w4a16_distill_workspace_bytes", M, K, V, group_size, T, 1 if grad else 0), x.device, stream)
     return (loss, lse, dx) if grad else (loss, lse)
 
 
