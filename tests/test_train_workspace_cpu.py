@@ -14,6 +14,7 @@ class Library:
 
     def __init__(self, mod, need=4096):
         self.mod, self.need, self.calls, self.running, self.clashes = mod, need, [], set(), []
+        self.capture = None
 
     def __getattr__(self, name):
         if name.endswith("_workspace_bytes"):
@@ -41,6 +42,8 @@ def mod(monkeypatch):
     import w4a16_int4_weight_amd as m
     monkeypatch.setattr(m, "_lib", Library(m))
     monkeypatch.setattr(m, "_raw_stream", lambda stream, device: STREAM)
+    monkeypatch.setattr(m, "_capture_of", lambda raw: m._lib.capture, raising=False)
+    monkeypatch.setattr(m, "_captured", {}, raising=False)
     monkeypatch.setattr(m, "_workspaces", {(None, STREAM): torch.zeros(4096, dtype=torch.uint8)})
     m._need.cache_clear()
 
@@ -103,3 +106,29 @@ def test_a_callers_workspace_is_passed_on(mod):
     mod._workspaces[(None, 0)] = ws
     mod.w4a16_gated(x, torch.zeros(1 << 15, dtype=torch.uint8), 64, workspace=ws)
     assert mod._lib.calls[-1][1:] == (ws.data_ptr(), 8192, STREAM)
+
+
+def test_a_capture_has_its_own_workspace(mod):
+    lib, op = mod._lib, calls(mod)[3]
+    op()
+    eager = lib.calls[-1][1]
+    lib.capture = 5
+    op()
+    first = lib.calls[-1][1]
+    assert first != eager and bool((mod._captured[(None, STREAM)][1][:512] == 0).all())
+    op()                                        # the calls of one capture share one
+    assert lib.calls[-1][1] == first
+    lib.need = 16384                            # ... which grows with them
+    mod._need.cache_clear()
+    op()
+    assert lib.calls[-1][2] == 16384
+    lib.capture = None                          # eager calls keep theirs, and grow it
+    op()
+    assert lib.calls[-1][1] not in (first, mod._captured[(None, STREAM)][1].data_ptr())
+    assert lib.calls[-1][1] == mod._workspaces[(None, STREAM)].data_ptr()
+    lib.capture = 6                             # another graph: cleared by that graph again
+    kept = mod._captured[(None, STREAM)][1]
+    kept.fill_(1)
+    op()
+    assert mod._captured[(None, STREAM)][1] is not kept
+    assert bool((mod._captured[(None, STREAM)][1][:512] == 0).all())

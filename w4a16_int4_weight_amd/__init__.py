@@ -13,7 +13,8 @@ Functions keep the C names:
   w4a16_packed_header(K, N, group_size, dtype) -> 64 bytes
   w4a16_parse_packed_header(header) -> (K, N, group_size, dtype, packed_bytes)
   w4a16_gemm(x, packed, N, group_size, bias=None, y=None, workspace=None, stream=None) -> y
-      (workspace=None: a zero-filled per-device workspace is allocated on demand)
+      (workspace=None: a zero-filled workspace per device and stream is allocated on demand;
+      in a captured graph, one in the graph's own memory)
   w4a16_gemm_ex(..., path="auto"|"gemv"|"mfma", gemv_max_m=-1)            -> y
   w4a16_gemm_noalloc(x, packed, N, group_size, bias=None, y=None, stream=None) -> y
       (no workspace: the library's per-GPU scratch array; nothing is allocated when y is given)
@@ -166,6 +167,9 @@ def _load():
     h.w4a16_distill.argtypes = [_vp, _vp, _vp, _vp, _sz, _int, _i64, _i64, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp,
                                 _vp, _sz, _vp]
     h.w4a16_distill.restype = _int
+    # the HIP runtime that the library is linked to
+    h.hipStreamGetCaptureInfo.argtypes = [_vp, ctypes.POINTER(_int), ctypes.POINTER(ctypes.c_ulonglong)]
+    h.hipStreamGetCaptureInfo.restype = _int
     h.w4a16_status_str.argtypes = [_int]
     h.w4a16_status_str.restype = ctypes.c_char_p
     _lib = h
@@ -391,6 +395,31 @@ def _default_workspace(device, nbytes, stream=None):
 
 
 _locks = {}
+_captured = {}           # (device, stream) -> (its last capture, that capture's workspace)
+CLEARED_BYTES = 512      # what has to be zero before a workspace's first use
+
+
+def _capture_of(raw):
+    """The number of the capture that the stream is recorded into, or None."""
+    if raw == 0:         # the device's default stream is never captured
+        return None
+    status, number = ctypes.c_int(), ctypes.c_ulonglong()
+    code = _load().hipStreamGetCaptureInfo(raw, ctypes.byref(status), ctypes.byref(number))
+    return number.value if code == 0 and status.value == 1 else None
+
+
+def _workspace_of_capture(key, capture, nbytes, device, stream):
+    """A workspace for the calls that one capture records on one stream, in the graph's own
+    memory and cleared by the graph, so that a replay neither meets a buffer that an eager
+    call has replaced nor depends on one that another graph has cleared. Eager calls never
+    see it."""
+    last = _captured.get(key)
+    if last is None or last[0] != capture or last[1].numel() < nbytes:
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(nbytes, CLEARED_BYTES), dtype=torch.uint8, device=device)
+            ws[:CLEARED_BYTES].zero_()
+        last = _captured[key] = (capture, ws)
+    return last[1]
 
 
 def _raw_stream(stream, device):
@@ -407,16 +436,21 @@ def _launch(name, args, workspace, need, device, stream, more=()):
     workspace, a call that needs one takes the (device, stream)'s own, which serves one
     call at a time: most entry points are several launches that meet in it, so the lock is
     held until a call's last launch is queued, and the launches of another thread's call on
-    that stream stay behind them. (ctypes lets other threads run during the call.)"""
+    that stream stay behind them. (ctypes lets other threads run during the call.) Under a
+    capture it is the capture's own."""
     fn = getattr(_load(), name)
     raw = _raw_stream(stream, device)
     if workspace is None and need > 0:
         key = (device.index, raw)
         lock = _locks.get(key) or _locks.setdefault(key, threading.RLock())
         with lock:
-            ws = _workspaces.get(key)
-            if ws is None or ws.numel() < need:
-                ws = _default_workspace(device, need, stream)
+            capture = _capture_of(raw)
+            if capture is not None:
+                ws = _workspace_of_capture(key, capture, need, device, stream)
+            else:
+                ws = _workspaces.get(key)
+                if ws is None or ws.numel() < need:
+                    ws = _default_workspace(device, need, stream)
             code = fn(*args, ws.data_ptr(), ws.nbytes, raw, *more)
     elif workspace is None:
         code = fn(*args, None, 0, raw, *more)
