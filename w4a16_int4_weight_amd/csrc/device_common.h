@@ -159,17 +159,23 @@ template <> struct Dequant<false> {
     }
 };
 
-// Powers of two that bring fp32 gradients and the weights into fp16, whose first 24 binades
-// from the top keep 11 bits: a set of gradients' largest magnitude goes to [2^8, 2^9), the
-// weight's largest |scale| to [2^6, 2^7), so that 15 times it stays below 2^11. Exact, and
-// taken off the result again. (Zero, infinite or no number: 0.)
+// Powers of two that bring fp32 gradients and the weights into fp16: a set of gradients'
+// largest magnitude goes to [2^8, 2^9), the weight's largest |scale| to [2^6, 2^7), so that
+// 15 times it stays below 2^11. fp16 keeps 11 bits down to 2^-14: a gradient 23 binades, a
+// scale 21 binades below the largest (a factor of 2 million) still has them all, the next
+// ten binades lose a bit each, and what lies lower becomes zero. Exact for every finite
+// float, and taken off the result again in one step, whose exponent is the sum of both.
+// (Zero, infinite or no number: 0. Below 2^-118 gradients stay lower than 2^8.)
 constexpr int kGradTop = 8, kScaleTop = 6;
 __device__ __forceinline__ int scale_exponent(float top, int to) {
-    if (!(top > 0.f) || top > 3e38f) return 0;
+    if (!(top > 0.f) || top > 3.40282347e38f) return 0;
     const int e = to - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
-    return e < -100 ? -100 : e > 100 ? 100 : e;
+    return e > 126 ? 126 : e;
 }
 __device__ __forceinline__ float power_of_two(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ f32x4 times_power_of_two(const f32x4 v, int e) {
+    return f32x4{__builtin_ldexpf(v[0], e), __builtin_ldexpf(v[1], e), __builtin_ldexpf(v[2], e), __builtin_ldexpf(v[3], e)};
+}
 
 // Direct global -> LDS copies (global_load_lds): each lane's 4 or 16 bytes land at
 // M0 + 4*lane or M0 + 16*lane, M0 being uniform over the wave. They count in vmcnt

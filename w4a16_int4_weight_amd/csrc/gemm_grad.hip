@@ -379,10 +379,7 @@ __global__ __launch_bounds__(512) void grad_kernel(const GradArgs a) {
                 if (a.add) v += hot ? *o * a.before[m] : *o;
                 *o = v;
             } else {
-                if constexpr (kScaled) {
-                    v *= power_of_two(-scale_exponent(a.rowmax[m], kGradTop));
-                    v *= power_of_two(-we);
-                }
+                if constexpr (kScaled) v = times_power_of_two(v, -we - scale_exponent(a.rowmax[m], kGradTop));
                 const uint2 o = make_uint2(pack2_rne<kScaleBF16>(v[0], v[1]), pack2_rne<kScaleBF16>(v[2], v[3]));
                 *reinterpret_cast<uint2*>(a.dx + (size_t)m * a.K + k) = o;
             }
@@ -406,9 +403,9 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restric
         s1 += p[1];
     }
     if (rowmax) {
-        const float by = power_of_two(-scale_exponent(rowmax[at / K], kGradTop)), by2 = power_of_two(-we);
-        s0 = s0 * by * by2;
-        s1 = s1 * by * by2;
+        const int e = -we - scale_exponent(rowmax[at / K], kGradTop);
+        s0 = times_power_of_two(s0, e);
+        s1 = times_power_of_two(s1, e);
     }
     *reinterpret_cast<uint4*>(dx + at) = make_uint4(pack2_rne<kBF16>(s0[0], s0[1]), pack2_rne<kBF16>(s0[2], s0[3]),
                                                     pack2_rne<kBF16>(s1[0], s1[1]), pack2_rne<kBF16>(s1[2], s1[3]));
