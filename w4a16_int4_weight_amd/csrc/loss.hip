@@ -380,9 +380,10 @@ __global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
     const int m = (int)blockIdx.x * 16 + i;
     const int M = a.M;
     const int mc = m < M ? m : M - 1;
+    // (a maximum passes over what is no number; the sums carry it, also where nothing else is left)
     auto join = [](float2 v, float2 o) {
         const float top = fmaxf(v.x, o.x);
-        return top == -INFINITY ? v : make_float2(top, v.y * __expf(v.x - top) + o.y * __expf(o.x - top));
+        return make_float2(top, top == -INFINITY ? v.y + o.y : v.y * __expf(v.x - top) + o.y * __expf(o.x - top));
     };
     float2 v = make_float2(-INFINITY, 0.f);
     for (int t0 = g; t0 < a.tiles; t0 += 128) {           // 8 loads in flight

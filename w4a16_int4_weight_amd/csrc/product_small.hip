@@ -216,8 +216,8 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
                 if (m >= M || u >= hi || n >= a.N) continue;
                 const float z = total(buf, os, m, oc);
                 if (n == label[k]) a.zsel[m] = z;
-                const float t = fmaxf(top[k], z);
-                if (t != -INFINITY) sum[k] = sum[k] * __expf(top[k] - t) + __expf(z - t);
+                const float t = fmaxf(top[k], z);                // passes over what is no number: the sum carries it
+                if (top[k] != -INFINITY || z != -INFINITY) sum[k] = sum[k] * __expf(top[k] - t) + __expf(z - t);
                 top[k] = t;
             }
         }
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
             for (int s = 1; s < kCols * S; s *= 2) {
                 const float t2 = __shfl_xor(t, s), v2 = __shfl_xor(v, s);
                 const float m2 = fmaxf(t, t2);
-                if (m2 != -INFINITY) v = v * __expf(t - m2) + v2 * __expf(t2 - m2);
+                v = m2 == -INFINITY ? v + v2 : v * __expf(t - m2) + v2 * __expf(t2 - m2);
                 t = m2;
             }
             const int m = om + k * kRowStep;
