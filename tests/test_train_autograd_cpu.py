@@ -1,0 +1,64 @@
+"""The differentiable operations' own logic, on functions that stand in for the library's."""
+
+import pytest
+import torch
+
+from w4a16_int4_weight_amd import autograd as ops
+
+K, V = 128, 64
+
+
+class Losses:
+    """Stand-ins whose gradient is dloss[m] * base, rounded to x's type."""
+
+    def __init__(self, monkeypatch):
+        self.asked = []
+        monkeypatch.setattr(ops, "w4a16_cross_entropy", self.cross_entropy)
+        monkeypatch.setattr(ops, "w4a16_distill", self.distill)
+
+    def base(self, x):
+        return x.float() * 0.25 + 0.5
+
+    def cross_entropy(self, x, labels, packed, V, group_size, dloss=None, grad=False):
+        self.asked.append(grad)
+        M = x.shape[0]
+        out = (torch.arange(M, dtype=torch.float32), torch.zeros(M))
+        if not grad:
+            assert dloss is None
+            return out
+        d = torch.ones(M) if dloss is None else dloss
+        return (*out, (d[:, None] * self.base(x)).to(x.dtype))
+
+    def distill(self, x, ids, top, packed, V, group_size, temperature=1.0, dloss=None, grad=False):
+        return self.cross_entropy(x, ids, packed, V, group_size, dloss, grad)
+
+
+@pytest.fixture
+def losses(monkeypatch):
+    return Losses(monkeypatch)
+
+
+def both(x, weights=None, top=None):
+    """-> the two losses' calls on x [M, K]"""
+    M = x.shape[0]
+    labels, ids = torch.zeros(M, dtype=torch.int32), torch.zeros((M, 3), dtype=torch.int32)
+    top = torch.zeros((M, 3)) if top is None else top
+    return [lambda: ops.cross_entropy(x, labels, None, V, weights=weights),
+            lambda: ops.distill(x, ids, top, None, V, weights=weights)]
+
+
+@pytest.mark.parametrize("i", [0, 1])
+def test_no_gradient_where_none_is_asked_for(losses, i):
+    x = torch.randn((4, K)).to(torch.bfloat16).requires_grad_(True)
+    weights = torch.full((4,), 0.25)
+    with torch.no_grad():
+        assert not both(x, weights)[i]().requires_grad
+    with torch.inference_mode():
+        both(x, weights)[i]()
+    both(x.detach(), weights)[i]()
+    assert losses.asked == [False, False, False]
+    # a checkpoint's first pass forms none, its second does
+    from torch.utils.checkpoint import checkpoint
+    checkpoint(lambda v: both(v, weights)[i](), x, use_reentrant=True).sum().backward()
+    assert losses.asked[3:] == [False, True]
+    assert torch.equal(x.grad, (0.25 * losses.base(x)).to(x.dtype))

@@ -10,7 +10,7 @@ fp16 or bf16, [..., K]; a dimension of any size is met as rows. Each call runs o
 current stream, like the functions it is made of.
 
 The losses form x's gradient in the forward pass, where the head is read for the loss
-anyway, scaled by `weights` (float32 per row; None: 1). Give the rows' weights there
+anyway (not under no_grad, or for an x that requires none), scaled by `weights` (float32 per row; None: 1). Give the rows' weights there
 (1 / count for a mean, a loss scale for fp16) and sum what comes back: the backward pass
 then multiplies by one, which is exact. Another factor on a row is one more rounding.
 """
@@ -60,9 +60,8 @@ class _Gated(torch.autograd.Function):
 
 class _Loss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weights, call):
+    def forward(ctx, x, weights, call, grad):
         flat = _flat(x)
-        grad = ctx.needs_input_grad[0]
         if weights is not None:
             weights = weights.reshape(-1).contiguous()
         out = call(flat, grad, weights if grad else None)
@@ -76,7 +75,12 @@ class _Loss(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, g):
         dx, = ctx.saved_tensors
-        return (dx.float() * g.reshape(-1, 1)).to(dx.dtype).view(ctx.shape), None, None
+        return (dx.float() * g.reshape(-1, 1)).to(dx.dtype).view(ctx.shape), None, None, None
+
+
+def _loss(x, weights, call):
+    # (asked here: inside a Function an x that requires a gradient says so under no_grad too)
+    return _Loss.apply(x, weights, call, x.requires_grad and torch.is_grad_enabled())
 
 
 def linear(x, packed, N, group_size=128, bias=None):
@@ -94,7 +98,7 @@ def cross_entropy(x, labels, packed, V, group_size=128, weights=None):
     a label outside [0, V) has loss and gradient 0."""
     def call(flat, grad, dloss):
         return w4a16_cross_entropy(flat, labels.reshape(-1).contiguous(), packed, V, group_size, dloss=dloss, grad=grad)
-    return _Loss.apply(x, weights, call)
+    return _loss(x, weights, call)
 
 
 def distill(x, top_ids, top_logits, packed, V, group_size=128, temperature=1.0, weights=None):
@@ -102,4 +106,4 @@ def distill(x, top_ids, top_logits, packed, V, group_size=128, temperature=1.0, 
     def call(flat, grad, dloss):
         return w4a16_distill(flat, _flat(top_ids), _flat(top_logits), packed, V, group_size, temperature=temperature,
                              dloss=dloss, grad=grad)
-    return _Loss.apply(x, weights, call)
+    return _loss(x, weights, call)
