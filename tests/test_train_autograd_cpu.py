@@ -62,3 +62,20 @@ def test_no_gradient_where_none_is_asked_for(losses, i):
     checkpoint(lambda v: both(v, weights)[i](), x, use_reentrant=True).sum().backward()
     assert losses.asked[3:] == [False, True]
     assert torch.equal(x.grad, (0.25 * losses.base(x)).to(x.dtype))
+
+
+@pytest.mark.parametrize("need", [False, True])
+def test_constants_that_require_a_gradient_are_refused(losses, monkeypatch, need):
+    monkeypatch.setattr(ops, "w4a16_gemm", lambda x, packed, N, group_size, bias=None: torch.zeros((x.shape[0], N)))
+    x = torch.randn((4, K)).to(torch.bfloat16).requires_grad_(need)
+    weights, top = torch.ones(4, requires_grad=True), torch.zeros((4, 3), requires_grad=True)
+    bias = torch.zeros(V, requires_grad=True)
+    calls = [both(x, weights)[0], both(x, weights)[1], both(x, top=top)[1],
+             lambda: ops.linear(x, torch.zeros(1, dtype=torch.uint8), V, bias=bias)]
+    for call in calls:
+        with pytest.raises(ValueError, match="detach"):
+            call()
+        with torch.no_grad():
+            call()
+    for call in both(x, weights.detach(), top.detach()):
+        call()

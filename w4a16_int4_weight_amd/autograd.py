@@ -5,7 +5,8 @@
   cross_entropy(x, labels, packed, V, group_size, weights)  -> weights[m] * loss[m]
   distill(x, top_ids, top_logits, packed, V, group_size, temperature, weights)
 
-Gradients go to x alone: the weights, a bias and a teacher's logits are constants. x is
+Gradients go to x alone: the weights, a bias, the rows' weights and a teacher's logits are
+constants, and ValueError is raised for one that requires a gradient (detach it). x is
 fp16 or bf16, [..., K]; a dimension of any size is met as rows. Each call runs on the
 current stream, like the functions it is made of.
 
@@ -24,6 +25,12 @@ __all__ = ["linear", "gated", "cross_entropy", "distill"]
 
 def _flat(x):
     return x.reshape(-1, x.shape[-1]).contiguous()
+
+
+def _constant(t, name):
+    if t is not None and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} is a constant here and gets no gradient: detach it")
+    return t
 
 
 class _Linear(torch.autograd.Function):
@@ -80,12 +87,12 @@ class _Loss(torch.autograd.Function):
 
 def _loss(x, weights, call):
     # (asked here: inside a Function an x that requires a gradient says so under no_grad too)
-    return _Loss.apply(x, weights, call, x.requires_grad and torch.is_grad_enabled())
+    return _Loss.apply(x, _constant(weights, "weights"), call, x.requires_grad and torch.is_grad_enabled())
 
 
 def linear(x, packed, N, group_size=128, bias=None):
     """w4a16_gemm, with w4a16_gemm_grad as its backward pass."""
-    return _Linear.apply(x, packed, N, group_size, bias)
+    return _Linear.apply(x, packed, N, group_size, _constant(bias, "bias"))
 
 
 def gated(x, packed, F, group_size=128, act="silu"):
@@ -103,6 +110,8 @@ def cross_entropy(x, labels, packed, V, group_size=128, weights=None):
 
 def distill(x, top_ids, top_logits, packed, V, group_size=128, temperature=1.0, weights=None):
     """w4a16_distill: weights[m] * loss[m], float32. top_ids, top_logits [..., T]."""
+    _constant(top_logits, "top_logits")
+
     def call(flat, grad, dloss):
         return w4a16_distill(flat, _flat(top_ids), _flat(top_logits), packed, V, group_size, temperature=temperature,
                              dloss=dloss, grad=grad)
