@@ -79,3 +79,20 @@ def test_constants_that_require_a_gradient_are_refused(losses, monkeypatch, need
             call()
     for call in both(x, weights.detach(), top.detach()):
         call()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("scale", [1.0, 65536.0])
+@pytest.mark.parametrize("weight", [2.0 ** -13, 1e-7, 1.0 / 24576, 0.0, 0.75])
+def test_a_scale_on_the_loss_reaches_small_gradients(losses, dtype, scale, weight):
+    # one rounding of weight * base, relative: half a step of the type; where the result with
+    # the scale is below the type's normal range, half a step there
+    x = torch.randn((6, K)).clamp(-1, 1).to(dtype).requires_grad_(True)
+    weights = torch.full((6,), weight)
+    info = torch.finfo(dtype)
+    for i in (0, 1):
+        x.grad = None
+        (both(x, weights)[i]().sum() * scale).backward()
+        want = losses.base(x.detach()).double() * float(weights[0]) * scale
+        err = (x.grad.double() - want).abs()
+        assert (err <= info.eps / 2 * want.abs() * 1.001 + info.tiny * info.eps / 2 * 1.001).all()

@@ -12,8 +12,11 @@ current stream, like the functions it is made of.
 
 The losses form x's gradient in the forward pass, where the head is read for the loss
 anyway (not under no_grad, or for an x that requires none), scaled by `weights` (float32 per row; None: 1). Give the rows' weights there
-(1 / count for a mean, a loss scale for fp16) and sum what comes back: the backward pass
-then multiplies by one, which is exact. Another factor on a row is one more rounding.
+(1 / count for a mean) and sum what comes back: the backward pass then multiplies by one,
+which is exact. A power of two on the loss (a gradient scaler's) is exact too; another
+factor on a row is one more rounding. fp16 keeps the gradient at its weight's mantissa and
+takes the weight's power of two into the backward pass, with the loss's own factor: what
+1 / count makes too small for fp16 is whole again under a loss scale.
 """
 
 import torch
@@ -71,18 +74,24 @@ class _Loss(torch.autograd.Function):
         flat = _flat(x)
         if weights is not None:
             weights = weights.reshape(-1).contiguous()
-        out = call(flat, grad, weights if grad else None)
+        dloss, power = weights, None
+        if grad and weights is not None and x.dtype == torch.float16:
+            dloss, power = torch.frexp(weights)
+        out = call(flat, grad, dloss if grad else None)
         ctx.shape = x.shape
         if grad:
-            ctx.save_for_backward(out[2])
+            ctx.save_for_backward(out[2], power)
         loss = out[0] if weights is None else out[0] * weights
         return loss.view(x.shape[:-1])
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g):
-        dx, = ctx.saved_tensors
-        return (dx.float() * g.reshape(-1, 1)).to(dx.dtype).view(ctx.shape), None, None, None
+        dx, power = ctx.saved_tensors
+        g = g.reshape(-1)
+        if power is not None:
+            g = torch.ldexp(g, power)
+        return (dx.float() * g[:, None]).to(dx.dtype).view(ctx.shape), None, None, None
 
 
 def _loss(x, weights, call):
