@@ -96,3 +96,12 @@ def test_a_scale_on_the_loss_reaches_small_gradients(losses, dtype, scale, weigh
         want = losses.base(x.detach()).double() * float(weights[0]) * scale
         err = (x.grad.double() - want).abs()
         assert (err <= info.eps / 2 * want.abs() * 1.001 + info.tiny * info.eps / 2 * 1.001).all()
+
+
+def test_linear_refuses_what_is_elsewhere(monkeypatch):
+    monkeypatch.setattr(ops, "w4a16_gemm", lambda *args, **more: pytest.fail("called"))
+    x, packed = torch.zeros((4, K), dtype=torch.bfloat16), torch.zeros(1 << 15, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="bias"):
+        ops.linear(x, packed, V, bias=torch.zeros(V, dtype=torch.bfloat16, device="meta"))
+    with pytest.raises(ValueError, match="packed"):
+        ops.linear(x, packed.to("meta"), V)

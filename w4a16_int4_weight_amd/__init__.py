@@ -424,11 +424,9 @@ def _workspace_of_capture(key, capture, nbytes, device, stream):
 
 def _raw_stream(stream, device):
     """The hipStream_t of `stream`, or of the device's current stream, as an integer."""
-    if stream is None:
-        if device.type == "cuda":
-            return torch._C._cuda_getCurrentRawStream(device.index)
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, not on {device}")
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _launch(name, args, workspace, need, device, stream, more=()):
@@ -617,6 +615,15 @@ def _rows(t, name):
     return t.shape
 
 
+def _beside(x, **tensors):
+    """ValueError for a tensor (None: not given) that is not where x is: the kernels get bare
+    addresses, and one of host memory would fault the GPU."""
+    device = x.device
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, not on {t.device}")
+
+
 def _result(t, name, shape, dtype, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
@@ -635,6 +642,7 @@ def w4a16_gemm_grad(dy, packed, K, group_size=128, dx=None, workspace=None, stre
     """dy [M, N] (fp16/bf16) times the transposed packed [K, N] weight -> dx [M, K]: the
     gradient of w4a16_gemm with respect to x."""
     M, N = _rows(dy, "dy")
+    _beside(dy, packed=packed, dx=dx, workspace=workspace)
     dx = _result(dx, "dx", (M, K), dy.dtype, dy.device)
     _launch("w4a16_gemm_grad",
             (dy.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(dy.dtype), dx.data_ptr(), M, K, N, group_size),
@@ -652,6 +660,7 @@ def w4a16_gated(x, packed, F, group_size=128, act="silu", h=None, workspace=None
     """Gated feed-forward block on one packed [K, 2F] weight (gate columns, then up):
     x [M, K] -> h [M, F] = act(x Wg) * (x Wu). act: "silu", "gelu" or "gelu_tanh"."""
     M, K = _rows(x, "x")
+    _beside(x, packed=packed, h=h, workspace=workspace)
     h = _result(h, "h", (M, F), x.dtype, x.device)
     _launch("w4a16_gated",
             (x.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(x.dtype), h.data_ptr(), M, K, F, group_size,
@@ -665,6 +674,7 @@ def w4a16_gated_grad(x, dh, packed, F, group_size=128, act="silu", dx=None, work
     M, K = _rows(x, "x")
     if _rows(dh, "dh") != (M, F) or dh.dtype != x.dtype:
         raise ValueError("dh must be a contiguous [M, F] tensor of x's dtype")
+    _beside(x, dh=dh, packed=packed, dx=dx, workspace=workspace)
     dx = _result(dx, "dx", (M, K), x.dtype, x.device)
     _launch("w4a16_gated_grad",
             (x.data_ptr(), dh.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(x.dtype), dx.data_ptr(), M, K, F,
@@ -695,6 +705,7 @@ def w4a16_cross_entropy(x, labels, packed, V, group_size=128, dloss=None, grad=F
     M, K, loss, lse, dx = _loss_args(x, dloss, grad, loss, lse, dx)
     if tuple(labels.shape) != (M,) or labels.dtype != torch.int32 or not labels.is_contiguous():
         raise ValueError("labels must be a contiguous int32 [M] tensor")
+    _beside(x, labels=labels, packed=packed, dloss=dloss, loss=loss, lse=lse, dx=dx, workspace=workspace)
     _launch("w4a16_cross_entropy",
             (x.data_ptr(), labels.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(x.dtype), M, K, V, group_size,
              None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(), dx.data_ptr() if grad else None),
@@ -714,6 +725,8 @@ def w4a16_distill(x, top_ids, top_logits, packed, V, group_size=128, temperature
         raise ValueError("top_ids must be an int32 [M, T] tensor")
     if _rows(top_logits, "top_logits") != (M, T) or top_logits.dtype != torch.float32:
         raise ValueError("top_logits must be a float32 [M, T] tensor")
+    _beside(x, top_ids=top_ids, top_logits=top_logits, packed=packed, dloss=dloss, loss=loss, lse=lse, dx=dx,
+            workspace=workspace)
     _launch("w4a16_distill",
             (x.data_ptr(), top_ids.data_ptr(), top_logits.data_ptr(), packed.data_ptr(), packed.nbytes, _dtype_code(x.dtype),
              M, K, V, group_size, T, temperature, None if dloss is None else dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(),

@@ -21,7 +21,7 @@ takes the weight's power of two into the backward pass, with the loss's own fact
 
 import torch
 
-from . import w4a16_cross_entropy, w4a16_distill, w4a16_gated, w4a16_gated_grad, w4a16_gemm, w4a16_gemm_grad
+from . import _beside, w4a16_cross_entropy, w4a16_distill, w4a16_gated, w4a16_gated_grad, w4a16_gemm, w4a16_gemm_grad
 
 __all__ = ["linear", "gated", "cross_entropy", "distill"]
 
@@ -101,6 +101,7 @@ def _loss(x, weights, call):
 
 def linear(x, packed, N, group_size=128, bias=None):
     """w4a16_gemm, with w4a16_gemm_grad as its backward pass."""
+    _beside(x, packed=packed, bias=bias)
     return _Linear.apply(x, packed, N, group_size, _constant(bias, "bias"))
 
 
