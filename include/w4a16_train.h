@@ -72,7 +72,10 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
  *   dx      [M, K] `dtype`, written in full, or NULL: no gradient. 16-byte aligned.
  * The vocabulary is taken in pieces: the largest buffer holds the unnormalised
  * probabilities of one piece (`dtype`, at most 256 MiB, 4096 rows at a time). The target
- * columns' part of dx is taken in fp32. No pointer may overlap another that is written. */
+ * columns' part of dx is taken in fp32. A row's label is left out of its sum, so that the
+ * loss, log(1 + sum_{v != label} e^{z_v - z_label}), is never negative, and small losses and
+ * gradients are right relative to themselves. No pointer may overlap another that is
+ * written. */
 size_t w4a16_cross_entropy_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t group_size, int grad);
 w4a16_status w4a16_cross_entropy(const void* x, const int32_t* labels, const void* packed, size_t packed_bytes,
                                  w4a16_dtype dtype, int64_t M, int64_t K, int64_t V, int64_t group_size,

@@ -23,6 +23,10 @@
 // is 8 times finer than bf16's rounding).
 // The targets' columns are zero in P and enter at the end in fp32, (q_t - p_t) W_t: for a
 // confident row that difference is small, and of two rounded numbers it would be lost.
+// A row's only target is left out of its tiles' sums too: with w = sum_{v != t} e^{z_v - z_t}
+// the loss is log(1 + w) and q_t - 1 = -w / (1 + w), neither a difference of large numbers
+// (lse - z_t, two sums of different order, came out at -1.5e-5 for losses of 1e-9, and 19%
+// off at 2e-3 where logits are in the hundreds).
 //
 // Roundings: P once and W once, to the operand type; dx once. Measured on 4096 x 2048 x
 // 131072 with its gradient: 9490 us with the tile formed twice and the scheduling left to
@@ -43,6 +47,7 @@ struct LossArgs {
     float inv_tau;
     float2* part;            // [tiles_n][M] (reference, sum) of a tile's row, from this launch's first tile
     const float* ref;        // [M]
+    const int32_t* only;     // [M] the column of a row's only target, left out (or -1), or NULL
     uint16_t* q;             // [M, ldq] P
     int ldq;
     const int32_t* live;     // [M] whether the row has a target, and so a gradient
@@ -72,6 +77,27 @@ __device__ __forceinline__ void loss_epilogue(const LossArgs& a, typename P::Sha
     for (int r = 0; r < P::MR; ++r) {
         const int m = m0 + 16 * r + c;
         ref[r] = a.ref[m < M ? m : M - 1];
+    }
+    if (a.only) {
+        // a target lies in few waves' columns (128 rows x 32 columns of 131072: in 3% of them)
+        int at[P::MR];
+        bool mine = false;
+#pragma unroll
+        for (int r = 0; r < P::MR; ++r) {
+            const int m = m0 + 16 * r + c;
+            at[r] = a.only[m < M ? m : M - 1] - nw;
+            mine |= (unsigned)at[r] < 16u * P::CBW;
+        }
+        if (__any(mine)) {
+#pragma unroll
+            for (int r = 0; r < P::MR; ++r) {
+                if (!__any((unsigned)at[r] < 16u * P::CBW)) continue;
+#pragma unroll
+                for (int j = 0; j < P::CBW; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][j][e] = at[r] == 16 * j + 4 * h + e ? -INFINITY : acc[r][j][e];
+            }
+        }
     }
     auto emit = [&](const float* rf) -> bool {       // true: a sum is out of range (or no number)
         bool high = false;
@@ -315,6 +341,7 @@ __global__ __launch_bounds__(256) void targets_kernel(const TargetArgs a) {
             if (i < j) first = false;
             p += sp[i];
         }
+        if (T == 1 && p == 0.f) first = false;       // (an only target that weighs nothing is none)
         first_id[j] = first ? id : -1;
         a.out_ids[(size_t)m * T + j] = first ? id : -1;
         a.weight[(size_t)m * T + j] = first ? p : 0.f;
@@ -346,8 +373,8 @@ __global__ __launch_bounds__(256) void targets_kernel(const TargetArgs a) {
     }
 }
 
-// Between a piece's two products: the targets' places in P become zero, and where a tile
-// took a reference of its own the rows' tiles are given the factors that bring them, and
+// Between a piece's two products: the targets' places in P become zero (T = 0: they are),
+// and where a tile took a reference of its own the rows' tiles are given the factors that bring them, and
 // the sums of the pieces before, to the row's highest reference.
 __global__ __launch_bounds__(256) void settle_kernel(const int32_t* __restrict__ ids, int M, int T, int N, int n0, int n,
                                                      uint16_t* __restrict__ q, int ldq, const int* __restrict__ hot,
@@ -385,6 +412,8 @@ struct RowArgs {
     float* gain;             // [M] the factor of P W^T in dx
     const float* ref;        // [M] P's reference (bf16) ...
     float* next_ref;         // ... or that of the P to come (fp16)
+    int only;                // the sums leave out a row's only target
+    float* rest;             // [M] then: q_t - 1
 };
 __global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
     __shared__ float2 sv[16][17];
@@ -392,6 +421,13 @@ __global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
     const int m = (int)blockIdx.x * 16 + i;
     const int M = a.M;
     const int mc = m < M ? m : M - 1;
+    bool live = false;
+    float z = 0.f;
+    if (a.only && g == 0) {
+        const int id = a.ids[mc];
+        live = id >= 0 && id < a.N;
+        if (live) z = a.zsel[mc];
+    }
     // (a maximum passes over what is no number; the sums carry it, also where nothing else is left)
     auto join = [](float2 v, float2 o) {
         const float top = fmaxf(v.x, o.x);
@@ -412,13 +448,41 @@ __global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
     __syncthreads();
     v = sv[0][i];
     for (int k = 1; k < 16; ++k) v = join(v, sv[k][i]);
-    const float lse = v.x + logf(v.y);
+    float lse = v.x + logf(v.y);
+    if (a.only) {
+        if (g != 0 || m >= M) return;
+        const float others = lse;                // log of the sum without the target
+        float loss = 0.f;
+        if (live) {
+            const float far = v.x - z;
+            lse = far > 0.f ? v.x + logf(v.y + __expf(-far)) : z + log1pf(v.y * __expf(far));
+            loss = far > 30.f ? lse - z : log1pf(v.y * __expf(far));
+        }
+        const float p = a.weight && live ? a.weight[m] : 1.f;        // 1, or no number
+        a.loss[m] = a.tau * a.tau * loss * p;
+        a.lse[m] = lse;
+        if (a.coef) {
+            const float cf = live ? a.tau * (a.dloss ? a.dloss[m] : 1.f) * p : 0.f;
+            const float rest = expm1f(-loss);
+            a.coef[m] = cf;
+            a.rest[m] = rest;
+            if (a.next_ref) {
+                // 2^15 of what the others have: the largest of them fills fp16 however little it is
+                const bool some = others - lse > -60.f;
+                a.next_ref[m] = (some ? others : lse) - kShiftBits * 0.6931471806f;
+                a.gain[m] = cf * (some && live ? -rest : 1.f) * (1.f / (1 << kShiftBits));
+            } else {
+                a.gain[m] = cf * __expf(a.ref[m] - lse);
+            }
+        }
+        return;
+    }
     __syncthreads();
     float sum = 0.f, mass = 0.f;
     for (int j = g; j < a.T; j += 16) {
         const int id = a.ids[(size_t)mc * a.T + j];
         if (id < 0 || id >= a.N) continue;
-        const float p = a.weight ? a.weight[(size_t)mc * a.T + j] : 1.f;
+        const float p = a.weight[(size_t)mc * a.T + j];
         if (p == 0.f) continue;
         sum += p * (lse - a.zsel[(size_t)mc * a.T + j]);
         mass += p;
@@ -432,12 +496,12 @@ __global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
             sum += sv[k][i].x;
             mass += sv[k][i].y;
         }
-        const bool live = mass != 0.f;
-        if (a.ent) sum += a.ent[m];
-        a.loss[m] = live ? a.tau * a.tau * sum : 0.f;
+        const bool some = mass != 0.f;
+        sum += a.ent[m];
+        a.loss[m] = some ? a.tau * a.tau * sum : 0.f;
         a.lse[m] = lse;
         if (a.coef) {
-            const float cf = live ? a.tau * (a.dloss ? a.dloss[m] : 1.f) : 0.f;
+            const float cf = some ? a.tau * (a.dloss ? a.dloss[m] : 1.f) : 0.f;
             a.coef[m] = cf;
             a.gain[m] = a.next_ref ? cf * (1.f / (1 << kShiftBits)) : cf * __expf(a.ref[m] - lse);
             if (a.next_ref) a.next_ref[m] = lse - kShiftBits * 0.6931471806f;
@@ -453,6 +517,7 @@ struct FinishArgs {
     int splits, M, K, N, T, UW, sub;
     const uint8_t* packed;
     const float *coef, *gain, *lse, *zsel, *weight;
+    const float* rest;       // q_t - 1 of a row's only target, or NULL
     const int32_t* ids;
     uint16_t* dx;
 };
@@ -470,8 +535,8 @@ __global__ __launch_bounds__(256) void finish_kernel(const FinishArgs a) {
         const int id = a.ids[(size_t)m * a.T + j];
         const bool ok = id >= 0 && id < a.N;
         sid[j] = ok ? id : 0;
-        sc[j] = ok ? coef * (__expf(a.zsel[(size_t)m * a.T + j] - a.lse[m]) - (a.weight ? a.weight[(size_t)m * a.T + j] : 1.f))
-                   : 0.f;
+        const size_t at_j = (size_t)m * a.T + j;
+        sc[j] = !ok ? 0.f : coef * (a.rest ? a.rest[m] : __expf(a.zsel[at_j] - a.lse[m]) - a.weight[at_j]);
     }
     __syncthreads();
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -561,7 +626,7 @@ struct LossLayout {
     GradPlan grad;
     int64_t piece, pieces;
     bool small;              // up to 16 rows without a gradient: one kernel before the rows'
-    size_t hot, partials, part, zsel, ids, weight, ent, coef, gain, ref, live, factor, before, q, gpart, end;
+    size_t hot, partials, part, zsel, ids, weight, ent, coef, gain, rest, ref, live, factor, before, q, gpart, end;
 };
 
 int64_t tile_columns(const ProductPlan& p) { return 128 * p.cbw; }
@@ -603,6 +668,7 @@ LossLayout loss_layout(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bo
     l.ent = take(distill ? (size_t)M * 4 : 0);
     l.coef = take((size_t)M * 4);
     l.gain = take((size_t)M * 4);
+    l.rest = take(grad && T == 1 ? (size_t)M * 4 : 0);
     l.ref = take((size_t)M * 4);
     l.live = take(grad && bf16 ? (size_t)M * 4 : 0);
     l.factor = take(grad && bf16 ? (size_t)l.prob.tiles_n * M * 4 : 0);
@@ -636,6 +702,7 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
     const bool distill = q.top != nullptr;
     const bool grad = q.dx != nullptr;
     const bool sums_first = !grad || !q.bf16;
+    const bool only = q.T == 1;
     for (int64_t r0 = 0; r0 < q.M; r0 += kRowsPerPass) {
         const int64_t M = q.M - r0 < kRowsPerPass ? q.M - r0 : kRowsPerPass;
         const LossLayout l = loss_layout(M, q.K, q.V, q.G, q.T, q.bf16, distill, grad);
@@ -684,6 +751,7 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
         a.p.partials = floats(l.partials);
         a.inv_tau = t.inv_tau;
         a.ref = ref;
+        a.only = only ? ids : nullptr;
         a.live = t.live;
         a.hot = hot;
         auto product = [&](const ProductPlan& p, int64_t n0, int64_t n, bool prob) {
@@ -704,12 +772,14 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
         rows.ent = t.ent;
         rows.zsel = t.zsel;
         rows.tau = q.tau;
+        rows.only = only;
         rows.dloss = q.dloss ? q.dloss + r0 : nullptr;
         rows.loss = q.loss + r0;
         rows.lse = q.lse + r0;
         if (grad) {
             rows.coef = floats(l.coef);
             rows.gain = floats(l.gain);
+            rows.rest = floats(l.rest);
             rows.ref = ref;
             if (!q.bf16) rows.next_ref = ref;
         }
@@ -738,9 +808,10 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
             const ProductPlan p = n == l.piece ? l.prob : plan_product(M, q.K, n, q.G, false);
             a.part = part + (size_t)tiles * M;
             product(p, n0, n, true);
-            hipLaunchKernelGGL(settle_kernel, dim3((unsigned)((M * q.T + 255) / 256)), dim3(256), 0, stream, ids, (int)M, (int)q.T,
-                               (int)q.V, (int)n0, (int)n, a.q, a.ldq, hot, a.part, p.tiles_n, ref, floats(l.factor),
-                               floats(l.before));
+            if (!only || hot)
+                hipLaunchKernelGGL(settle_kernel, dim3((unsigned)((M * q.T + 255) / 256)), dim3(256), 0, stream, ids, (int)M,
+                                   only ? 0 : (int)q.T, (int)q.V, (int)n0, (int)n, a.q, a.ldq, hot, a.part, p.tiles_n, ref,
+                                   floats(l.factor), floats(l.before));
             tiles += p.tiles_n;
             GradCall g{};
             g.d = a.q;
@@ -781,6 +852,7 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
         f.lse = rows.lse;
         f.zsel = t.zsel;
         f.weight = t.weight;
+        f.rest = only ? rows.rest : nullptr;
         f.ids = ids;
         f.dx = q.dx + r0 * q.K;
         // shared where a thread alone would meet 16 loads or more (65 rows, 20 targets, 64

@@ -214,8 +214,11 @@ __global__ __launch_bounds__(kThreads) void small_kernel(const SmallArgs a) {
             for (int k = 0; k < kSlots; ++k) {
                 const int m = om + k * kRowStep, n = 16 * u + oc;
                 if (m >= M || u >= hi || n >= a.N) continue;
-                const float z = total(buf, os, m, oc);
-                if (n == label[k]) a.zsel[m] = z;
+                float z = total(buf, os, m, oc);
+                if (n == label[k]) {
+                    a.zsel[m] = z;
+                    z = -INFINITY;                               // the target is left out of the sum
+                }
                 const float t = fmaxf(top[k], z);                // passes over what is no number: the sum carries it
                 if (top[k] != -INFINITY || z != -INFINITY) sum[k] = sum[k] * __expf(top[k] - t) + __expf(z - t);
                 top[k] = t;
