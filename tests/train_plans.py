@@ -5,7 +5,7 @@ import ctypes
 
 
 class _Product(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int) for n in ("mr", "cbw", "sub", "tiles_m", "tiles_n", "splits")] + [("bytes", ctypes.c_size_t)]
+    _fields_ = [(n, ctypes.c_int) for n in ("mr", "sub", "tiles_m", "tiles_n", "splits")] + [("bytes", ctypes.c_size_t)]
 
 
 class _Grad(ctypes.Structure):

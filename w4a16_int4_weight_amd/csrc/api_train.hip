@@ -68,7 +68,7 @@ struct GatedLayout {
 
 // one pass over M rows: the forward's K-split partials and, for the gradient, dg | du and
 // the transposed product's partials
-GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) {
+GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad, bool bf16) {
     GatedLayout l{};
     const size_t partial = w4a16::plan_product(M, K, 2 * F, G, true).partial_bytes;
     l.partials = w4a16::kSplitCounterBytes;
@@ -84,8 +84,8 @@ GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) 
         at += round256(w4a16::kScaleParts * 4);
         l.d = at;
         at += round256((size_t)M * 4 * F);
-        l.d_rest = at;                    // (fp16; one size for both types)
-        if (w4a16::grad_takes_rest(w4a16::plan_grad(M, K, 2 * F, false), false)) at += round256((size_t)M * 4 * F);
+        l.d_rest = at;
+        if (w4a16::grad_takes_rest(w4a16::plan_grad(M, K, 2 * F, false), bf16)) at += round256((size_t)M * 4 * F);
         l.d32 = at;
         if (w4a16::small_product(M, K)) at += round256((size_t)M * 8 * F);
         l.gpart = at;
@@ -97,12 +97,13 @@ GatedLayout gated_layout(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) 
     return l;
 }
 
+// (of both types: fp16's, which may keep d_rest)
 size_t gated_workspace(int64_t M, int64_t K, int64_t F, int64_t G, bool grad) {
-    if (!grad) return gated_layout(M, K, F, G, false).end;
+    if (!grad) return gated_layout(M, K, F, G, false, false).end;
     const int64_t full = M < kGatedRowsPerPass ? M : kGatedRowsPerPass;
-    size_t need = gated_layout(full, K, F, G, true).end;
+    size_t need = gated_layout(full, K, F, G, true, false).end;
     if (M > full && M % full) {
-        const size_t tail = gated_layout(M % full, K, F, G, true).end;
+        const size_t tail = gated_layout(M % full, K, F, G, true, false).end;
         if (tail > need) need = tail;
     }
     return need;
@@ -229,7 +230,7 @@ w4a16_status w4a16_gated(const void* x, const void* packed, size_t packed_bytes,
     if (st != W4A16_OK) return st;
     st = check_device();
     if (st != W4A16_OK) return st;
-    const GatedLayout l = gated_layout(M, K, F, G, false);
+    const GatedLayout l = gated_layout(M, K, F, G, false, dtype == W4A16_BF16);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     w4a16::GatedCall q{};
     q.x = static_cast<const uint16_t*>(x);
@@ -267,7 +268,7 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
     hipStream_t s = static_cast<hipStream_t>(stream);
     for (int64_t r0 = 0; r0 < M; r0 += kGatedRowsPerPass) {
         const int64_t rows = M - r0 < kGatedRowsPerPass ? M - r0 : kGatedRowsPerPass;
-        const GatedLayout l = gated_layout(rows, K, F, G, true);
+        const GatedLayout l = gated_layout(rows, K, F, G, true, bf16);
         w4a16::GatedCall q{};
         q.x = static_cast<const uint16_t*>(x) + r0 * K;
         q.dh = static_cast<const uint16_t*>(dh) + r0 * F;
@@ -298,7 +299,7 @@ w4a16_status w4a16_gated_grad(const void* x, const void* dh, const void* packed,
         g.scaled = true;
         g.d_rest = q.d_rest;
         g.rowmax = rowmax;
-        g.tile_columns = w4a16::gated_tile_columns(rows, K, F, G);
+        g.tile_columns = w4a16::gated_tile_columns(rows, K);
         g.tile_factor = g.tile_columns ? reinterpret_cast<uint32_t*>(ws + l.factor) : nullptr;
         g.scale_max = scale_max;
         g.ld = 2 * F;

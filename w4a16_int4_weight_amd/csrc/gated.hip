@@ -240,9 +240,9 @@ __global__ __launch_bounds__(256) void convert_kernel(const float* __restrict__ 
         make_uint4(rest(lo[0], lo[1], o.x), rest(lo[2], lo[3], o.y), rest(hi[0], hi[1], o.z), rest(hi[2], hi[3], o.w));
 }
 
-template <bool kBF16, int MR, int CBW, int kSub, bool kGrad>
+template <bool kBF16, int MR, int kSub, bool kGrad>
 void launch_cfg(GatedArgs& a, hipStream_t s) {
-    using P = TileProduct<kBF16, MR, CBW, 8, kSub, true>;
+    using P = TileProduct<kBF16, MR, kProductColumns / 128, 8, kSub, true>;
     const int64_t ids = product_ids(a.p.tiles_m, a.p.tiles_n, a.p.splits);
     hipLaunchKernelGGL((gated_kernel<P, kGrad>), dim3((unsigned)ids), dim3(P::kThreads), 0, s, a);
 }
@@ -250,17 +250,17 @@ void launch_cfg(GatedArgs& a, hipStream_t s) {
 template <bool kBF16, bool kGrad>
 void launch_typed(const ProductPlan& p, GatedArgs& a, hipStream_t s) {
     if (p.sub == 4) {
-        if (p.mr == 1) launch_cfg<kBF16, 1, 2, 4, kGrad>(a, s);
-        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 4, kGrad>(a, s);
-        else launch_cfg<kBF16, 4, 2, 4, kGrad>(a, s);
+        if (p.mr == 1) launch_cfg<kBF16, 1, 4, kGrad>(a, s);
+        else if (p.mr == 2) launch_cfg<kBF16, 2, 4, kGrad>(a, s);
+        else launch_cfg<kBF16, 4, 4, kGrad>(a, s);
     } else if (p.sub == 2) {
-        if (p.mr == 1) launch_cfg<kBF16, 1, 2, 2, kGrad>(a, s);
-        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 2, kGrad>(a, s);
-        else launch_cfg<kBF16, 4, 2, 2, kGrad>(a, s);
-    } else if (p.mr == 1) launch_cfg<kBF16, 1, 2, 1, kGrad>(a, s);
-    else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 1, kGrad>(a, s);
-    else if (p.mr == 4) launch_cfg<kBF16, 4, 2, 1, kGrad>(a, s);
-    else launch_cfg<kBF16, 8, 2, 1, kGrad>(a, s);
+        if (p.mr == 1) launch_cfg<kBF16, 1, 2, kGrad>(a, s);
+        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, kGrad>(a, s);
+        else launch_cfg<kBF16, 4, 2, kGrad>(a, s);
+    } else if (p.mr == 1) launch_cfg<kBF16, 1, 1, kGrad>(a, s);
+    else if (p.mr == 2) launch_cfg<kBF16, 2, 1, kGrad>(a, s);
+    else if (p.mr == 4) launch_cfg<kBF16, 4, 1, kGrad>(a, s);
+    else launch_cfg<kBF16, 8, 1, kGrad>(a, s);
 }
 
 }  // namespace
@@ -280,32 +280,30 @@ ProductPlan plan_product(int64_t M, int64_t K, int64_t cols, int64_t G, bool gat
         const int64_t want = kTargetWorkgroups / tiles, most = KB / 4;
         return want < most ? want : most;
     };
-    struct Shape { int mr, cbw; double rate; };
+    struct Shape { int mr; double rate; };
     // finer groups scale each fragment 2 or 4 times; their 128-row tile does not fit in LDS
-    static constexpr Shape kShapes[] = {{8, 2, 0.85}, {4, 2, 0.7}, {2, 2, 0.5}};
+    static constexpr Shape kShapes[] = {{8, 0.85}, {4, 0.7}, {2, 0.5}};
     if (M <= 16) {
         p.mr = 1;
-        p.cbw = 2;
     } else {
         double best = 0.0;
         for (const Shape& c : kShapes) {
             if (c.mr == 8 && (p.sub > 1 || M <= 64)) continue;
             const int64_t tm = (M + 16 * c.mr - 1) / (16 * c.mr);
-            const int64_t tn = (cols + 128 * c.cbw - 1) / (128 * c.cbw);
+            const int64_t tn = (cols + kProductColumns - 1) / kProductColumns;
             const int64_t tiles = tm * tn, rounds = (tiles + kTargetWorkgroups - 1) / kTargetWorkgroups;
             const int64_t splits = splits_of(tiles);
             // a 128-row tile takes 2.1 us a row block; a tile's start and end as much as one,
             // a split's meeting by its partial tiles
-            const double cost = (double)rounds * ((double)KB / (double)splits * c.mr * c.cbw / c.rate + 20.0 +
+            const double cost = (double)rounds * ((double)KB / (double)splits * c.mr * 2.0 / c.rate + 20.0 +
                                                   (splits > 1 ? 4.0 * c.mr * (double)splits : 0.0));
             if (best == 0.0 || cost < best) {
                 best = cost;
                 p.mr = c.mr;
-                p.cbw = c.cbw;
             }
         }
     }
-    const int64_t width = 128 * p.cbw;      // weight columns of a tile
+    constexpr int64_t width = kProductColumns;
     p.tiles_m = (int)((M + 16 * p.mr - 1) / (16 * p.mr));
     p.tiles_n = (int)(gated ? (cols / 2 + width / 2 - 1) / (width / 2) : (cols + width - 1) / width);
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
@@ -319,8 +317,8 @@ int gated_tiles(int64_t M, int64_t K, int64_t F, int64_t G) {
     return small_product(M, K) ? small_workgroups(F / 8) : plan_product(M, K, 2 * F, G, true).tiles_n;
 }
 
-int gated_tile_columns(int64_t M, int64_t K, int64_t F, int64_t G) {
-    return small_product(M, K) ? 0 : 64 * plan_product(M, K, 2 * F, G, true).cbw;
+int gated_tile_columns(int64_t M, int64_t K) {
+    return small_product(M, K) ? 0 : kProductColumns / 2;
 }
 
 hipError_t launch_gated_tops(const GatedCall& q, float* rowmax, uint32_t* factor, float* scale_max, hipStream_t stream) {

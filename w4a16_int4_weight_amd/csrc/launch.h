@@ -111,9 +111,10 @@ hipError_t launch_w4a8_gemm(const W4A8Act& a, const uint8_t* packed, const uint1
                             int64_t K, int64_t N, int64_t G, bool bf16, void* workspace, hipStream_t stream);
 
 // Tiles of the training and scoring products (csrc/tile_product.h): `cols` columns of the
-// weight (2F for a gated block), 8 waves of cbw column blocks, 16 mr rows.
+// weight (2F for a gated block), 16 mr rows and 256 columns (8 waves of 2 column blocks) each.
+constexpr int kProductColumns = 256;
 struct ProductPlan {
-    int mr, cbw, sub;
+    int mr, sub;
     int tiles_m, tiles_n, splits;
     size_t partial_bytes;  // fp32 partial tiles of a K split (0 without one)
 };
@@ -139,7 +140,7 @@ struct GatedCall {
 };
 hipError_t launch_gated(const GatedCall& call, hipStream_t stream);
 int gated_tiles(int64_t M, int64_t K, int64_t F, int64_t G);
-int gated_tile_columns(int64_t M, int64_t K, int64_t F, int64_t G);       // 0: d's rows have one scale
+int gated_tile_columns(int64_t M, int64_t K);       // 0: d's rows have one scale
 // Between a backward's products: the rows' largest |d| from `tops`, the factors [tile][M] (two
 // fp16) that bring the tiles to their row's scale, and the largest |scale| of the weight in
 // kScaleParts parts.

@@ -587,9 +587,9 @@ __global__ __launch_bounds__(256) void finish_kernel(const FinishArgs a) {
     }
 }
 
-template <bool kBF16, int MR, int CBW, int kSub, bool kProb>
+template <bool kBF16, int MR, int kSub, bool kProb>
 void launch_cfg(LossArgs& a, hipStream_t s) {
-    using P = TileProduct<kBF16, MR, CBW, 8, kSub, false>;
+    using P = TileProduct<kBF16, MR, kProductColumns / 128, 8, kSub, false>;
     const int64_t ids = product_ids(a.p.tiles_m, a.p.tiles_n, a.p.splits);
     hipLaunchKernelGGL((loss_kernel<P, kProb>), dim3((unsigned)ids), dim3(P::kThreads), 0, s, a);
 }
@@ -597,17 +597,17 @@ void launch_cfg(LossArgs& a, hipStream_t s) {
 template <bool kBF16, bool kProb>
 void launch_typed(const ProductPlan& p, LossArgs& a, hipStream_t s) {
     if (p.sub == 4) {
-        if (p.mr == 1) launch_cfg<kBF16, 1, 2, 4, kProb>(a, s);
-        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 4, kProb>(a, s);
-        else launch_cfg<kBF16, 4, 2, 4, kProb>(a, s);
+        if (p.mr == 1) launch_cfg<kBF16, 1, 4, kProb>(a, s);
+        else if (p.mr == 2) launch_cfg<kBF16, 2, 4, kProb>(a, s);
+        else launch_cfg<kBF16, 4, 4, kProb>(a, s);
     } else if (p.sub == 2) {
-        if (p.mr == 1) launch_cfg<kBF16, 1, 2, 2, kProb>(a, s);
-        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 2, kProb>(a, s);
-        else launch_cfg<kBF16, 4, 2, 2, kProb>(a, s);
-    } else if (p.mr == 1) launch_cfg<kBF16, 1, 2, 1, kProb>(a, s);
-    else if (p.mr == 2) launch_cfg<kBF16, 2, 2, 1, kProb>(a, s);
-    else if (p.mr == 4) launch_cfg<kBF16, 4, 2, 1, kProb>(a, s);
-    else launch_cfg<kBF16, 8, 2, 1, kProb>(a, s);
+        if (p.mr == 1) launch_cfg<kBF16, 1, 2, kProb>(a, s);
+        else if (p.mr == 2) launch_cfg<kBF16, 2, 2, kProb>(a, s);
+        else launch_cfg<kBF16, 4, 2, kProb>(a, s);
+    } else if (p.mr == 1) launch_cfg<kBF16, 1, 1, kProb>(a, s);
+    else if (p.mr == 2) launch_cfg<kBF16, 2, 1, kProb>(a, s);
+    else if (p.mr == 4) launch_cfg<kBF16, 4, 1, kProb>(a, s);
+    else launch_cfg<kBF16, 8, 1, kProb>(a, s);
 }
 
 void launch_any(const ProductPlan& p, LossArgs& a, bool bf16, bool prob, hipStream_t s) {
@@ -622,21 +622,19 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Where one pass over `M` rows keeps its pieces, in bytes from the workspace's start
 struct LossLayout {
-    ProductPlan stats, prob;
+    ProductPlan stats, prob;   // stats: without a gradient, and fp16's
     GradPlan grad;
     int64_t piece, pieces;
     bool small;              // up to 16 rows without a gradient: one kernel before the rows'
     size_t hot, partials, part, zsel, ids, weight, ent, coef, gain, rest, ref, live, factor, before, q, gpart, end;
 };
 
-int64_t tile_columns(const ProductPlan& p) { return 128 * p.cbw; }
-
 LossLayout loss_layout(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bool bf16, bool distill, bool grad) {
     LossLayout l{};
     l.small = !distill && !grad && small_product(M, K);
-    if (!l.small) l.stats = plan_product(M, K, V, G, false);
+    if (!l.small && !(grad && bf16)) l.stats = plan_product(M, K, V, G, false);
     size_t partial = l.stats.partial_bytes;
-    int64_t tiles = l.small ? small_workgroups(padded_cols(V) / kColsPerBlock) : l.stats.tiles_n;
+    int64_t tiles = l.small ? small_workgroups(padded_cols(V) / kColsPerBlock) : l.stats.tiles_n;       // bf16's: below
     if (grad) {
         // pieces of the vocabulary: P of a piece takes at most 256 MiB (it then stays in
         // the last-level cache between the two products)
@@ -829,7 +827,7 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
             g.hot = hot;
             g.factor = floats(l.factor);
             g.before = floats(l.before);
-            g.factor_columns = (int)tile_columns(p);
+            g.factor_columns = kProductColumns;
             err = launch_grad(l.grad, g, stream);
             if (err != hipSuccess) return err;
         }

@@ -283,10 +283,9 @@ struct TileProduct {
 #pragma unroll
             for (int j = 0; j < CBW; ++j) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-        // Block t on operands `cur`; block t + 1 is decoded into `nxt` behind its MFMAs, and
-        // each fragment is scaled behind those of the next. Stages t and t + 1 are in LDS,
-        // t + 2 is on its way.
-        auto block = [&](int t, Operands& cur, Operands& nxt) {
+        // Tiles of one fragment. Block t on operands `cur`; block t + 1 is decoded into `nxt`
+        // behind its MFMAs. Stages t and t + 1 are in LDS, t + 2 is on its way.
+        [[maybe_unused]] auto block = [&](int t, Operands& cur, Operands& nxt) {
             arrive(t);
             if (t + kStages - 1 < nkb) issue(t + kStages - 1);
             if constexpr (kBF16) {
@@ -294,7 +293,7 @@ struct TileProduct {
             }
             const Stage& st = sh.ring[t % kStages];
             const Stage& sn = sh.ring[(t + 1) % kStages];
-            uint4 q[CBW], f[4], fn[4];
+            uint4 q[CBW], f[4];
             uint32_t md[CBW][kSub];
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = st.x[c * 16 + ((4 * i + h) ^ c)];
@@ -302,65 +301,40 @@ struct TileProduct {
             for (int j = 0; j < CBW; ++j) q[j] = sn.w[(w * CBW + j) * 64 + lane];
             scales(nxt, t + 1, md);
             if constexpr (kBF16) {
-                // X of fragment w % MR (four lanes write the same value)
-                const int rx = w % MR;
+                // X (every lane and wave of a row writes the same value)
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
                     float X = 0.f;
 #pragma unroll
                     for (int i = 0; i < 4 / kSub; ++i) {
-                        const uint4 v = st.x[(16 * rx + c) * 16 + ((4 * (u * (4 / kSub) + i) + h) ^ c)];
+                        const uint4 v = f[u * (4 / kSub) + i];
                         X = product_dot2<true>(v.x, 0x3F803F80u, X);
                         X = product_dot2<true>(v.y, 0x3F803F80u, X);
                         X = product_dot2<true>(v.z, 0x3F803F80u, X);
                         X = product_dot2<true>(v.w, 0x3F803F80u, X);
                     }
-                    X = quarter_sum(X);
-                    sh.xsum[(t >> 2) & 1][(t & 3) * kSub + u][16 * rx + c] = X;
+                    sh.xsum[(t >> 2) & 1][(t & 3) * kSub + u][c] = quarter_sum(X);
                 }
             }
-            f32x4 T[2][CBW][kSub];
-            constexpr int kWords = (4 * CBW + MR - 1) / MR;              // decoded behind a fragment
+            f32x4 T[CBW][kSub];
 #pragma unroll
-            for (int r = 0; r < MR; ++r) {
-                if (r + 1 < MR) {
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) fn[i] = st.x[(16 * (r + 1) + c) * 16 + ((4 * i + h) ^ c)];
+                for (int j = 0; j < CBW; ++j) {
+                    const int u = i * kSub / 4;
+                    const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
+                    T[j][u] = mfma16x16x32<kBF16>(cur.b[j][i], f[i], i % (4 / kSub) == 0 ? zero : T[j][u]);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < CBW; ++j)
 #pragma unroll
-                    for (int j = 0; j < CBW; ++j) {
-                        const int u = i * kSub / 4;
-                        const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
-                        T[r & 1][j][u] = mfma16x16x32<kBF16>(cur.b[j][i], f[i], i % (4 / kSub) == 0 ? zero : T[r & 1][j][u]);
-                    }
-                if (r > 0) {
-#pragma unroll
-                    for (int j = 0; j < CBW; ++j)
-#pragma unroll
-                        for (int u = 0; u < kSub; ++u)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[r - 1][j][e] = fmaf(cur.s[j][u][e], T[(r - 1) & 1][j][u][e], acc[r - 1][j][e]);
-                }
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) {
-                    const int wd = r * kWords + k;
-                    if (wd < 4 * CBW) decode(nxt, wd / 4, wd % 4, word(q[wd / 4], wd % 4), md);
-                }
-                if (r + 1 < MR) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = fn[i];
-                }
-            }
+                for (int i = 0; i < 4; ++i) decode(nxt, j, i, word(q[j], i), md);
 #pragma unroll
             for (int j = 0; j < CBW; ++j)
 #pragma unroll
                 for (int u = 0; u < kSub; ++u)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[MR - 1][j][e] = fmaf(cur.s[j][u][e], T[(MR - 1) & 1][j][u][e], acc[MR - 1][j][e]);
+                    for (int e = 0; e < 4; ++e) acc[0][j][e] = fmaf(cur.s[j][u][e], T[j][u][e], acc[0][j][e]);
             // keep the decoding and the sums in this block: they would be moved down to
             // their next use, behind the barrier and away from the MFMAs that hide them
 #pragma unroll
@@ -368,8 +342,7 @@ struct TileProduct {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     asm volatile("" : "+v"(nxt.b[j][i].x), "+v"(nxt.b[j][i].y), "+v"(nxt.b[j][i].z), "+v"(nxt.b[j][i].w));
-#pragma unroll
-                for (int r = 0; r < MR; ++r) asm volatile("" : "+v"(acc[r][j]));
+                asm volatile("" : "+v"(acc[0][j]));
             }
         };
 
