@@ -328,8 +328,11 @@ __global__ __launch_bounds__(256) void targets_kernel(const TargetArgs a) {
             if (sp[j] > 0.f) en += sp[j] * logf(sp[j]);
         }
         for (int s = 32; s > 0; s >>= 1) en += __shfl_xor(en, s);
-        if (lane == 0) a.ent[m] = en;
-        if (lane == 0 && a.hot) a.live[m] = sum != 0.f;
+        if (lane == 0) {
+            a.ent[m] = en;
+            if (a.hot) a.live[m] = sum != 0.f;
+            if (T == 1 && sp[0] == 0.f) sid[0] = -1;         // an only target that weighs nothing is none
+        }
     }
     __syncthreads();
     for (int j = tid; j < T; j += 256) {
@@ -341,7 +344,6 @@ __global__ __launch_bounds__(256) void targets_kernel(const TargetArgs a) {
             if (i < j) first = false;
             p += sp[i];
         }
-        if (T == 1 && p == 0.f) first = false;       // (an only target that weighs nothing is none)
         first_id[j] = first ? id : -1;
         a.out_ids[(size_t)m * T + j] = first ? id : -1;
         a.weight[(size_t)m * T + j] = first ? p : 0.f;
@@ -412,18 +414,19 @@ struct RowArgs {
     float* gain;             // [M] the factor of P W^T in dx
     const float* ref;        // [M] P's reference (bf16) ...
     float* next_ref;         // ... or that of the P to come (fp16)
-    int only;                // the sums leave out a row's only target
-    float* rest;             // [M] then: q_t - 1
+    float* rest;             // [M] q_t - 1 (kOnly)
 };
+// kOnly: one target a row, which the sums leave out
+template <bool kOnly>
 __global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
     __shared__ float2 sv[16][17];
     const int i = (int)threadIdx.x & 15, g = (int)threadIdx.x >> 4;
     const int m = (int)blockIdx.x * 16 + i;
     const int M = a.M;
     const int mc = m < M ? m : M - 1;
-    bool live = false;
-    float z = 0.f;
-    if (a.only && g == 0) {
+    [[maybe_unused]] bool live = false;
+    [[maybe_unused]] float z = 0.f;
+    if constexpr (kOnly) {
         const int id = a.ids[mc];
         live = id >= 0 && id < a.N;
         if (live) z = a.zsel[mc];
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const RowArgs a) {
     v = sv[0][i];
     for (int k = 1; k < 16; ++k) v = join(v, sv[k][i]);
     float lse = v.x + logf(v.y);
-    if (a.only) {
+    if constexpr (kOnly) {
         if (g != 0 || m >= M) return;
         const float others = lse;                // log of the sum without the target
         float loss = 0.f;
@@ -770,7 +773,6 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
         rows.ent = t.ent;
         rows.zsel = t.zsel;
         rows.tau = q.tau;
-        rows.only = only;
         rows.dloss = q.dloss ? q.dloss + r0 : nullptr;
         rows.loss = q.loss + r0;
         rows.lse = q.lse + r0;
@@ -781,7 +783,11 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
             rows.ref = ref;
             if (!q.bf16) rows.next_ref = ref;
         }
-        const dim3 rows_grid((unsigned)((M + 15) / 16));
+        auto join_rows = [&]() {
+            const dim3 grid((unsigned)((M + 15) / 16));
+            if (only) hipLaunchKernelGGL((rows_kernel<true>), grid, dim3(256), 0, stream, rows);
+            else hipLaunchKernelGGL((rows_kernel<false>), grid, dim3(256), 0, stream, rows);
+        };
         if (sums_first) {
             a.part = part;
             if (l.small) {
@@ -792,7 +798,7 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
                 product(l.stats, 0, q.V, false);
                 rows.tiles = l.stats.tiles_n;
             }
-            hipLaunchKernelGGL(rows_kernel, rows_grid, dim3(256), 0, stream, rows);
+            join_rows();
         }
         hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
@@ -833,7 +839,7 @@ hipError_t launch_loss(const LossCall& q, hipStream_t stream) {
         }
         if (!sums_first) {
             rows.tiles = tiles;
-            hipLaunchKernelGGL(rows_kernel, rows_grid, dim3(256), 0, stream, rows);
+            join_rows();
         }
         FinishArgs f{};
         f.part = floats(l.gpart);
