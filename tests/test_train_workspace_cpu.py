@@ -44,6 +44,7 @@ def mod(monkeypatch):
     monkeypatch.setattr(m, "_raw_stream", lambda stream, device: STREAM)
     monkeypatch.setattr(m, "_capture_of", lambda raw: m._lib.capture, raising=False)
     monkeypatch.setattr(m, "_captured", {}, raising=False)
+    monkeypatch.setattr(m, "_recorded", {}, raising=False)
     monkeypatch.setattr(m, "_workspaces", {(None, STREAM): torch.zeros(4096, dtype=torch.uint8)})
     m._need.cache_clear()
 
@@ -132,3 +133,32 @@ def test_a_capture_has_its_own_workspace(mod):
     op()
     assert mod._captured[(None, STREAM)][1] is not kept
     assert bool((mod._captured[(None, STREAM)][1][:512] == 0).all())
+
+
+@pytest.mark.parametrize("i", [5, 6, 7])
+def test_captured_products_share_a_workspace_that_is_never_replaced(mod, i):
+    lib, op = mod._lib, calls(mod)[i]
+    lib.capture = 1                              # without a warm-up: the capture's own
+    op()
+    assert lib.calls[-1][1] == mod._captured[(None, STREAM)][1].data_ptr()
+    lib.capture = None
+    op()
+    eager = lib.calls[-1][1]
+    lib.capture = 2
+    op()
+    shared = lib.calls[-1][1]
+    kept = mod._recorded[None][0]
+    assert shared == kept.data_ptr() != eager and kept.numel() >= 4096 and int(kept.count_nonzero()) == 0
+    calls(mod)[3]()                              # the other entries' calls have their own
+    assert lib.calls[-1][1] not in (shared, eager)
+    lib.capture = None                           # a larger need brings another; the first stays
+    lib.need = 16384
+    op()
+    lib.capture = 3
+    op()
+    assert lib.calls[-1][1:3] == (mod._recorded[None][1].data_ptr(), 16384)
+    assert mod._recorded[None][0] is kept
+    lib.need = 4096
+    lib.capture = None
+    op()
+    assert len(mod._recorded[None]) == 2

@@ -14,7 +14,8 @@ Functions keep the C names:
   w4a16_parse_packed_header(header) -> (K, N, group_size, dtype, packed_bytes)
   w4a16_gemm(x, packed, N, group_size, bias=None, y=None, workspace=None, stream=None) -> y
       (workspace=None: a zero-filled workspace per device and stream is allocated on demand;
-      in a captured graph, one in the graph's own memory)
+      captured calls share one of the device, if a call that needs as much was made before,
+      so graphs of them that run at the same time need workspaces of their own)
   w4a16_gemm_ex(..., path="auto"|"gemv"|"mfma", gemv_max_m=-1)            -> y
   w4a16_gemm_noalloc(x, packed, N, group_size, bias=None, y=None, stream=None) -> y
       (no workspace: the library's per-GPU scratch array; nothing is allocated when y is given)
@@ -29,7 +30,8 @@ functions as differentiable torch operations: the `autograd` module):
   w4a16_cross_entropy(x, labels, packed, V, group_size, dloss, grad) -> (loss, lse[, dx])
   w4a16_distill(x, top_ids, top_logits, packed, V, group_size, temperature, dloss, grad)
       -> (loss, lse[, dx])
-  (each takes its outputs, workspace and stream as keywords, like w4a16_gemm)
+  (each takes its outputs, workspace and stream as keywords, like w4a16_gemm; captured
+  without a workspace, they take one in the graph's own memory)
 
 Load-path helpers built on those calls (host-side data movement only):
   repack_from_host(qweight, qzeros, scales, group_size, fmt, chunk_columns, device)
@@ -396,6 +398,7 @@ def _default_workspace(device, nbytes, stream=None):
 
 _locks = {}
 _captured = {}           # (device, stream) -> (its last capture, that capture's workspace)
+_recorded = {}           # device -> cleared workspaces for captured products, the largest last; none is ever freed
 CLEARED_BYTES = 512      # what has to be zero before a workspace's first use
 
 
@@ -408,11 +411,15 @@ def _capture_of(raw):
     return number.value if code == 0 and status.value == 1 else None
 
 
-def _workspace_of_capture(key, capture, nbytes, device, stream):
+def _workspace_of_capture(key, capture, nbytes, device, stream, product):
     """A workspace for the calls that one capture records on one stream, in the graph's own
     memory and cleared by the graph, so that a replay neither meets a buffer that an eager
     call has replaced nor depends on one that another graph has cleared. Eager calls never
-    see it."""
+    see it. Products take the one that their eager calls before the capture have left for
+    all graphs of the device, already clear (a fill in the graph costs 2 us a replay);
+    graphs that share it must not run at the same time."""
+    if product and _recorded.get(key[0]) and _recorded[key[0]][-1].numel() >= nbytes:
+        return _recorded[key[0]][-1]
     last = _captured.get(key)
     if last is None or last[0] != capture or last[1].numel() < nbytes:
         with torch.cuda.stream(stream):
@@ -429,13 +436,14 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
-def _launch(name, args, workspace, need, device, stream, more=()):
+def _launch(name, args, workspace, need, device, stream, more=(), product=False):
     """The library's `name`(*args, workspace, its bytes, stream, *more), checked. Without a
     workspace, a call that needs one takes the (device, stream)'s own, which serves one
     call at a time: most entry points are several launches that meet in it, so the lock is
     held until a call's last launch is queued, and the launches of another thread's call on
     that stream stay behind them. (ctypes lets other threads run during the call.) Under a
-    capture it is the capture's own."""
+    capture it is another (_workspace_of_capture). product: w4a16_gemm's and w4a8_gemm's
+    entry points, one launch each."""
     fn = getattr(_load(), name)
     raw = _raw_stream(stream, device)
     if workspace is None and need > 0:
@@ -444,11 +452,16 @@ def _launch(name, args, workspace, need, device, stream, more=()):
         with lock:
             capture = _capture_of(raw)
             if capture is not None:
-                ws = _workspace_of_capture(key, capture, need, device, stream)
+                ws = _workspace_of_capture(key, capture, need, device, stream, product)
             else:
                 ws = _workspaces.get(key)
                 if ws is None or ws.numel() < need:
                     ws = _default_workspace(device, need, stream)
+                if product:
+                    kept = _recorded.setdefault(device.index, [])
+                    if not kept or kept[-1].numel() < need:
+                        with torch.cuda.stream(stream):
+                            kept.append(torch.zeros(need, dtype=torch.uint8, device=device))
             code = fn(*args, ws.data_ptr(), ws.nbytes, raw, *more)
     elif workspace is None:
         code = fn(*args, None, 0, raw, *more)
@@ -477,7 +490,7 @@ def _gemm_args(x, packed, N, group_size, bias, y, workspace):
 def w4a16_gemm(x, packed, N, group_size=128, bias=None, y=None, workspace=None, stream=None):
     """x [M, K] (fp16/bf16) times the packed weight (+ bias) -> y [M, N] of x's dtype."""
     args, need, y = _gemm_args(x, packed, N, group_size, bias, y, workspace)
-    _launch("w4a16_gemm", args, workspace, need, x.device, stream)
+    _launch("w4a16_gemm", args, workspace, need, x.device, stream, product=True)
     return y
 
 
@@ -487,7 +500,7 @@ def w4a16_gemm_ex(x, packed, N, group_size=128, bias=None, y=None, workspace=Non
     if path not in PATHS:
         raise W4A16Error(9, f"path {path!r}")
     args, need, y = _gemm_args(x, packed, N, group_size, bias, y, workspace)
-    _launch("w4a16_gemm_ex", args, workspace, need, x.device, stream, (PATHS[path], gemv_max_m))
+    _launch("w4a16_gemm_ex", args, workspace, need, x.device, stream, (PATHS[path], gemv_max_m), product=True)
     return y
 
 
@@ -579,7 +592,7 @@ def w4a8_gemm(act, packed, M, K, N, group_size=128, dtype=torch.bfloat16, bias=N
         raise ValueError("bias must be a contiguous [N] tensor of `dtype`")
     args = (_ptr(act), act.numel() * act.element_size(), _ptr(packed), packed.numel() * packed.element_size(),
             _dtype_code(dtype), _ptr(y), M, K, N, group_size, _ptr(bias))
-    _launch("w4a8_gemm", args, workspace, need, act.device, stream)
+    _launch("w4a8_gemm", args, workspace, need, act.device, stream, product=True)
     return y
 
 
