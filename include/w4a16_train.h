@@ -54,7 +54,12 @@ typedef enum {
  * w4a16_gated_grad is its backward to x: it forms both projections again from x and
  * returns dx = dg Wg^T + du Wu^T, dg = dh u a'(g), du = dh a(g). dg and du are rounded once
  * to fp16 at a power of two of their row's largest value, and so are the weights at one of
- * the largest scale. dh [M, F]. 8192 rows at a time. */
+ * the largest scale (a scale less than 2^-21 of it loses bits, one below 2^-31 is taken as
+ * 0). With fp16 tensors what dg's and du's rounding leaves is kept in a second fp16 value
+ * where the product's tiles have up to 128 rows, in practice up to several hundred rows: the
+ * error against exact arithmetic, in the norm, is 2.9e-4 there and 3.5e-4 above (2.1e-4: the
+ * result's own rounding; bf16: 1.7e-3, all of it the result's). dh [M, F]. 8192 rows at a
+ * time. */
 size_t w4a16_gated_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t group_size, int grad);
 w4a16_status w4a16_gated(const void* x, const void* packed, size_t packed_bytes, w4a16_dtype dtype, void* h, int64_t M,
                          int64_t K, int64_t F, int64_t group_size, w4a16_act act, void* workspace,

@@ -12,10 +12,11 @@
 // W^T follows, which brings a row's tiles to one scale (gemm_grad.hip): rounded to bf16 they
 // would be off by as much as the result's own rounding, and fp32 took 8 F bytes a row.
 //
-// Measured: 512 rows x 2048 x 13312 37 us (757 TFLOP/s; 208 tiles, one round), 4096 rows 247
-// us (903); the backward of 4096 rows 523 us (855 over both products). Bound by the matrix
-// cores and the vector instructions between their MFMAs; a tile's start and end, which no
-// other workgroup of its compute unit covers, take a tenth.
+// Measured: 512 rows x 2048 x 13312 37 us (757 TFLOP/s; 208 tiles, one round), 4096 rows 242
+// us (923); the backward of 4096 rows 557 us (802 over both products; 525 where every call
+// has the same inputs), fp16 503. Bound as tile_product.h has it: matrix cores 0.35 busy,
+// vector units 0.39 with other work; a tile's start and end, which no other workgroup of its
+// compute unit covers, take a tenth.
 #include "device_common.h"
 #include "gate.h"
 #include "launch.h"

@@ -21,8 +21,10 @@
 // is split over workgroups into fp32 partial tiles, added in split order by a second
 // kernel (the result does not depend on the order of arrival).
 //
-// Measured with every compute unit busy (4096 x 8192 -> 4096, bf16): 264 us, 1041 TFLOP/s;
-// bound by LDS (writes and reads of a stage take as long as its MFMAs) and the decoding.
+// Measured with every compute unit busy (4096 x 8192 -> 4096, bf16): 257 us, 1070 TFLOP/s;
+// bound by LDS and the decoding: the matrix cores are busy 0.43 of the time, LDS about 0.5 (a
+// third of it bank conflicts), and the two vector instructions an MFMA run beside it in only
+// 0.02: a stage is decoded, written and read in bursts.
 // 4096 x 2048 -> 6656 has 416 tiles for 256 compute units: 144 us, the second round 0.6 full.
 // Few rows are bound by the partial tiles' traffic and the latency of a few stages.
 #include "device_common.h"

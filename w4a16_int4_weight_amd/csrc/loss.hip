@@ -16,7 +16,7 @@
 // fp32's range. A row that goes higher in some tile takes that tile's maximum as the tile's
 // reference, and the product with W^T brings the row's tiles to a common one ("hot": rare,
 // right for any logits, off the usual path: 4096 x 2048 x 131072 takes 5790 us instead of
-// 4700). A row without a target, whose reference is column 0's logit and may lie anywhere,
+// 4700 on one set of inputs). A row without a target, whose reference is column 0's logit and may lie anywhere,
 // takes references of its own for its log-sum but makes nothing hot: its gradient is zero.
 // fp16 has not that range: there the statistics come first, in a product of their own, and
 // P = 2^15 q is formed with r = lse - 15 log 2, in fp16 (the target term of a loss in fp16
@@ -30,8 +30,8 @@
 //
 // Roundings: P once and W once, to the operand type; dx once. Measured on 4096 x 2048 x
 // 131072 with its gradient: 9490 us with the tile formed twice and the scheduling left to
-// the compiler, 4700 us so (two products of 2.2 TFLOP, 930 and 980 TFLOP/s); bound by the
-// matrix cores and the vector instructions between their MFMAs.
+// the compiler, 4900 us so (4730 where every call has the same inputs; two products of 2.2
+// TFLOP, about 900 TFLOP/s each); bound as tile_product.h and gemm_grad.hip have it.
 #include "device_common.h"
 #include "launch.h"
 #include "tile_product.h"

@@ -15,9 +15,11 @@
 // of what the difference loses; here the shifts hide behind the loads). X comes from the
 // same MFMAs against ones, once for all units. fp16 takes q - z exactly in 16 bits.
 //
-// Measured: 2048 x 13312, one row or 16, 7 us a call (10 us with 16-row tiles and K split over
-// workgroups); 2048 x 131072, one row, 31 us, 4.6 TB/s (36 us). With 512 workgroups instead
-// of 256: 9.0 and 38.7 us a call.
+// Measured: 2048 x 13312, one row or 16, 7.4 us a call, the kernel 6.3 (10 us with 16-row tiles
+// and K split over workgroups); 2048 x 131072, one row, 35 us, 4.1 TB/s (the matrix-vector
+// kernel of the product reads the same codes in 22 us: here a barrier a batch keeps the waves
+// together, and the vector units decode half the time). With 512 workgroups instead of 256:
+// 9.0 and 38.7 us a call.
 #include "device_common.h"
 #include "gate.h"
 #include "launch.h"

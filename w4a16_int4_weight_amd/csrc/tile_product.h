@@ -18,11 +18,15 @@
 // XOR-swizzled by row) and the waves' packed codes, filled by direct global -> LDS
 // copies; a wave decodes its codes of the block into registers once and runs through
 // its MR row fragments with them, so each weight is decoded once per 16 MR rows.
-// What bounds it at 128 rows: the issue of vector instructions between the MFMAs (about 3
-// each) and the registers that let them be placed there. Measured on 4096 x 2048 x 131072
-// with the loss's epilogue: 3530 us with the decoding and scaling left to the compiler's
-// order, 2420 us in the order below and with the zero points on the matrix cores (bf16,
-// 908 TFLOP/s; fp16, whose codes lose their zero point in 16 bits, 2230 us).
+// What bounds it at 128 rows, by counters (4096 x 2048 x 32768 with the loss's epilogue): the
+// matrix cores are busy 0.37 of the time, the vector units with other work (4 instructions
+// an MFMA, epilogue included) 0.39, both at once 0.14, so that for the rest, 0.38, a SIMD
+// issues neither: its two waves wait for each other at the barrier of a row block or for a
+// tile's start and end. Groups of 32: 11 instructions an MFMA, matrix cores 0.11.
+// Measured on 4096 x 2048 x 131072 with the loss's epilogue: 3530 us with the decoding and
+// scaling left to the compiler's order, 2410 us in the order below and with the zero points
+// on the matrix cores (bf16, 912 TFLOP/s; fp16, whose codes lose their zero point in 16 bits,
+// 2230 us).
 // X is summed by wave r for fragment r, passed on through LDS and taken off every fourth
 // row block. The MFMA takes the weights as its first operand, so a lane holds four adjacent
 // columns of one row.
