@@ -33,6 +33,12 @@ functions as differentiable torch operations: the `autograd` module):
   (each takes its outputs, workspace and stream as keywords, like w4a16_gemm; captured
   without a workspace, they take one in the graph's own memory)
 
+Decoding with mixtures of int4 experts, and drawing tokens (include/w4a16_serve.h):
+  w4a16_route(x, router, top_k, bias, score, normalize, scale) -> (ids, weights) [M, T]
+  w4a16_moe(x, ids, weights, gate_up, down, F, group_size, act, residual) -> y [M, K]
+  w4a16_moe_layer(x, router, gate_up, down, F, top_k, ...)     -> (y, ids, weights)
+  w4a16_sample(logits, u, temperature, top_k, top_p, min_p)    -> (ids, logprob) [M]
+
 Load-path helpers built on those calls (host-side data movement only):
   repack_from_host(qweight, qzeros, scales, group_size, fmt, chunk_columns, device)
       checkpoint tensors in host memory -> packed device buffer, one column chunk of
@@ -64,6 +70,8 @@ __all__ = [
     "ACTS", "w4a16_gemm_grad", "w4a16_gemm_grad_workspace_bytes", "w4a16_gated", "w4a16_gated_grad",
     "w4a16_gated_workspace_bytes", "w4a16_cross_entropy", "w4a16_cross_entropy_workspace_bytes", "w4a16_distill",
     "w4a16_distill_workspace_bytes",
+    "SCORES", "w4a16_route", "w4a16_route_workspace_bytes", "w4a16_moe", "w4a16_moe_workspace_bytes", "w4a16_moe_layer",
+    "w4a16_moe_layer_workspace_bytes", "w4a16_sample", "w4a16_sample_workspace_bytes",
 ]
 
 STATUS = {
@@ -76,6 +84,8 @@ PAYLOAD_OFFSET = 1 << 16       # packed bytes start 64 KiB into a saved file (pa
 DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 PATHS = {"auto": 0, "gemv": 1, "mfma": 2}
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
 class W4A16Error(RuntimeError):
@@ -83,6 +93,13 @@ class W4A16Error(RuntimeError):
         self.code = code
         self.status = STATUS.get(code, str(code))
         super().__init__(f"{what}: {self.status} ({w4a16_status_str(code)})")
+
+
+class _Sampling(ctypes.Structure):
+    """w4a16_sampling of include/w4a16_serve.h"""
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
 
 
 _lib = None
@@ -169,6 +186,24 @@ def _load():
     h.w4a16_distill.argtypes = [_vp, _vp, _vp, _vp, _sz, _int, _i64, _i64, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp,
                                 _vp, _sz, _vp]
     h.w4a16_distill.restype = _int
+    h.w4a16_route_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+    h.w4a16_route_workspace_bytes.restype = _sz
+    h.w4a16_route.argtypes = [_vp, _vp, _vp, _int, _i64, _i64, _i64, _i64, _int, _int, _f32, _vp, _vp, _vp, _sz, _vp]
+    h.w4a16_route.restype = _int
+    h.w4a16_moe_workspace_bytes.argtypes = [_i64] * 6
+    h.w4a16_moe_workspace_bytes.restype = _sz
+    h.w4a16_moe.argtypes = [_vp, _vp, _vp, _vp, _sz, _sz, _vp, _sz, _sz, _int, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64,
+                            _int, _vp, _sz, _vp]
+    h.w4a16_moe.restype = _int
+    h.w4a16_moe_layer_workspace_bytes.argtypes = [_i64] * 6
+    h.w4a16_moe_layer_workspace_bytes.restype = _sz
+    h.w4a16_moe_layer.argtypes = [_vp, _vp, _vp, _int, _int, _f32, _vp, _sz, _sz, _vp, _sz, _sz, _int, _vp, _vp, _vp, _vp,
+                                  _i64, _i64, _i64, _i64, _i64, _i64, _int, _vp, _sz, _vp]
+    h.w4a16_moe_layer.restype = _int
+    h.w4a16_sample_workspace_bytes.argtypes = [_i64, _i64]
+    h.w4a16_sample_workspace_bytes.restype = _sz
+    h.w4a16_sample.argtypes = [_vp, _int, _i64, _vp, _i64, _i64, ctypes.POINTER(_Sampling), _vp, _vp, _vp, _sz, _vp]
+    h.w4a16_sample.restype = _int
     # the HIP runtime that the library is linked to
     h.hipStreamGetCaptureInfo.argtypes = [_vp, ctypes.POINTER(_int), ctypes.POINTER(ctypes.c_ulonglong)]
     h.hipStreamGetCaptureInfo.restype = _int
@@ -746,6 +781,148 @@ def w4a16_distill(x, top_ids, top_logits, packed, V, group_size=128, temperature
              dx.data_ptr() if grad else None),
             workspace, _need("w4a16_distill_workspace_bytes", M, K, V, group_size, T, 1 if grad else 0), x.device, stream)
     return (loss, lse, dx) if grad else (loss, lse)
+
+
+# ---------------------------------------------------------------- mixtures of experts, drawing tokens
+# (include/w4a16_serve.h)
+
+def w4a16_route_workspace_bytes(M, K, E, T):
+    return _load().w4a16_route_workspace_bytes(M, K, E, T)
+
+
+def w4a16_moe_workspace_bytes(M, K, F, E, T, group_size):
+    return _load().w4a16_moe_workspace_bytes(M, K, F, E, T, group_size)
+
+
+def w4a16_moe_layer_workspace_bytes(M, K, F, E, T, group_size):
+    return _load().w4a16_moe_layer_workspace_bytes(M, K, F, E, T, group_size)
+
+
+def w4a16_sample_workspace_bytes(M, V):
+    return _load().w4a16_sample_workspace_bytes(M, V)
+
+
+def _router_args(x, router, top_k, bias, score, ids, weights):
+    """-> (M, K, E, the score's code, ids, weights)"""
+    M, K = _rows(x, "x")
+    E, Kr = _rows(router, "router")
+    if Kr != K or router.dtype != x.dtype:
+        raise ValueError("router must be a contiguous [E, K] tensor of x's dtype")
+    if bias is not None and (tuple(bias.shape) != (E,) or bias.dtype != torch.float32 or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous float32 [E] tensor")
+    if score not in SCORES:
+        raise W4A16Error(9, f"score {score!r}")
+    if top_k < 1:
+        raise W4A16Error(2, f"top_k {top_k}")
+    ids = _result(ids, "ids", (M, top_k), torch.int32, x.device)
+    weights = _result(weights, "weights", (M, top_k), torch.float32, x.device)
+    return M, K, E, SCORES[score], ids, weights
+
+
+def w4a16_route(x, router, top_k, bias=None, score="softmax", normalize=True, scale=1.0, ids=None, weights=None,
+                workspace=None, stream=None):
+    """Router of a mixture of experts. x [M, K], router [E, K] (fp16/bf16) -> (ids int32,
+    weights float32) [M, top_k]: the experts of the largest x . router^T, ties to the lowest,
+    and their scores ("softmax" over the experts, or each expert's "sigmoid"), with `normalize`
+    over their sum, times `scale`. bias float32 [E] enters the choice alone."""
+    M, K, E, code, ids, weights = _router_args(x, router, top_k, bias, score, ids, weights)
+    _beside(x, router=router, bias=bias, ids=ids, weights=weights, workspace=workspace)
+    _launch("w4a16_route",
+            (x.data_ptr(), router.data_ptr(), None if bias is None else bias.data_ptr(), _dtype_code(x.dtype), M, K, E, top_k,
+             code, 1 if normalize else 0, scale, ids.data_ptr(), weights.data_ptr()),
+            workspace, _need("w4a16_route_workspace_bytes", M, K, E, top_k), x.device, stream)
+    return ids, weights
+
+
+def _experts_args(x, gate_up, down, F, group_size, residual, y):
+    """-> (E, (gate_up's and down's addresses, bytes and strides), y)"""
+    M, K = _rows(x, "x")
+    for t, name, rows, cols in ((gate_up, "gate_up", K, 2 * F), (down, "down", F, K)):
+        if t.dim() != 2 or t.dtype != torch.uint8 or t.stride(1) != 1 or t.shape[0] != gate_up.shape[0]:
+            raise ValueError(f"{name} must be a uint8 [E, bytes] tensor, each row one expert's packed [{rows}, {cols}] weight")
+    if residual is not None and (tuple(residual.shape) != (M, K) or residual.dtype != x.dtype or not residual.is_contiguous()):
+        raise ValueError("residual must be a contiguous [M, K] tensor of x's dtype")
+    y = _result(y, "y", (M, K), x.dtype, x.device)
+    E = gate_up.shape[0]
+    args = ()
+    for t in (gate_up, down):
+        stride = t.stride(0) if E > 1 else t.shape[1] // 16 * 16       # (a lone row's stride says nothing)
+        args += (t.data_ptr(), (E - 1) * stride + t.shape[1], stride)
+    return E, args, y
+
+
+def w4a16_moe(x, ids, weights, gate_up, down, F, group_size=128, act="silu", residual=None, y=None, workspace=None,
+              stream=None):
+    """Experts' gated feed-forward blocks on packed int4 weights: x [M, K] (fp16/bf16), ids
+    int32 and weights float32 [M, T] (an id outside [0, E): none) -> y [M, K] = residual +
+    sum_j weights[:, j] * (act(x Wg) * (x Wu)) Wd over the experts ids[:, j]. gate_up and down:
+    uint8 [E, bytes], row e expert e's packed [K, 2F] and [F, K] weight."""
+    M, K = _rows(x, "x")
+    E, experts, y = _experts_args(x, gate_up, down, F, group_size, residual, y)
+    Mi, T = _rows(ids, "ids")
+    if Mi != M or ids.dtype != torch.int32:
+        raise ValueError("ids must be an int32 [M, T] tensor")
+    if _rows(weights, "weights") != (M, T) or weights.dtype != torch.float32:
+        raise ValueError("weights must be a float32 [M, T] tensor")
+    _beside(x, ids=ids, weights=weights, gate_up=gate_up, down=down, residual=residual, y=y, workspace=workspace)
+    _launch("w4a16_moe",
+            (x.data_ptr(), ids.data_ptr(), weights.data_ptr(), *experts, _dtype_code(x.dtype),
+             None if residual is None else residual.data_ptr(), y.data_ptr(), M, K, F, E, T, group_size, _act_code(act)),
+            workspace, _need("w4a16_moe_workspace_bytes", M, K, F, E, T, group_size), x.device, stream)
+    return y
+
+
+def w4a16_moe_layer(x, router, gate_up, down, F, top_k, group_size=128, act="silu", bias=None, score="softmax",
+                    normalize=True, scale=1.0, residual=None, ids=None, weights=None, y=None, workspace=None, stream=None):
+    """w4a16_route and w4a16_moe in one call -> (y, ids, weights)."""
+    E, experts, y = _experts_args(x, gate_up, down, F, group_size, residual, y)
+    M, K, Er, code, ids, weights = _router_args(x, router, top_k, bias, score, ids, weights)
+    if Er != E:
+        raise ValueError("router and gate_up must have the same number of experts")
+    _beside(x, router=router, bias=bias, ids=ids, weights=weights, gate_up=gate_up, down=down, residual=residual, y=y,
+            workspace=workspace)
+    _launch("w4a16_moe_layer",
+            (x.data_ptr(), router.data_ptr(), None if bias is None else bias.data_ptr(), code, 1 if normalize else 0, scale,
+             *experts, _dtype_code(x.dtype), None if residual is None else residual.data_ptr(), ids.data_ptr(),
+             weights.data_ptr(), y.data_ptr(), M, K, F, E, top_k, group_size, _act_code(act)),
+            workspace, _need("w4a16_moe_layer_workspace_bytes", M, K, F, E, top_k, group_size), x.device, stream)
+    return y, ids, weights
+
+
+def w4a16_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None, logprob=None, workspace=None,
+                 stream=None):
+    """One token a row from logits [M, V] (fp16, bf16 or float32; rows may have a stride) and
+    uniform numbers u float32 [M] -> (ids int32, logprob float32) [M]: softmax at `temperature`
+    (0: the largest), restricted to the top_k largest (0: all), of these to the shortest run
+    of the likeliest that reaches top_p (1: all), of these to those at least min_p times as
+    likely as the likeliest; the token at u of what is left, in index order, and the logarithm
+    of its probability there. Each setting is a number or one per row ([M], float32; top_k
+    int32)."""
+    if logits.dim() != 2 or logits.dtype not in LOGITS or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a [M, V] tensor of fp16, bf16 or float32 with adjacent columns")
+    M, V = logits.shape
+    ld = logits.stride(0) if M > 1 else V
+    if ld < V:
+        raise ValueError("rows of logits must not overlap")
+    if tuple(u.shape) != (M,) or u.dtype != torch.float32 or not u.is_contiguous():
+        raise ValueError("u must be a contiguous float32 [M] tensor")
+    how, settings = _Sampling(), {}
+    for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                               ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            if tuple(value.shape) != (M,) or value.dtype != dtype or not value.is_contiguous():
+                raise ValueError(f"{name} must be a number or a contiguous [M] tensor of {dtype}")
+            settings[name] = value
+            setattr(how, name + "s", value.data_ptr())
+        else:
+            setattr(how, name, value)
+    ids = _result(ids, "ids", (M,), torch.int32, logits.device)
+    logprob = _result(logprob, "logprob", (M,), torch.float32, logits.device)
+    _beside(logits, u=u, ids=ids, logprob=logprob, workspace=workspace, **settings)
+    _launch("w4a16_sample",
+            (logits.data_ptr(), LOGITS[logits.dtype], ld, u.data_ptr(), M, V, ctypes.byref(how), ids.data_ptr(),
+             logprob.data_ptr()), workspace, _need("w4a16_sample_workspace_bytes", M, V), logits.device, stream)
+    return ids, logprob
 
 
 # ---------------------------------------------------------------- streaming references

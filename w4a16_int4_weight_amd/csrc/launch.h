@@ -221,4 +221,64 @@ int max_loss_targets();
 size_t loss_workspace(int64_t M, int64_t K, int64_t V, int64_t G, int64_t T, bool distill, bool grad);
 hipError_t launch_loss(const LossCall& call, hipStream_t stream);
 
+// Router of a mixture of experts (csrc/route.hip): counters zero, left zero; logits of
+// route_logits_bytes.
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxChosen = 32;         // experts of a row
+struct RouteCall {
+    const uint16_t* x;
+    const uint16_t* router;
+    const float* bias;
+    int64_t M, K, E, T;
+    int sigmoid, normalize;
+    float scale;
+    int32_t* ids;
+    float* weights;
+    bool bf16;
+    uint32_t* counters;
+    void* logits;
+};
+size_t route_logits_bytes(int64_t M, int64_t E);
+hipError_t launch_route(const RouteCall& call, hipStream_t stream);
+
+// Mixture of experts on packed weights. M T pairs are indexed in 32 bits, and h's rows
+// (2 M T F elements) within 4 GiB.
+struct MoeCall {
+    const uint16_t* x;
+    const int32_t* ids;
+    const float* weights;
+    const uint8_t* gate_up;
+    const uint8_t* down;
+    int64_t gate_up_stride, down_stride;
+    const uint16_t* residual;   // or NULL
+    uint16_t* y;
+    int64_t M, K, F, E, T, G;
+    int act;
+    bool bf16;
+};
+// csrc/moe_tile.hip: scratch of layout.end bytes, nothing in it kept between calls
+struct MoeTileLayout {
+    int mr, slots;
+    size_t list, slot, h, out, end;
+};
+MoeTileLayout moe_tile_layout(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T, int64_t G);
+hipError_t launch_moe_tile(const MoeCall& call, uint8_t* scratch, hipStream_t stream);
+
+// Draws a token from each row's logits (csrc/sample.hip). kind: 0 fp16, 1 bf16, 2 fp32.
+struct SampleCall {
+    const void* logits;
+    int kind;
+    int64_t ld, M, V;
+    const float* u;
+    float temperature, top_p, min_p;
+    int32_t top_k;
+    const float* temperatures;
+    const int32_t* top_ks;
+    const float* top_ps;
+    const float* min_ps;
+    int32_t* ids;
+    float* logprob;             // or NULL
+};
+hipError_t launch_sample(const SampleCall& call, hipStream_t stream);
+
 }  // namespace w4a16

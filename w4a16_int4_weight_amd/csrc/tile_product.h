@@ -49,6 +49,17 @@ struct ProductArgs {
     int tiles_m, tiles_n, splits;
     uint32_t* counters;     // K split: tile counters and partial tiles
     float* partials;
+    const int32_t* rows;    // gathered tiles: rows of x (RowsInOrder does not read it)
+    int row_div;
+};
+
+// Which rows of x a tile's rows are: those of [m0, M) in order, the last one repeated. at() is
+// relative to base().
+struct RowsInOrder {
+    static __device__ __forceinline__ const uint16_t* base(const ProductArgs& a, int m0) { return a.x + (size_t)m0 * a.K; }
+    static __device__ __forceinline__ int at(const ProductArgs& a, int m0, int row) {
+        return (m0 + row < a.M ? m0 + row : a.M - 1) - m0;
+    }
 };
 
 constexpr int kProductXcds = 8;
@@ -99,7 +110,8 @@ __device__ __forceinline__ float quarter_max(float v) {
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
-template <bool kBF16_, int MR_, int CBW_, int W_, int kSub_, bool kGated_>
+// kScaleBF16: the type of the weight's scales, where it is not that of x.
+template <bool kBF16_, int MR_, int CBW_, int W_, int kSub_, bool kGated_, class Rows = RowsInOrder, bool kScaleBF16 = kBF16_>
 struct TileProduct {
     static constexpr bool kBF16 = kBF16_, kGated = kGated_;
     static constexpr int MR = MR_, CBW = CBW_, W = W_, kSub = kSub_;
@@ -168,15 +180,14 @@ struct TileProduct {
 
         // copies: wave-uniform bases and per-lane byte offsets. Rows past M read row M - 1
         // and columns past the last read the last: they feed outputs that are not used.
-        const uint8_t* xbase = uniform_ptr(a.x + (size_t)m0 * K);
+        const uint8_t* xbase = uniform_ptr(Rows::base(a, m0));
         uint32_t xoff[kSlabs];
         int xslab[kSlabs];
 #pragma unroll
         for (int t = 0; t < kSlabs; ++t) {
             xslab[t] = (w * kSlabs + t) % kXSlabs;
             const int row = 4 * xslab[t] + (lane >> 4);
-            const int m = m0 + row < a.M ? m0 + row : a.M - 1;
-            xoff[t] = 2u * ((uint32_t)(m - m0) * (uint32_t)K + 8u * (uint32_t)((lane & 15) ^ (row & 15)));
+            xoff[t] = 2u * ((uint32_t)Rows::at(a, m0, row) * (uint32_t)K + 8u * (uint32_t)((lane & 15) ^ (row & 15)));
         }
         const uint8_t* wbase[CBW];
         const uint8_t* mbase[CBW];
@@ -230,7 +241,7 @@ struct TileProduct {
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
                     md[j][u] = sh.meta[(t >> 2) % kMetaSlots][w][(16 * j + c) * kUnits + (t & 3) * kSub + u];
-                    sh.scale[w][u][16 * j + c] = half_bits_to_f32<kBF16>(md[j][u] & 0xFFFFu);
+                    sh.scale[w][u][16 * j + c] = half_bits_to_f32<kScaleBF16>(md[j][u] & 0xFFFFu);
                 }
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -254,7 +265,8 @@ struct TileProduct {
         // Zero points of the group of row blocks 4 g .. 4 g + n - 1, by the matrix cores:
         // acc -= sum over its units of s (128 + z) X. Lane quarter h takes unit 4 v + h of
         // MFMA v. X (24 bits) is cut into three bf16 values, s (128 + z) (16 bits) into two,
-        // each exactly, and their six products fill six of a quarter's eight places.
+        // each exactly, and their six products fill six of a quarter's eight places. (An fp16
+        // scale makes it 19 bits and three values: eight products, all but the smallest.)
         auto take_off = [&](int g, int n) {
 #pragma unroll
             for (int v = 0; v < kSub; ++v) {
@@ -264,10 +276,15 @@ struct TileProduct {
 #pragma unroll
                 for (int j = 0; j < CBW; ++j) {
                     const uint32_t md = sh.meta[g % kMetaSlots][w][(16 * j + c) * kUnits + u];
-                    const float f = -half_bits_to_f32<true>(md & 0xFFFFu) * (128.f + (float)((md >> 16) & 0xFu));
+                    const float f = -half_bits_to_f32<kScaleBF16>(md & 0xFFFFu) * (128.f + (float)((md >> 16) & 0xFu));
                     const float f1 = bf16_bits_to_f32(f32_to_half_bits<true>(f));
                     const uint32_t p = in ? pack2_rne<true>(f1, f - f1) : 0u;
-                    S[j] = make_uint4(p, p, p, 0u);
+                    uint32_t p3 = 0u;
+                    if constexpr (!kScaleBF16) {
+                        const float f3 = f - f1 - bf16_bits_to_f32(f32_to_half_bits<true>(f - f1));
+                        p3 = in ? pack2_rne<true>(f3, f3) : 0u;
+                    }
+                    S[j] = make_uint4(p, p, p, p3);
                 }
 #pragma unroll
                 for (int r = 0; r < MR; ++r) {
@@ -276,7 +293,7 @@ struct TileProduct {
                     const float r1 = X - bf16_bits_to_f32(x1);
                     const uint32_t x2 = f32_to_half_bits<true>(r1);
                     const uint32_t x3 = f32_to_half_bits<true>(r1 - bf16_bits_to_f32(x2));
-                    const uint4 xx = make_uint4(x1 * 0x10001u, x2 * 0x10001u, x3 * 0x10001u, 0u);
+                    const uint4 xx = make_uint4(x1 * 0x10001u, x2 * 0x10001u, x3 * 0x10001u, kScaleBF16 ? 0u : x1 | x2 << 16);
 #pragma unroll
                     for (int j = 0; j < CBW; ++j) acc[r][j] = mfma16x16x32<true>(S[j], xx, acc[r][j]);
                 }
@@ -365,7 +382,7 @@ struct TileProduct {
                 sc[j][u] = *reinterpret_cast<const f32x4*>(&sh.scale[w][u][16 * j + 4 * h]);
             };
             auto write_scale = [&](int j, int u, uint32_t m) {
-                sh.scale[w][u][16 * j + c] = half_bits_to_f32<kBF16>(m & 0xFFFFu);
+                sh.scale[w][u][16 * j + c] = half_bits_to_f32<kScaleBF16>(m & 0xFFFFu);
             };
             // behind the last fragment of a block the next block's scales come in, each
             // after its last use
