@@ -16,7 +16,7 @@ LIB_NAME = "libw4a16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.hip", "repack.hip", "gemv.hip", "gemv_strip.hip", "gemv_small.hip", "gemm.hip", "embedding.hip", "w4a8.hip", "measure.hip",
            "api_train.hip", "gated.hip", "product_small.hip", "gemm_grad.hip", "loss.hip",
-           "api_serve.hip", "route.hip", "moe_tile.hip", "sample.hip"]
+           "api_serve.hip", "route.hip", "moe.hip", "moe_tile.hip", "sample.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -110,12 +110,16 @@ int64_t unit_group(int64_t group_size) { return group_size == -1 ? w4a16::kRowsP
 
 int64_t moe_rows(int64_t M, int64_t T) { return M < kPairsPerPass / T ? M : kPairsPerPass / T; }
 
+size_t moe_scratch(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T, int64_t G) {
+    return w4a16::moe_small(M, K) ? w4a16::moe_small_scratch(M, K, F, E, T) : w4a16::moe_tile_layout(M, K, F, E, T, G).end;
+}
+
 size_t moe_workspace(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T, int64_t group_size) {
     const int64_t G = unit_group(group_size);
     const int64_t full = moe_rows(M, T), tail = M % full;
-    size_t need = w4a16::moe_tile_layout(full, K, F, E, T, G).end;
+    size_t need = moe_scratch(full, K, F, E, T, G);
     if (tail) {
-        const size_t rest = w4a16::moe_tile_layout(tail, K, F, E, T, G).end;
+        const size_t rest = moe_scratch(tail, K, F, E, T, G);
         if (rest > need) need = rest;
     }
     return w4a16::kSplitCounterBytes + need;
@@ -157,7 +161,9 @@ hipError_t run_moe(const void* x, const int32_t* ids, const float* weights, cons
         q.G = unit_group(group_size);
         q.act = (int)act;
         q.bf16 = dtype == W4A16_BF16;
-        const hipError_t err = w4a16::launch_moe_tile(q, ws + w4a16::kSplitCounterBytes, s);
+        uint8_t* scratch = ws + w4a16::kSplitCounterBytes;
+        const hipError_t err = w4a16::moe_small(q.M, K) ? w4a16::launch_moe_small(q, reinterpret_cast<uint32_t*>(ws), scratch, s)
+                                                        : w4a16::launch_moe_tile(q, scratch, s);
         if (err != hipSuccess) return err;
     }
     return hipSuccess;
