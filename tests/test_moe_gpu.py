@@ -64,6 +64,13 @@ def test_many_experts(w, M):
     run(w, ex, M, 32, drop=0.5)
 
 
+@pytest.mark.parametrize("K,F,G,dtype", [(4096, 128, 32, "bf16"), (4096, 256, 64, "fp16"), (4224, 128, 128, "bf16"), (2176, 384, 128, "fp16")])
+def test_long_rows(w, K, F, G, dtype):
+    ex = experts(w, 3, K, F, dtype, G)
+    for M in (1, 9, 16, 18):
+        run(w, ex, M, 2, seed=K)
+
+
 @pytest.mark.parametrize("M", [1, 16, 33, 150])
 def test_one_expert_and_one_entry(w, M):
     ex = experts(w, 1, 256, 128, "fp16", 128)

@@ -2,17 +2,18 @@
 // launches. More rows, or K over 4096: moe_tile.hip.
 //
 // Bound by the time to read the routed experts' codes, so both kernels deal equal shares of
-// them to the compute units, as product_small.hip does for one weight. Each workgroup first
-// makes the list of the experts that some row names, from ids (at most 512), in LDS; nothing
-// on the host depends on it.
+// them to the compute units. Each workgroup first makes the list of the experts that some row
+// names, from ids (at most 512), in LDS; nothing on the host depends on it. The activations
+// of all rows are one operand of 16 rows: it costs the matrix cores the same whether one row
+// of it counts or all.
 //
 // up_kernel: a unit is 8 gate and 8 up columns of one listed expert over the whole of K.
-// Workgroup g takes a contiguous share of the units; its waves split K, hold the activations
-// of all rows in registers for good (a 16-row operand costs the matrix cores the same
-// whether one row of it counts or all), and their partial sums meet in LDS, two buffers in
-// turn. h is multiplied by the row's weight for the expert, so that the down projections
-// add up, and left in two bf16 values (16 bits: one would be off by as much as the result's
-// own rounding; fp16 overflows where bf16 models do not).
+// Workgroup g takes a contiguous share of the units, each of its waves a contiguous run of
+// that share's chunks of 4 blocks of 1 KiB, whether it ends inside a unit or not: a unit that began in one
+// wave and goes on in the next meets in LDS at the end, the only barrier behind the first
+// loads. h is multiplied by the row's weight for the expert, so that the down projections add
+// up, and left in two bf16 values (16 bits: one would be off by as much as the result's own
+// rounding; fp16 overflows where bf16 models do not).
 //
 // down_kernel: one sum over (listed expert, row of Wd). Workgroup (columns, split) takes 64
 // columns and a share of that sum's row blocks, each wave every 8th of them; rows that an
@@ -37,7 +38,6 @@ constexpr int kMaxEntries = kMaxRows * kMaxChosen;
 constexpr int kDownBlocks = 4;              // 16-column blocks of a down workgroup
 constexpr int kDownColumns = kDownBlocks * kColsPerBlock;
 static_assert(kMaxEntries <= kThreads, "a thread an entry");
-static_assert(kMaxExperts <= 2 * kThreads, "two experts a thread");
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
@@ -63,15 +63,19 @@ struct Listed {
     uint32_t words[kMaxExperts / 32];
     int before[kMaxExperts / 32];
     int count;
-    int id[kMaxEntries];            // of each entry
+    int id[kMaxEntries];                    // of each entry
     int16_t expert[kMaxEntries];
-    uint32_t rows[kMaxEntries];     // bit m: row m names expert[i]
+    uint32_t rows[kMaxEntries];             // bit m: row m names expert[i]
 };
 
-__device__ __forceinline__ void make_list(const MoeArgs& a, Listed& l) {
+// an id's position among the listed experts
+__device__ __forceinline__ int place(const Listed& l, int e) {
+    return l.before[e >> 5] + __popc(l.words[e >> 5] & ((1u << (e & 31)) - 1u));
+}
+
+// id: the entry of this thread's number, -1 past the last
+__device__ __forceinline__ void make_list(const MoeArgs& a, Listed& l, int id) {
     const int tid = (int)threadIdx.x;
-    const int n = a.M * a.T;
-    int id = tid < n ? a.ids[tid] : -1;
     if (id >= a.E) id = -1;
     if (tid < kMaxExperts / 32) l.words[tid] = 0u;
     l.id[tid] = id;
@@ -90,10 +94,11 @@ __device__ __forceinline__ void make_list(const MoeArgs& a, Listed& l) {
         if (tid == kMaxExperts / 32 - 1) l.count = sum;
     }
     __syncthreads();
-    auto place = [&](int e) { return l.before[e >> 5] + __popc(l.words[e >> 5] & ((1u << (e & 31)) - 1u)); };
-    for (int e = tid; e < kMaxExperts; e += kThreads)
-        if ((l.words[e >> 5] >> (e & 31)) & 1u) l.expert[place(e)] = (int16_t)e;
-    if (id >= 0) atomicOr(&l.rows[place(id)], 1u << (tid / a.T));
+    if (id >= 0) {
+        const int i = place(l, id);
+        l.expert[i] = (int16_t)id;          // (every entry that names it writes the same)
+        atomicOr(&l.rows[i], 1u << (tid / a.T));
+    }
     __syncthreads();
 }
 
@@ -121,128 +126,189 @@ __device__ __forceinline__ uint4 operand(uint32_t d, uint32_t md) {
     return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-template <bool kBF16, int kSub, int JP>
+// lane c of each 16 takes lane c + 8's (mod 16)
+__device__ __forceinline__ uint32_t turn8(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true);
+}
+__device__ __forceinline__ float turn8(float v) { return __uint_as_float(turn8(__float_as_uint(v))); }
+
+template <bool kBF16, int kSub, int kAct>
 __global__ __launch_bounds__(kThreads) void up_kernel(const MoeArgs a) {
-    constexpr int S = JP == 4 ? 2 : 4;                     // units of a batch
-    __shared__ f32x4 part[2][S][kWaves][64];
+    constexpr int C = 4, D = kSub == 4 ? 2 : 3;            // row blocks of a chunk, chunks on their way per wave
+    extern __shared__ uint4 xs[];                          // [KB][4][64]: operands of the rows, then X [KB kSub][16]
     __shared__ Listed list;
-    __shared__ float entry_weight[kMaxEntries];
+    __shared__ uint8_t entry_of[kMaxEntries][kMaxRows];    // the first entry of a row that names a listed expert
+    __shared__ float row_weight[kMaxEntries];              // of each first entry: all the row's weights for its expert
+    __shared__ f32x4 begun[kWaves][64];                    // a wave's part of the unit that an earlier one began
+    float* entry_weight = reinterpret_cast<float*>(&begun[0][0]);      // (done with before the first unit ends)
 
     const int tid = (int)threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lane = tid & 63, c = lane & 15, h = lane >> 4;
     const int M = a.M, F = a.F, KB = a.K / kRowsPerBlock, UW = (int)padded_units(a.K, kRowsPerBlock / kSub);
-    const int kb0 = w * JP;
+    float* xsum = reinterpret_cast<float*>(xs + KB * 256);
 
-    // the activations of this wave's row blocks: row c (rows past M: row M - 1), and X
-    uint4 xf[JP][4];
-    const uint16_t* xr = a.x + (size_t)(c < M ? c : M - 1) * a.K + 8 * h;
-#pragma unroll
-    for (int j = 0; j < JP; ++j) {
-        const int kb = kb0 + j < KB ? kb0 + j : KB - 1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xf[j][i] = *reinterpret_cast<const uint4*>(xr + (size_t)kb * kRowsPerBlock + 32 * i);
-    }
+    const int id = tid < M * a.T ? a.ids[tid] : -1;
     entry_weight[tid] = tid < M * a.T ? a.weights[tid] : 0.f;
-    make_list(a, list);
+    // rows past M are left as they are: they feed results that are not used
+    {
+        const int m = tid & 15;
+        const uint16_t* xr = a.x + (size_t)m * a.K;
+        if (m < M)
+            for (int q = tid >> 4; q < a.K / 8; q += kThreads / 16)
+                xs[(q >> 2) * 64 + 16 * (q & 3) + m] = *reinterpret_cast<const uint4*>(xr + 8 * q);
+    }
+    make_list(a, list, id);
+    if (list.id[tid] >= 0) {
+        const int m = tid / a.T, e0 = m * a.T;
+        float sum = 0.f;
+        bool first = true;
+        for (int j = e0; j < e0 + a.T; ++j)
+            if (list.id[j] == id) {
+                sum += entry_weight[j];
+                first = first && j >= tid;
+            }
+        if (first) {
+            entry_of[place(list, id)][m] = (uint8_t)(tid - e0);
+            row_weight[tid] = sum;
+        }
+    }
 
     const int per = F / 8, U = list.count * per;           // units of an expert, of all
     const int nwg = (int)gridDim.x, g = xcd_share((int)blockIdx.x, nwg);
     const int lo = (int)((int64_t)g * U / nwg), hi = (int)((int64_t)(g + 1) * U / nwg);
-    if (lo >= hi) return;
+    const int per_unit = (KB + C - 1) / C, chunks = (hi - lo) * per_unit;
+    auto first_of = [&](int wave) { return (int)((int64_t)chunks * wave / kWaves); };
+    const int c0 = first_of(w), c1 = first_of(w + 1);
 
-    struct Batch {
-        uint4 q[S][JP];
-        uint32_t md[S][JP * kSub];
+    // a chunk: C row blocks of a unit, those past the last one with scales of 0
+    struct Chunk {
+        uint4 q[C];
+        uint4 md[kSub];
     };
-    auto load = [&](Batch& b, int u0) {
-        if (kb0 >= KB) return;                             // a wave past the last row block
+    int lu = lo + c0 / per_unit, lk = c0 % per_unit;       // the chunk to load next
+    const uint8_t* at;
+    const uint4* meta;
+    auto enter = [&]() {
+        const int i = lu / per;
+        const uint8_t* base = a.gate_up + (int64_t)__builtin_amdgcn_readfirstlane((int)list.expert[i]) * a.gate_up_stride;
+        const int n = (c >> 3) * F + 8 * (lu - i * per) + (c & 7);
+        at = base + ((size_t)(n >> 4) * KB) * kBlockBytes + 16 * (16 * h + (n & 15));
+        meta = reinterpret_cast<const uint4*>(base + (size_t)a.K * F + (size_t)n * UW * 4);
+    };
+    auto issue = [&](Chunk& s) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int u = u0 + s < hi ? u0 + s : hi - 1;
-            const int i = u / per;
-            const uint8_t* base = a.gate_up + (int64_t)__builtin_amdgcn_readfirstlane((int)list.expert[i]) * a.gate_up_stride;
-            const int n = (c >> 3) * F + 8 * (u - i * per) + (c & 7);
-            const uint8_t* at = base + ((size_t)(n >> 4) * KB) * kBlockBytes + 16 * (16 * h + (n & 15));
+        for (int j = 0; j < C; ++j) s.q[j] = load_once(at + (size_t)(C * lk + j < KB ? C * lk + j : KB - 1) * kBlockBytes);
 #pragma unroll
-            for (int j = 0; j < JP; ++j) b.q[s][j] = load_once(at + (size_t)(kb0 + j < KB ? kb0 + j : KB - 1) * kBlockBytes);
-            const uint32_t* m = reinterpret_cast<const uint32_t*>(base + (size_t)a.K * F) + (size_t)n * UW;
-#pragma unroll
-            for (int j = 0; j < JP * kSub; ++j) b.md[s][j] = __builtin_nontemporal_load(m + (kb0 * kSub + j < UW ? kb0 * kSub + j : UW - 1));
+        for (int v = 0; v < kSub; ++v) s.md[v] = meta[lk * kSub + v < UW / 4 ? lk * kSub + v : UW / 4 - 1];
+        if (++lk == per_unit) {                            // past the share's end the last unit repeats
+            lk = 0;
+            if (lu + 1 < hi) {
+                ++lu;
+                enter();
+            }
         }
     };
+    Chunk ring[D];
+    if (c0 < c1) {
+        enter();
+#pragma unroll
+        for (int d = 0; d < D; ++d) issue(ring[d]);
+    }
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    [[maybe_unused]] f32x4 X[JP][kSub];
     if constexpr (kBF16) {
         const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-#pragma unroll
-        for (int j = 0; j < JP; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int u = i * kSub / 4;
-                X[j][u] = mfma16x16x32<true>(xf[j][i], ones, i % (4 / kSub) == 0 ? zero : X[j][u]);
-            }
-    }
-    // rows 4 h + e, column c of unit s
-    auto multiply = [&](const Batch& b, int s) {
-        f32x4 acc = zero;
-#pragma unroll
-        for (int j = 0; j < JP; ++j) {
-            if (kb0 + j >= KB) continue;
-            f32x4 T[kSub];
+        for (int kb = w; kb < KB; kb += kWaves) {
+            f32x4 X[kSub];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int u = i * kSub / 4;
-                T[u] = mfma16x16x32<kBF16>(xf[j][i], operand<kBF16>(word_of(b.q[s][j], i), b.md[s][j * kSub + u]),
-                                           i % (4 / kSub) == 0 ? zero : T[u]);
+                X[u] = mfma16x16x32<true>(xs[(kb * 4 + i) * 64 + lane], ones, i % (4 / kSub) == 0 ? zero : X[u]);
             }
+            if (c == 0) {
 #pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                const uint32_t md = b.md[s][j * kSub + u];
-                const float sc = half_bits_to_f32<kBF16>(md & 0xFFFFu);
-                const float zb = 16.f + (float)((md >> 16) & 0xFu);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(sc, kBF16 ? fmaf(-zb, X[j][u][e], T[u][e]) : T[u][e], acc[e]);
+                for (int u = 0; u < kSub; ++u) *reinterpret_cast<f32x4*>(xsum + (kb * kSub + u) * 16 + 4 * h) = X[u];
             }
         }
-        return acc;
-    };
-    auto total = [&](int buf, int s, int m, int col) {
-        float v = 0.f;
-        const int at = 16 * (m >> 2) + col, e = m & 3;
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i) v += reinterpret_cast<const float*>(&part[buf][s][i][at])[e];
-        return v;
-    };
-    constexpr int kRowStep = kThreads / (8 * S);           // rows met at a time
-    static_assert(kRowStep >= kMaxRows, "a thread meets one row");
-    const int oc = tid % 8, os = tid / 8 % S, om = tid / (8 * S);
-    auto turn = [&](Batch& cur, Batch& nxt, int u0, int buf) {
-        if (u0 + S < hi) load(nxt, u0 + S);
-#pragma unroll
-        for (int s = 0; s < S; ++s) part[buf][s][w][lane] = multiply(cur, s);
-        __syncthreads();
-        const int u = u0 + os;
-        if (u >= hi || om >= M) return;
+    }
+    __syncthreads();
+
+    // rows 4 h + e, column c of a finished unit: lanes c < 8 make h of rows 4 h, 4 h + 1, the others of the next two
+    auto finish = [&](const f32x4 acc, int u) {
         const int i = u / per;
-        if (!((list.rows[i] >> om) & 1u)) return;
-        const int expert = list.expert[i];
-        float weight = 0.f;
-        for (int j = 0; j < a.T; ++j) weight += list.id[om * a.T + j] == expert ? entry_weight[om * a.T + j] : 0.f;
-        const float gv = total(buf, os, om, oc), uv = total(buf, os, om, oc + 8);
-        float slope;
-        const float pr = a.act == 0 ? gate_prob<0>(gv, &slope) : a.act == 1 ? gate_prob<1>(gv, &slope) : gate_prob<2>(gv, &slope);
-        const float o = gv * pr * uv * weight;
-        const uint32_t top = f32_to_half_bits<true>(o);
-        uint16_t* to = a.h + (((size_t)i * M + om) * 2) * F + 8 * (u - i * per) + oc;
-        to[0] = (uint16_t)top;
-        to[F] = f32_to_half_bits<true>(o - bf16_bits_to_f32(top));
+        const uint32_t rows = list.rows[i];
+        const bool lower = c < 8;
+        const f32x4 other = {turn8(acc[0]), turn8(acc[1]), turn8(acc[2]), turn8(acc[3])};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int m = 4 * h + e + (lower ? 0 : 2);
+            if (!((rows >> m) & 1u)) continue;
+            const float gv = lower ? acc[e] : other[2 + e], uv = lower ? other[e] : acc[2 + e];
+            const float weight = row_weight[m * a.T + entry_of[i][m]];
+            float slope;
+            const float pr = gate_prob<kAct>(gv, &slope);
+            const float o = gv * pr * uv * weight;
+            const uint32_t top = f32_to_half_bits<true>(o);
+            uint16_t* to = a.h + (((size_t)i * M + m) * 2) * F + 8 * (u - i * per) + (c & 7);
+            to[0] = (uint16_t)top;
+            to[F] = f32_to_half_bits<true>(o - bf16_bits_to_f32(top));
+        }
     };
-    Batch b0, b1;
-    load(b0, lo);
-    for (int u0 = lo; u0 < hi; u0 += 2 * S) {
-        turn(b0, b1, u0, 0);
-        if (u0 + S < hi) turn(b1, b0, u0 + S, 1);
+    int u = lo + c0 / per_unit, k = c0 % per_unit;         // the chunk to multiply next
+    bool own = k == 0;                                     // the unit began in this wave
+    f32x4 acc = zero;
+    auto multiply = [&](const Chunk& s) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const bool in = C * k + j < KB;
+            const int kb = in ? C * k + j : KB - 1;
+            f32x4 T[kSub];
+            uint32_t md[kSub];
+#pragma unroll
+            for (int v = 0; v < kSub; ++v) md[v] = word_of(s.md[(j * kSub + v) / 4], (j * kSub + v) % 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int v = i * kSub / 4;
+                T[v] = mfma16x16x32<kBF16>(xs[(kb * 4 + i) * 64 + lane], operand<kBF16>(word_of(s.q[j], i), md[v]),
+                                           i % (4 / kSub) == 0 ? zero : T[v]);
+            }
+#pragma unroll
+            for (int v = 0; v < kSub; ++v) {
+                const float sc = in ? half_bits_to_f32<kBF16>(md[v] & 0xFFFFu) : 0.f;
+                if constexpr (kBF16) {
+                    const float zb = 16.f + (float)((md[v] >> 16) & 0xFu);
+                    const f32x4 X = *reinterpret_cast<const f32x4*>(xsum + (kb * kSub + v) * 16 + 4 * h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(sc, fmaf(-zb, X[e], T[v][e]), acc[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(sc, T[v][e], acc[e]);
+                }
+            }
+        }
+        if (++k == per_unit) {
+            if (own) finish(acc, u);
+            else begun[w][lane] = acc;
+            acc = zero;
+            k = 0;
+            own = true;
+            ++u;
+        }
+    };
+    for (int b = c0; b < c1; b += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (b + d < c1) multiply(ring[d]);
+            issue(ring[d]);
+        }
+    }
+    if (k && !own) begun[w][lane] = acc;
+    __syncthreads();
+    if (k && own) {
+        // the waves that went on with the unit, in their order
+        const int end = (u + 1 - lo) * per_unit;
+        for (int v = w + 1; first_of(v) < end; ++v) acc += begun[v][lane];
+        finish(acc, u);
     }
 }
 
@@ -258,7 +324,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(const MoeArgs a) {
     const int M = a.M, K = a.K, F = a.F, FB = F / kRowsPerBlock, UW = (int)padded_units(F, kRowsPerBlock / kSub);
     const int groups = K / kDownColumns;
     const int group = (int)blockIdx.x % groups, split = (int)blockIdx.x / groups;
-    make_list(a, list);
+    make_list(a, list, tid < M * a.T ? a.ids[tid] : -1);
 
     const int all = list.count * FB;                       // row blocks of the whole sum
     const int lo = (int)((int64_t)all * split / a.splits), hi = (int)((int64_t)all * (split + 1) / a.splits);
@@ -318,15 +384,16 @@ __global__ __launch_bounds__(kThreads) void down_kernel(const MoeArgs a) {
             }
         }
     };
-    Batch b0, b1;
-    int r = lo + w;
-    if (r < hi) load(b0, r);
-    for (; r < hi; r += 2 * kWaves) {
-        if (r + kWaves < hi) load(b1, r + kWaves);
-        multiply(b0);
-        if (r + kWaves < hi) {
-            if (r + 2 * kWaves < hi) load(b0, r + 2 * kWaves);
-            multiply(b1);
+    constexpr int D = 2;                                   // row blocks on their way per wave
+    Batch ring[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (lo + w + d * kWaves < hi) load(ring[d], lo + w + d * kWaves);
+    for (int r = lo + w; r < hi; r += D * kWaves) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (r + d * kWaves < hi) multiply(ring[d]);
+            if (r + (d + D) * kWaves < hi) load(ring[d], r + (d + D) * kWaves);
         }
     }
 #pragma unroll
@@ -386,11 +453,14 @@ __global__ __launch_bounds__(kThreads) void down_kernel(const MoeArgs a) {
 }
 
 template <bool kBF16, int kSub>
-void launch_sub(const MoeArgs& a, int grid, int jp, hipStream_t s) {
-    if (jp <= 1) hipLaunchKernelGGL((up_kernel<kBF16, kSub, 1>), dim3(grid), dim3(kThreads), 0, s, a);
-    else if (jp <= 2) hipLaunchKernelGGL((up_kernel<kBF16, kSub, 2>), dim3(grid), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((up_kernel<kBF16, kSub, 4>), dim3(grid), dim3(kThreads), 0, s, a);
+hipError_t launch_sub(const MoeArgs& a, int grid, hipStream_t s) {
+    const int KB = a.K / kRowsPerBlock;
+    const size_t lds = (size_t)KB * (4096 + 64 * kSub);    // 136 KiB at most, beside 23.3 of the kernel's own
+    if (a.act == 0) hipLaunchKernelGGL((up_kernel<kBF16, kSub, 0>), dim3(grid), dim3(kThreads), lds, s, a);
+    else if (a.act == 1) hipLaunchKernelGGL((up_kernel<kBF16, kSub, 1>), dim3(grid), dim3(kThreads), lds, s, a);
+    else hipLaunchKernelGGL((up_kernel<kBF16, kSub, 2>), dim3(grid), dim3(kThreads), lds, s, a);
     hipLaunchKernelGGL((down_kernel<kBF16, kSub>), dim3(a.K / kDownColumns * a.splits), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
 }
 
 int64_t most_listed(int64_t M, int64_t E, int64_t T) { return E < M * T ? E : M * T; }
@@ -403,13 +473,13 @@ int down_splits(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T) {
     return n < 1 ? 1 : (int)n;
 }
 
-size_t round256(size_t v) { return (v + 255) / 256 * 256; }
-
-size_t h_bytes(int64_t M, int64_t F, int64_t E, int64_t T) { return round256((size_t)most_listed(M, E, T) * (size_t)(4 * M * F)); }
+size_t h_bytes(int64_t M, int64_t F, int64_t E, int64_t T) {
+    return ((size_t)most_listed(M, E, T) * (size_t)(4 * M * F) + 255) / 256 * 256;
+}
 
 }  // namespace
 
-bool moe_small(int64_t M, int64_t K) { return M <= kMaxRows && K <= 4 * kWaves * kRowsPerBlock; }
+bool moe_small(int64_t M, int64_t K) { return M <= kMaxRows && K <= 4096; }
 
 size_t moe_small_scratch(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T) {
     const int splits = down_splits(M, K, F, E, T);
@@ -430,19 +500,18 @@ hipError_t launch_moe_small(const MoeCall& q, uint32_t* counters, uint8_t* scrat
     a.h = reinterpret_cast<uint16_t*>(scratch);
     a.counters = counters;
     a.partials = reinterpret_cast<float*>(scratch + h_bytes(q.M, q.F, q.E, q.T));
+    a.splits = down_splits(q.M, q.K, q.F, q.E, q.T);
     a.M = (int)q.M;
     a.K = (int)q.K;
     a.F = (int)q.F;
     a.E = (int)q.E;
     a.T = (int)q.T;
-    a.splits = down_splits(q.M, q.K, q.F, q.E, q.T);
     a.act = q.act;
     const int64_t units = most_listed(q.M, q.E, q.T) * (q.F / 8);
     const int grid = (int)(units < kTargetWorkgroups ? units : kTargetWorkgroups);
-    const int jp = (int)((q.K / kRowsPerBlock + kWaves - 1) / kWaves), sub = units_per_block(q.G);
-    if (q.bf16) sub == 4 ? launch_sub<true, 4>(a, grid, jp, stream) : sub == 2 ? launch_sub<true, 2>(a, grid, jp, stream) : launch_sub<true, 1>(a, grid, jp, stream);
-    else sub == 4 ? launch_sub<false, 4>(a, grid, jp, stream) : sub == 2 ? launch_sub<false, 2>(a, grid, jp, stream) : launch_sub<false, 1>(a, grid, jp, stream);
-    return hipGetLastError();
+    const int sub = units_per_block(q.G);
+    if (q.bf16) return sub == 4 ? launch_sub<true, 4>(a, grid, stream) : sub == 2 ? launch_sub<true, 2>(a, grid, stream) : launch_sub<true, 1>(a, grid, stream);
+    return sub == 4 ? launch_sub<false, 4>(a, grid, stream) : sub == 2 ? launch_sub<false, 2>(a, grid, stream) : launch_sub<false, 1>(a, grid, stream);
 }
 
 }  // namespace w4a16
