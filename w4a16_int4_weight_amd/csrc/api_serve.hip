@@ -111,7 +111,7 @@ int64_t unit_group(int64_t group_size) { return group_size == -1 ? w4a16::kRowsP
 int64_t moe_rows(int64_t M, int64_t T) { return M < kPairsPerPass / T ? M : kPairsPerPass / T; }
 
 size_t moe_scratch(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T, int64_t G) {
-    return w4a16::moe_small(M, K) ? w4a16::moe_small_scratch(M, K, F, E, T) : w4a16::moe_tile_layout(M, K, F, E, T, G).end;
+    return w4a16::moe_small(M, K, T) ? w4a16::moe_small_scratch(M, K, F, E, T) : w4a16::moe_tile_layout(M, K, F, E, T, G).end;
 }
 
 size_t moe_workspace(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T, int64_t group_size) {
@@ -162,7 +162,7 @@ hipError_t run_moe(const void* x, const int32_t* ids, const float* weights, cons
         q.act = (int)act;
         q.bf16 = dtype == W4A16_BF16;
         uint8_t* scratch = ws + w4a16::kSplitCounterBytes;
-        const hipError_t err = w4a16::moe_small(q.M, K) ? w4a16::launch_moe_small(q, reinterpret_cast<uint32_t*>(ws), scratch, s)
+        const hipError_t err = w4a16::moe_small(q.M, K, T) ? w4a16::launch_moe_small(q, reinterpret_cast<uint32_t*>(ws), scratch, s)
                                                         : w4a16::launch_moe_tile(q, scratch, s);
         if (err != hipSuccess) return err;
     }

@@ -257,7 +257,7 @@ struct MoeCall {
     bool bf16;
 };
 // csrc/moe.hip, where moe_small: counters zero, left zero; scratch of moe_small_scratch bytes
-bool moe_small(int64_t M, int64_t K);
+bool moe_small(int64_t M, int64_t K, int64_t T);
 size_t moe_small_scratch(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T);
 hipError_t launch_moe_small(const MoeCall& call, uint32_t* counters, uint8_t* scratch, hipStream_t stream);
 // csrc/moe_tile.hip: scratch of layout.end bytes, nothing in it kept between calls

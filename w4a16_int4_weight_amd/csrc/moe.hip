@@ -1,15 +1,15 @@
-// Mixture of experts for up to 16 rows: the routed experts' codes are streamed once, in two
+// Mixture of experts for up to 16 rows and 256 entries: the routed experts' codes are streamed once, in two
 // launches. More rows, or K over 4096: moe_tile.hip.
 //
 // Bound by the time to read the routed experts' codes, so both kernels deal equal shares of
 // them to the compute units. Each workgroup first makes the list of the experts that some row
-// names, from ids (at most 512), in LDS; nothing on the host depends on it. The activations
+// names, from ids (at most 256), in LDS; nothing on the host depends on it. The activations
 // of all rows are one operand of 16 rows: it costs the matrix cores the same whether one row
 // of it counts or all.
 //
-// up_kernel: a unit is 8 gate and 8 up columns of one listed expert over the whole of K.
+// up_kernel: a unit is 16 gate and 16 up columns of one listed expert over the whole of K.
 // Workgroup g takes a contiguous share of the units, each of its waves a contiguous run of
-// that share's chunks of 4 blocks of 1 KiB, whether it ends inside a unit or not: a unit that began in one
+// that share's chunks of 4 row blocks, whether it ends inside a unit or not: a unit that began in one
 // wave and goes on in the next meets in LDS at the end, the only barrier behind the first
 // loads. h is multiplied by the row's weight for the expert, so that the down projections add
 // up, and left in two bf16 values (16 bits: one would be off by as much as the result's own
@@ -34,7 +34,7 @@ constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTargetWorkgroups = 256;      // one per compute unit
 constexpr int kMaxRows = 16;
-constexpr int kMaxEntries = kMaxRows * kMaxChosen;
+constexpr int kMaxEntries = 256;            // M T: what LDS holds beside 16 rows of 4096
 constexpr int kDownBlocks = 4;              // 16-column blocks of a down workgroup
 constexpr int kDownColumns = kDownBlocks * kColsPerBlock;
 static_assert(kMaxEntries <= kThreads, "a thread an entry");
@@ -60,46 +60,43 @@ struct MoeArgs {
 
 // The experts that some row names, in rising order, and which rows name each.
 struct Listed {
-    uint32_t words[kMaxExperts / 32];
-    int before[kMaxExperts / 32];
-    int count;
+    uint4 words[kMaxExperts / 128];         // a bit an expert
     int id[kMaxEntries];                    // of each entry
     int16_t expert[kMaxEntries];
     uint32_t rows[kMaxEntries];             // bit m: row m names expert[i]
 };
 
-// an id's position among the listed experts
-__device__ __forceinline__ int place(const Listed& l, int e) {
-    return l.before[e >> 5] + __popc(l.words[e >> 5] & ((1u << (e & 31)) - 1u));
-}
-
-// id: the entry of this thread's number, -1 past the last
-__device__ __forceinline__ void make_list(const MoeArgs& a, Listed& l, int id) {
+// id: the entry of this thread's number, -1 past the last. Returns how many experts are
+// listed; `place`: the position of this thread's entry among them.
+__device__ __forceinline__ int make_list(const MoeArgs& a, Listed& l, int id, int* place) {
     const int tid = (int)threadIdx.x;
+    uint32_t* words = reinterpret_cast<uint32_t*>(l.words);
+    if (tid < kMaxExperts / 32) words[tid] = 0u;
+    if (tid < kMaxEntries) l.rows[tid] = 0u;
+    __syncthreads();
     if (id >= a.E) id = -1;
-    if (tid < kMaxExperts / 32) l.words[tid] = 0u;
-    l.id[tid] = id;
-    l.rows[tid] = 0u;
+    if (tid < kMaxEntries) l.id[tid] = id;
+    if (id >= 0) atomicOr(&words[id >> 5], 1u << (id & 31));
     __syncthreads();
-    if (id >= 0) atomicOr(&l.words[id >> 5], 1u << (id & 31));
-    __syncthreads();
-    if (tid < 64) {
-        const int own = tid < kMaxExperts / 32 ? __popc(l.words[tid]) : 0;
-        int sum = own;
-        for (int s = 1; s < 32; s <<= 1) {
-            const int o = __shfl_up(sum, s);
-            if (tid >= s) sum += o;
+    int count = 0, before = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxExperts / 128; ++k) {
+        const uint4 q = l.words[k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t v = e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w;
+            const int own = (id >> 5) - (4 * k + e);       // > 0: a word below the id's
+            before += __popc(own > 0 ? v : own == 0 ? v & ((1u << (id & 31)) - 1u) : 0u);
+            count += __popc(v);
         }
-        if (tid < kMaxExperts / 32) l.before[tid] = sum - own;
-        if (tid == kMaxExperts / 32 - 1) l.count = sum;
     }
-    __syncthreads();
     if (id >= 0) {
-        const int i = place(l, id);
-        l.expert[i] = (int16_t)id;          // (every entry that names it writes the same)
-        atomicOr(&l.rows[i], 1u << (tid / a.T));
+        l.expert[before] = (int16_t)id;     // (every entry that names it writes the same)
+        atomicOr(&l.rows[before], 1u << (tid / a.T));
     }
+    *place = before;
     __syncthreads();
+    return __builtin_amdgcn_readfirstlane(count);
 }
 
 __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
@@ -126,21 +123,15 @@ __device__ __forceinline__ uint4 operand(uint32_t d, uint32_t md) {
     return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-// lane c of each 16 takes lane c + 8's (mod 16)
-__device__ __forceinline__ uint32_t turn8(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true);
-}
-__device__ __forceinline__ float turn8(float v) { return __uint_as_float(turn8(__float_as_uint(v))); }
-
 template <bool kBF16, int kSub, int kAct>
 __global__ __launch_bounds__(kThreads) void up_kernel(const MoeArgs a) {
-    constexpr int C = 4, D = kSub == 4 ? 2 : 3;            // row blocks of a chunk, chunks on their way per wave
+    constexpr int C = 4;                                   // row blocks of a chunk
     extern __shared__ uint4 xs[];                          // [KB][4][64]: operands of the rows, then X [KB kSub][16]
     __shared__ Listed list;
     __shared__ uint8_t entry_of[kMaxEntries][kMaxRows];    // the first entry of a row that names a listed expert
     __shared__ float row_weight[kMaxEntries];              // of each first entry: all the row's weights for its expert
-    __shared__ f32x4 begun[kWaves][64];                    // a wave's part of the unit that an earlier one began
-    float* entry_weight = reinterpret_cast<float*>(&begun[0][0]);      // (done with before the first unit ends)
+    __shared__ f32x4 begun[kWaves][2][64];                 // a wave's part of the unit that an earlier one began
+    float* entry_weight = reinterpret_cast<float*>(&begun[0][0][0]);      // (done with before the first unit ends)
 
     const int tid = (int)threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -149,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const MoeArgs a) {
     float* xsum = reinterpret_cast<float*>(xs + KB * 256);
 
     const int id = tid < M * a.T ? a.ids[tid] : -1;
-    entry_weight[tid] = tid < M * a.T ? a.weights[tid] : 0.f;
+    if (tid < M * a.T) entry_weight[tid] = a.weights[tid];
     // rows past M are left as they are: they feed results that are not used
     {
         const int m = tid & 15;
@@ -158,8 +149,9 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const MoeArgs a) {
             for (int q = tid >> 4; q < a.K / 8; q += kThreads / 16)
                 xs[(q >> 2) * 64 + 16 * (q & 3) + m] = *reinterpret_cast<const uint4*>(xr + 8 * q);
     }
-    make_list(a, list, id);
-    if (list.id[tid] >= 0) {
+    int place;
+    const int listed = make_list(a, list, id, &place);
+    if (tid < kMaxEntries && list.id[tid] >= 0) {
         const int m = tid / a.T, e0 = m * a.T;
         float sum = 0.f;
         bool first = true;
@@ -169,12 +161,12 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const MoeArgs a) {
                 first = first && j >= tid;
             }
         if (first) {
-            entry_of[place(list, id)][m] = (uint8_t)(tid - e0);
+            entry_of[place][m] = (uint8_t)(tid - e0);
             row_weight[tid] = sum;
         }
     }
 
-    const int per = F / 8, U = list.count * per;           // units of an expert, of all
+    const int per = F / 16, U = listed * per;              // units of an expert, of all
     const int nwg = (int)gridDim.x, g = xcd_share((int)blockIdx.x, nwg);
     const int lo = (int)((int64_t)g * U / nwg), hi = (int)((int64_t)(g + 1) * U / nwg);
     const int per_unit = (KB + C - 1) / C, chunks = (hi - lo) * per_unit;
@@ -183,37 +175,50 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const MoeArgs a) {
 
     // a chunk: C row blocks of a unit, those past the last one with scales of 0
     struct Chunk {
-        uint4 q[C];
-        uint4 md[kSub];
+        uint4 q[2][C];                                     // gate, up
+        uint4 md[2][kSub];
     };
-    int lu = lo + c0 / per_unit, lk = c0 % per_unit;       // the chunk to load next
-    const uint8_t* at;
-    const uint4* meta;
+    // The chunk to load next. An odd run's last turn loads one more: its last chunk's first
+    // lines again (steps of 0), so that the waits count the same in every turn.
+    int lu = lo + c0 / per_unit, lk = c0 % per_unit, left = c1 - c0;
+    const uint8_t* at = a.gate_up;
+    const uint4* meta = reinterpret_cast<const uint4*>(a.gate_up);
+    size_t up_codes = 0, up_meta = 0;
+    uint32_t step = 0, meta_step = 0;
     auto enter = [&]() {
-        const int i = lu / per;
+        const int i = lu / per, nb = lu - i * per;
         const uint8_t* base = a.gate_up + (int64_t)__builtin_amdgcn_readfirstlane((int)list.expert[i]) * a.gate_up_stride;
-        const int n = (c >> 3) * F + 8 * (lu - i * per) + (c & 7);
-        at = base + ((size_t)(n >> 4) * KB) * kBlockBytes + 16 * (16 * h + (n & 15));
-        meta = reinterpret_cast<const uint4*>(base + (size_t)a.K * F + (size_t)n * UW * 4);
+        at = base + (size_t)nb * KB * kBlockBytes + 16 * lane;
+        meta = reinterpret_cast<const uint4*>(base + (size_t)a.K * F) + (size_t)(16 * nb + c) * (UW / 4);
     };
     auto issue = [&](Chunk& s) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) s.q[j] = load_once(at + (size_t)(C * lk + j < KB ? C * lk + j : KB - 1) * kBlockBytes);
+        for (int p = 0; p < 2; ++p) {
 #pragma unroll
-        for (int v = 0; v < kSub; ++v) s.md[v] = meta[lk * kSub + v < UW / 4 ? lk * kSub + v : UW / 4 - 1];
-        if (++lk == per_unit) {                            // past the share's end the last unit repeats
+            for (int j = 0; j < C; ++j)
+                s.q[p][j] = load_once(at + p * up_codes + (size_t)((uint32_t)(C * lk + j < KB ? C * lk + j : KB - 1) * step));
+#pragma unroll
+            for (int v = 0; v < kSub; ++v)
+                s.md[p][v] = meta[p * up_meta + (uint32_t)(lk * kSub + v < UW / 4 ? lk * kSub + v : UW / 4 - 1) * meta_step];
+        }
+        if (--left <= 0) {
+            up_codes = up_meta = 0;
+            step = meta_step = 0;
+        } else if (++lk == per_unit) {
             lk = 0;
-            if (lu + 1 < hi) {
-                ++lu;
-                enter();
-            }
+            ++lu;
+            enter();
         }
     };
-    Chunk ring[D];
-    if (c0 < c1) {
+    Chunk r0, r1;
+    if (left > 0) {
+        up_codes = (size_t)(F / kColsPerBlock) * KB * kBlockBytes;
+        up_meta = (size_t)F * UW / 4;
+        step = kBlockBytes;
+        meta_step = 1;
         enter();
-#pragma unroll
-        for (int d = 0; d < D; ++d) issue(ring[d]);
+        issue(r0);
+        if (left > 0) issue(r1);
     }
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     if constexpr (kBF16) {
@@ -233,81 +238,92 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const MoeArgs a) {
     }
     __syncthreads();
 
-    // rows 4 h + e, column c of a finished unit: lanes c < 8 make h of rows 4 h, 4 h + 1, the others of the next two
-    auto finish = [&](const f32x4 acc, int u) {
+    // rows 4 h + e, column c of a finished unit
+    auto finish = [&](const f32x4 (&acc)[2], int u) {
         const int i = u / per;
-        const uint32_t rows = list.rows[i];
-        const bool lower = c < 8;
-        const f32x4 other = {turn8(acc[0]), turn8(acc[1]), turn8(acc[2]), turn8(acc[3])};
+        const uint32_t rows = list.rows[i] >> (4 * h);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int m = 4 * h + e + (lower ? 0 : 2);
-            if (!((rows >> m) & 1u)) continue;
-            const float gv = lower ? acc[e] : other[2 + e], uv = lower ? other[e] : acc[2 + e];
+        for (int e = 0; e < 4; ++e) {
+            if (!((rows >> e) & 1u)) continue;
+            const int m = 4 * h + e;
             const float weight = row_weight[m * a.T + entry_of[i][m]];
             float slope;
-            const float pr = gate_prob<kAct>(gv, &slope);
-            const float o = gv * pr * uv * weight;
+            const float o = acc[0][e] * gate_prob<kAct>(acc[0][e], &slope) * acc[1][e] * weight;
             const uint32_t top = f32_to_half_bits<true>(o);
-            uint16_t* to = a.h + (((size_t)i * M + m) * 2) * F + 8 * (u - i * per) + (c & 7);
+            uint16_t* to = a.h + (((size_t)i * M + m) * 2) * F + 16 * (u - i * per) + c;
             to[0] = (uint16_t)top;
             to[F] = f32_to_half_bits<true>(o - bf16_bits_to_f32(top));
         }
     };
     int u = lo + c0 / per_unit, k = c0 % per_unit;         // the chunk to multiply next
     bool own = k == 0;                                     // the unit began in this wave
-    f32x4 acc = zero;
+    f32x4 acc[2] = {zero, zero};
     auto multiply = [&](const Chunk& s) {
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const bool in = C * k + j < KB;
             const int kb = in ? C * k + j : KB - 1;
-            f32x4 T[kSub];
-            uint32_t md[kSub];
+            f32x4 T[2][kSub];
+            uint32_t md[2][kSub];
 #pragma unroll
-            for (int v = 0; v < kSub; ++v) md[v] = word_of(s.md[(j * kSub + v) / 4], (j * kSub + v) % 4);
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int v = 0; v < kSub; ++v) md[p][v] = word_of(s.md[p][(j * kSub + v) / 4], (j * kSub + v) % 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int v = i * kSub / 4;
-                T[v] = mfma16x16x32<kBF16>(xs[(kb * 4 + i) * 64 + lane], operand<kBF16>(word_of(s.q[j], i), md[v]),
-                                           i % (4 / kSub) == 0 ? zero : T[v]);
+                const uint4 x = xs[(kb * 4 + i) * 64 + lane];
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    T[p][v] = mfma16x16x32<kBF16>(x, operand<kBF16>(word_of(s.q[p][j], i), md[p][v]), i % (4 / kSub) == 0 ? zero : T[p][v]);
             }
 #pragma unroll
             for (int v = 0; v < kSub; ++v) {
-                const float sc = in ? half_bits_to_f32<kBF16>(md[v] & 0xFFFFu) : 0.f;
-                if constexpr (kBF16) {
-                    const float zb = 16.f + (float)((md[v] >> 16) & 0xFu);
-                    const f32x4 X = *reinterpret_cast<const f32x4*>(xsum + (kb * kSub + v) * 16 + 4 * h);
+                [[maybe_unused]] f32x4 X;
+                if constexpr (kBF16) X = *reinterpret_cast<const f32x4*>(xsum + (kb * kSub + v) * 16 + 4 * h);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(sc, fmaf(-zb, X[e], T[v][e]), acc[e]);
-                } else {
+                for (int p = 0; p < 2; ++p) {
+                    const float sc = in ? half_bits_to_f32<kBF16>(md[p][v] & 0xFFFFu) : 0.f;
+                    const float zb = 16.f + (float)((md[p][v] >> 16) & 0xFu);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(sc, T[v][e], acc[e]);
+                    for (int e = 0; e < 4; ++e) acc[p][e] = fmaf(sc, kBF16 ? fmaf(-zb, X[e], T[p][v][e]) : T[p][v][e], acc[p][e]);
                 }
             }
         }
         if (++k == per_unit) {
-            if (own) finish(acc, u);
-            else begun[w][lane] = acc;
-            acc = zero;
+            if (own) {
+                finish(acc, u);
+            } else {
+                begun[w][0][lane] = acc[0];
+                begun[w][1][lane] = acc[1];
+            }
+            acc[0] = acc[1] = zero;
             k = 0;
             own = true;
             ++u;
         }
     };
-    for (int b = c0; b < c1; b += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (b + d < c1) multiply(ring[d]);
-            issue(ring[d]);
-        }
+    int b = c0;
+    for (; b + 2 < c1; b += 2) {
+        multiply(r0);
+        issue(r0);
+        multiply(r1);
+        issue(r1);
     }
-    if (k && !own) begun[w][lane] = acc;
+    if (b < c1) multiply(r0);
+    if (b + 1 < c1) multiply(r1);
+    if (k && !own) {
+        begun[w][0][lane] = acc[0];
+        begun[w][1][lane] = acc[1];
+    }
     __syncthreads();
     if (k && own) {
         // the waves that went on with the unit, in their order
         const int end = (u + 1 - lo) * per_unit;
-        for (int v = w + 1; first_of(v) < end; ++v) acc += begun[v][lane];
+        for (int v = w + 1; first_of(v) < end; ++v) {
+            acc[0] += begun[v][0][lane];
+            acc[1] += begun[v][1][lane];
+        }
         finish(acc, u);
     }
 }
@@ -324,9 +340,10 @@ __global__ __launch_bounds__(kThreads) void down_kernel(const MoeArgs a) {
     const int M = a.M, K = a.K, F = a.F, FB = F / kRowsPerBlock, UW = (int)padded_units(F, kRowsPerBlock / kSub);
     const int groups = K / kDownColumns;
     const int group = (int)blockIdx.x % groups, split = (int)blockIdx.x / groups;
-    make_list(a, list, tid < M * a.T ? a.ids[tid] : -1);
+    int place;
+    const int listed = make_list(a, list, tid < M * a.T ? a.ids[tid] : -1, &place);
 
-    const int all = list.count * FB;                       // row blocks of the whole sum
+    const int all = listed * FB;                       // row blocks of the whole sum
     const int lo = (int)((int64_t)all * split / a.splits), hi = (int)((int64_t)all * (split + 1) / a.splits);
     struct Batch {
         uint4 q[CB];
@@ -455,7 +472,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(const MoeArgs a) {
 template <bool kBF16, int kSub>
 hipError_t launch_sub(const MoeArgs& a, int grid, hipStream_t s) {
     const int KB = a.K / kRowsPerBlock;
-    const size_t lds = (size_t)KB * (4096 + 64 * kSub);    // 136 KiB at most, beside 23.3 of the kernel's own
+    const size_t lds = (size_t)KB * (4096 + 64 * kSub);    // 136 KiB at most, beside 23.8 of the kernel's own
     if (a.act == 0) hipLaunchKernelGGL((up_kernel<kBF16, kSub, 0>), dim3(grid), dim3(kThreads), lds, s, a);
     else if (a.act == 1) hipLaunchKernelGGL((up_kernel<kBF16, kSub, 1>), dim3(grid), dim3(kThreads), lds, s, a);
     else hipLaunchKernelGGL((up_kernel<kBF16, kSub, 2>), dim3(grid), dim3(kThreads), lds, s, a);
@@ -479,7 +496,7 @@ size_t h_bytes(int64_t M, int64_t F, int64_t E, int64_t T) {
 
 }  // namespace
 
-bool moe_small(int64_t M, int64_t K) { return M <= kMaxRows && K <= 4096; }
+bool moe_small(int64_t M, int64_t K, int64_t T) { return M <= kMaxRows && M * T <= kMaxEntries && K <= 4096; }
 
 size_t moe_small_scratch(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T) {
     const int splits = down_splits(M, K, F, E, T);
@@ -507,7 +524,7 @@ hipError_t launch_moe_small(const MoeCall& q, uint32_t* counters, uint8_t* scrat
     a.E = (int)q.E;
     a.T = (int)q.T;
     a.act = q.act;
-    const int64_t units = most_listed(q.M, q.E, q.T) * (q.F / 8);
+    const int64_t units = most_listed(q.M, q.E, q.T) * (q.F / 16);
     const int grid = (int)(units < kTargetWorkgroups ? units : kTargetWorkgroups);
     const int sub = units_per_block(q.G);
     if (q.bf16) return sub == 4 ? launch_sub<true, 4>(a, grid, stream) : sub == 2 ? launch_sub<true, 2>(a, grid, stream) : launch_sub<true, 1>(a, grid, stream);

@@ -2,10 +2,13 @@
 //
 // The choice is discrete, so l is summed in fp64: a product of two 16-bit values is exact in
 // fp32 (22 bits at most), and its sums here err in the 53rd bit. A wave forms one expert's l
-// of one row, its lanes splitting K in 16-byte pieces; 8 waves of a workgroup take 8 experts
-// of the same rows. The workgroup that finishes its rows' last experts (a counter, as
-// split_k.h has it) reads the l of its rows back and chooses: a wave a row, each lane holding
-// every 64th expert.
+// of a group of rows, the expert's weights in registers, its lanes splitting K in 16-byte
+// pieces; 8 waves of a workgroup take 8 experts of the same rows. The workgroup that finishes
+// its rows' last experts (a counter, as split_k.h has it) reads the l of its rows back and
+// chooses, a wave a row: each lane holds every 64th expert, the largest of all lanes comes by
+// row shifts, its owner by a ballot.
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 #include "split_k.h"
@@ -15,7 +18,7 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kMaxPerLane = kMaxExperts / 64;
+constexpr int kPieces = 4;                  // 16-byte pieces of the weights a lane holds: K up to 2048 at a time
 
 struct RouteArgs {
     const uint16_t* x;
@@ -31,95 +34,113 @@ struct RouteArgs {
     uint64_t* logits;       // fp64 bits [M][E]
 };
 
-__device__ __forceinline__ double wave_sum(double v) {
-    for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
+// v combined over the wave by row shifts, whole in lane 63 (lanes without a source take `none`)
+template <class Op>
+__device__ __forceinline__ double wave_join(double v, double none, Op op) {
+    auto step = [&](auto ctrl, auto rows) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v), n = __builtin_bit_cast(uint64_t, none);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)n, (int)(uint32_t)b, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(n >> 32), (int)(b >> 32), decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+        v = op(v, __builtin_bit_cast(double, (uint64_t)hi << 32 | lo));
+    };
+    using std::integral_constant;
+    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});      // row_shr 1, 2, 4, 8
+    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});      // lane 15 of a row to the next row
+    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});      // lane 31 to the upper half
     return v;
 }
+__device__ __forceinline__ double from_lane(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    return from_lane(wave_join(v, 0.0, [](double a, double b) { return a + b; }), 63);
+}
 __device__ __forceinline__ double wave_max(double v) {
-    for (int s = 32; s > 0; s >>= 1) v = fmax(v, __shfl_xor(v, s));
-    return v;
+    return from_lane(wave_join(v, -INFINITY, [](double a, double b) { return fmax(a, b); }), 63);
 }
 
 template <bool kBF16>
-__device__ __forceinline__ double dot8(const uint4& a, const uint4& b, double acc) {
+__device__ __forceinline__ void dot8(const uint4& a, const uint4& b, double (&acc)[2]) {
     const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        acc += (double)(half_bits_to_f32<kBF16>(aw[i] & 0xFFFFu) * half_bits_to_f32<kBF16>(bw[i] & 0xFFFFu));
-        acc += (double)(half_bits_to_f32<kBF16>(aw[i] >> 16) * half_bits_to_f32<kBF16>(bw[i] >> 16));
+        acc[0] += (double)(half_bits_to_f32<kBF16>(aw[i] & 0xFFFFu) * half_bits_to_f32<kBF16>(bw[i] & 0xFFFFu));
+        acc[1] += (double)(half_bits_to_f32<kBF16>(aw[i] >> 16) * half_bits_to_f32<kBF16>(bw[i] >> 16));
     }
-    return acc;
 }
 
-// one row by one wave
+// one row by one wave, N experts a lane
+template <int N>
 __device__ __forceinline__ void choose(const RouteArgs& a, int m) {
     const int lane = (int)threadIdx.x & 63;
-    double l[kMaxPerLane], by[kMaxPerLane];
+    double l[N];
     double top = -INFINITY;
-    const int n = (a.E - lane + 63) / 64;                // experts lane, lane + 64, ...
 #pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i) {
-        l[i] = by[i] = -INFINITY;
-        if (i < n) {
-            const uint64_t* p = a.logits + (size_t)m * a.E + lane + 64 * i;
-            l[i] = __builtin_bit_cast(double, __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-            top = fmax(top, l[i]);
-        }
+    for (int i = 0; i < N; ++i) {
+        const int e = lane + 64 * i;
+        const uint64_t* p = a.logits + (size_t)m * a.E + (e < a.E ? e : 0);
+        l[i] = __builtin_bit_cast(double, __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (lane + 64 * i >= a.E) l[i] = -INFINITY;
+        top = fmax(top, l[i]);
     }
     top = wave_max(top);
-    double sum = 0.0;
-    if (!a.sigmoid) {
+    // scores; softmax's are divided by their sum at the end, unless it leaves with `normalize`
+    double s[N], sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < kMaxPerLane; ++i)
-            if (i < n) sum += exp(l[i] - top);
-        sum = wave_sum(sum);
+    for (int i = 0; i < N; ++i) {
+        s[i] = a.sigmoid ? 1.0 / (1.0 + exp(-l[i])) : exp(l[i] - top);
+        sum += lane + 64 * i < a.E ? s[i] : 0.0;
     }
-    auto score = [&](double v) { return a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - top) / sum; };
+    sum = a.sigmoid ? 1.0 : wave_sum(sum);
+    // what the choice goes by: -infinity for no number, no number for what is taken or not there
+    double by[N];
 #pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i)
-        if (i < n) {
-            by[i] = a.bias ? score(l[i]) + (double)a.bias[lane + 64 * i] : l[i];
-            if (!(by[i] > -INFINITY)) by[i] = -INFINITY;  // no number: behind all others
-        }
-    uint32_t taken = 0;
-    double mine = 0.0, total = 0.0;                       // lane j keeps the j-th weight
+    for (int i = 0; i < N; ++i) {
+        const int e = lane + 64 * i;
+        by[i] = a.bias ? s[i] / sum + (double)a.bias[e < a.E ? e : 0] : l[i];
+        if (!(by[i] > -INFINITY)) by[i] = -INFINITY;
+        if (e >= a.E) by[i] = NAN;
+    }
+    double mine = 0.0, total = 0.0;                       // lane j keeps the j-th
     int my_id = 0;
     for (int j = 0; j < a.T; ++j) {
-        // (value, expert) of the lane's best that is left; ties to the lowest expert
-        double v = 0.0, lv = 0.0;
-        int e = 0x7FFFFFFF;
+        double best = by[0];
 #pragma unroll
-        for (int i = 0; i < kMaxPerLane; ++i)
-            if (i < n && !((taken >> i) & 1u) && (e == 0x7FFFFFFF || by[i] > v)) {
-                v = by[i];
-                lv = l[i];
-                e = lane + 64 * i;
+        for (int i = 1; i < N; ++i) best = fmax(best, by[i]);
+        best = from_lane(wave_join(best, NAN, [](double x, double y) { return fmax(x, y); }), 63);
+        // the lowest expert that has it
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint64_t has = __ballot(by[i] == best);
+            if (found || has == 0) continue;
+            found = true;
+            const int owner = __builtin_ctzll(has);
+            const double w = from_lane(s[i], owner);
+            total += w;
+            if (lane == owner) by[i] = NAN;
+            if (lane == j) {
+                mine = w;
+                my_id = owner + 64 * i;
             }
-        for (int s = 32; s > 0; s >>= 1) {
-            const double v2 = __shfl_xor(v, s), l2 = __shfl_xor(lv, s);
-            const int e2 = __shfl_xor(e, s);
-            if (e2 != 0x7FFFFFFF && (e == 0x7FFFFFFF || v2 > v || (v2 == v && e2 < e))) {
-                v = v2;
-                lv = l2;
-                e = e2;
-            }
-        }
-        if ((e & 63) == lane) taken |= 1u << (e >> 6);
-        const double w = score(lv);
-        total += w;
-        if (lane == j) {
-            mine = w;
-            my_id = e;
         }
     }
     if (lane < a.T) {
-        const double w = a.normalize ? (total == 0.0 ? 0.0 : mine / total) : mine;
+        const double w = a.normalize ? (total == 0.0 ? 0.0 : mine / total) : mine / sum;
         a.ids[(size_t)m * a.T + lane] = my_id;
         a.weights[(size_t)m * a.T + lane] = (float)(w * (double)a.scale);
     }
 }
 
-template <bool kBF16>
+template <bool kBF16, int N>
 __global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a) {
     __shared__ int last;
     const int tid = (int)threadIdx.x, w = tid >> 6, lane = tid & 63;
@@ -127,15 +148,24 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a) {
     const int g = (int)blockIdx.x / tiles, e = (int)blockIdx.x % tiles * kWaves + w;
     const int m0 = g * a.group, m1 = m0 + a.group < a.M ? m0 + a.group : a.M;
     if (e < a.E) {
-        const uint16_t* r = a.router + (size_t)e * a.K;
+        const uint4* r = reinterpret_cast<const uint4*>(a.router + (size_t)e * a.K);
+        const int pieces = a.K / 8;
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        uint4 rw[kPieces];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) rw[p] = lane + 64 * p < pieces ? r[lane + 64 * p] : none;
         for (int m = m0; m < m1; ++m) {
-            const uint16_t* x = a.x + (size_t)m * a.K;
-            double acc = 0.0;
-            for (int k = 8 * lane; k < a.K; k += 512)
-                acc = dot8<kBF16>(*reinterpret_cast<const uint4*>(x + k), *reinterpret_cast<const uint4*>(r + k), acc);
-            acc = wave_sum(acc);
-            if (lane == 0)
-                __hip_atomic_store(a.logits + (size_t)m * a.E + e, __builtin_bit_cast(uint64_t, acc), __ATOMIC_RELAXED,
+            const uint4* x = reinterpret_cast<const uint4*>(a.x + (size_t)m * a.K);
+            double acc[2] = {0.0, 0.0};
+            uint4 xw[kPieces];
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) xw[p] = lane + 64 * p < pieces ? x[lane + 64 * p] : none;
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) dot8<kBF16>(xw[p], rw[p], acc);
+            for (int q = lane + 64 * kPieces; q < pieces; q += 64) dot8<kBF16>(x[q], r[q], acc);
+            const double sum = wave_join(acc[0] + acc[1], 0.0, [](double u, double v) { return u + v; });
+            if (lane == 63)
+                __hip_atomic_store(a.logits + (size_t)m * a.E + e, __builtin_bit_cast(uint64_t, sum), __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
         }
     }
@@ -145,8 +175,17 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a) {
         last = __hip_atomic_fetch_add(&a.counters[g], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(tiles - 1);
     __syncthreads();
     if (!last) return;
-    for (int m = m0 + w; m < m1; m += kWaves) choose(a, m);
+    for (int m = m0 + w; m < m1; m += kWaves) choose<N>(a, m);
     if (tid == 0) __hip_atomic_store(&a.counters[g], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <bool kBF16>
+void launch_typed(const RouteArgs& a, int grid, hipStream_t s) {
+    const int n = (a.E + 63) / 64;
+    if (n == 1) hipLaunchKernelGGL((route_kernel<kBF16, 1>), dim3(grid), dim3(kThreads), 0, s, a);
+    else if (n == 2) hipLaunchKernelGGL((route_kernel<kBF16, 2>), dim3(grid), dim3(kThreads), 0, s, a);
+    else if (n <= 4) hipLaunchKernelGGL((route_kernel<kBF16, 4>), dim3(grid), dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((route_kernel<kBF16, kMaxExperts / 64>), dim3(grid), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
@@ -172,8 +211,8 @@ hipError_t launch_route(const RouteCall& q, hipStream_t stream) {
     // one counter per group of rows
     a.group = (int)((q.M + kMaxSplitTiles - 1) / kMaxSplitTiles);
     const int groups = (a.M + a.group - 1) / a.group, tiles = (a.E + kWaves - 1) / kWaves;
-    if (q.bf16) hipLaunchKernelGGL((route_kernel<true>), dim3(groups * tiles), dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((route_kernel<false>), dim3(groups * tiles), dim3(kThreads), 0, stream, a);
+    if (q.bf16) launch_typed<true>(a, groups * tiles, stream);
+    else launch_typed<false>(a, groups * tiles, stream);
     return hipGetLastError();
 }
 
