@@ -114,7 +114,7 @@ typedef struct {
  *   logits  [M, V], `type`, row m at logits + m * row_stride elements (row_stride >= V), aligned
  *           to its element; read only. Rows on 16-byte boundaries are read faster.
  * 1 <= V <= 2^28. Weights and their sums are in fp64; top_p's sums in 64-bit fixed point, a
- * step of 2^-62 V (V rounded up to a power of two) of the largest weight. */
+ * step of 2^-62 V (V rounded up to a power of two; at least 2^-51) of the largest weight. */
 size_t w4a16_sample_workspace_bytes(int64_t M, int64_t V);
 w4a16_status w4a16_sample(const void* logits, w4a16_logits type, int64_t row_stride, const float* u, int64_t M, int64_t V,
                           const w4a16_sampling* how, int32_t* ids, float* logprob, void* workspace,
