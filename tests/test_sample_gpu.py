@@ -52,6 +52,15 @@ def test_sample(w, M, V, dtype):
         check(w, z, u, **s)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M", [64, 65, 130])
+def test_few_rows_and_many(w, M, dtype):
+    """Rows that take several workgroups each, and rows that take one."""
+    z, u = make(M, M, 17001, dtype, spread=1.0)
+    for s in SETTINGS:
+        check(w, z, u, **s)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("pad", [1, 5, 8])
 def test_rows_with_a_stride(w, pad, dtype):

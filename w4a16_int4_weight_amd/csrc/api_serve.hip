@@ -273,9 +273,9 @@ w4a16_status w4a16_moe_layer(const void* x, const void* router, const float* bia
 }
 
 size_t w4a16_sample_workspace_bytes(int64_t M, int64_t V) {
-    (void)M;
-    (void)V;
-    return 0;
+    if (M <= 0 || M >= kMaxRows || V < 1 || V > kMaxVocabulary) return 0;
+    const size_t need = w4a16::sample_workspace(M, V);
+    return need ? w4a16::kSplitCounterBytes + need : 0;
 }
 
 w4a16_status w4a16_sample(const void* logits, w4a16_logits type, int64_t row_stride, const float* u, int64_t M, int64_t V,
@@ -311,7 +311,8 @@ w4a16_status w4a16_sample(const void* logits, w4a16_logits type, int64_t row_str
     q.min_ps = how->min_ps;
     q.ids = ids;
     q.logprob = logprob;
-    return from_hip(w4a16::launch_sample(q, static_cast<hipStream_t>(stream)));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    return from_hip(w4a16::launch_sample(q, ws ? ws + w4a16::kSplitCounterBytes : nullptr, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -283,6 +283,8 @@ struct SampleCall {
     int32_t* ids;
     float* logprob;             // or NULL
 };
-hipError_t launch_sample(const SampleCall& call, hipStream_t stream);
+// scratch of sample_workspace bytes (NULL where that is 0), nothing in it kept between calls
+size_t sample_workspace(int64_t M, int64_t V);
+hipError_t launch_sample(const SampleCall& call, void* scratch, hipStream_t stream);
 
 }  // namespace w4a16

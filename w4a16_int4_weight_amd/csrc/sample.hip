@@ -4,21 +4,24 @@
 //   that reaches p of their weight, of these w >= min_p;  the token: the first v in rising
 //   order whose running sum of kept w exceeds u times the whole.
 //
-// One workgroup a row; wave i takes the i-th contiguous piece, so that sums of waves are sums in
-// index order. The row is met two or three times, from the L2 after the first:
-//   - its largest, and every thread's;
-//   - top-k up to 1024: the k-th largest of the threads' largest bounds the k-th of all from
-//     below; the few logits from it on are put into a list in LDS, in index order, and all the
-//     rest happens there. A random row of 131072 and k = 50 lists 51.
-//   - top-p alone: the sum of all w, and w by sixteenths of an octave below the largest; the
-//     logits down to the one where p is reached go into the list.
-//   - neither: sums of w, then of the sixteenth, and so on, in which the token lies.
-// Where a list would overflow, thresholds are found over the row itself, digit by digit.
+// A row is cut into 16 contiguous pieces, so that sums of pieces are sums in index order. It is met
+// two to four times, from the caches after the first:
+//   1. the largest logit, and the largest of 256 groups;
+//   2. top-k up to 192: the k-th largest of the groups' bounds the k-th of all from below, and the
+//      few logits from it on are put into a list, in index order; all the rest happens there (a
+//      random row of 131072 and k = 50 lists 56). Otherwise: the sums of w, and with top-p w by
+//      eighths of an octave below the largest;
+//   3. top-p alone: the logits of the eighth in which p is reached are listed, those above it summed;
+//   4. the draw: the piece whose sum of kept w holds the target, its sixteenth, and so on.
+// A few rows take 16 workgroups each, in a launch for each of these; many rows one workgroup each,
+// a wave a piece, in one launch. What the lists do not hold (top-k over 1024, lists of more than 512
+// in a piece) is found over the row itself.
 //
-// Logits are compared as whole numbers (order-preserving keys), thresholds found digit by digit
-// from the top: counts for k, sums of weights in 64-bit fixed point for p (whole numbers, so that
-// the order of the additions changes nothing). Ties at a threshold go to the lowest index. w and
-// the sums of the draw are in fp64: next to a border 32 bits would give another token.
+// Logits are compared as whole numbers (order-preserving keys). Lists of up to 256 are sorted by
+// counting, an entry a thread; in longer ones and over the row thresholds are found digit by digit
+// from the top: counts for k, sums of weights in 64-bit fixed point for p (whole numbers, so that the
+// order of the additions changes nothing). Ties at a threshold go to the lowest index. w and the sums
+// of the draw are in fp64: next to a border 32 bits would give another token.
 #include "device_common.h"
 #include "launch.h"
 
@@ -27,11 +30,28 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
+constexpr int kPieces = kWaves;
+constexpr int kPieceThreads = 256;              // of a workgroup that takes one piece
 constexpr int kVec = 8;                         // consecutive logits of a lane
 constexpr int kStep = 64 * kVec;                // of a wave
-constexpr int kRoom = 512;                      // listed logits of a wave
-constexpr int kOctaves = 16;                    // below the largest, 16 bins each
+constexpr int kRoom = 512;                      // listed logits of a piece
+constexpr int kShort = 256;                     // and of all in a short list
+constexpr int kGroups = 256;
+constexpr int kBins = 256, kBinsPerOctave = 8;  // below the largest
 constexpr int kNone = 0x7FFFFFFF;
+
+// what the launches for few rows leave to each other
+struct Left {
+    float group_max[kGroups];
+    double sum[kPieces];                        // of all w (top-p) or of those that min-p keeps
+    double above[kPieces];                      // top-p: of w above the list, and of those that min-p keeps
+    double above_kept[kPieces];
+    int listed[kPieces];
+    int pad[16];
+    unsigned long long mass[kPieces][kBins];
+    uint32_t key[kPieces][kRoom];
+    int index[kPieces][kRoom];
+};
 
 struct SampleArgs {
     const void* logits;
@@ -48,6 +68,28 @@ struct SampleArgs {
     int32_t* ids;
     float* logprob;
     int aligned;            // rows on 16-byte boundaries
+    Left* left;             // [M], or NULL: one workgroup a row
+};
+
+// a row's settings
+struct How {
+    float t;
+    bool greedy, limit_k, limit_p, by_groups, by_bins;
+    int k;
+    double p, min_w;
+    __device__ __forceinline__ How(const SampleArgs& a, int m) {
+        t = a.temperatures ? a.temperatures[m] : a.temperature;
+        greedy = !(t > 0.f);
+        k = greedy ? 1 : a.top_ks ? a.top_ks[m] : a.top_k;
+        limit_k = k >= 1 && k < a.V;
+        const float pf = a.top_ps ? a.top_ps[m] : a.top_p;
+        limit_p = pf < 1.f;
+        p = (double)fmaxf(pf, 0.f);
+        const float mf = a.min_ps ? a.min_ps[m] : a.min_p;
+        min_w = mf > 0.f ? (double)fminf(mf, 1.f) : 0.0;
+        by_groups = limit_k && k <= kGroups * 3 / 4;
+        by_bins = limit_p && !limit_k;
+    }
 };
 
 // kKind: 0 fp16, 1 bf16, 2 fp32. Values of the type take the top kBits of an fp32 key.
@@ -69,18 +111,21 @@ template <int kKind> struct Logit {
                 r.q[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
             }
         } else {
-            uint32_t w[kKind == 2 ? 8 : 4];
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
+            // (rolled: it is in every loop over the row, and rarely taken)
+            r.q[0] = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (kKind == 2) r.q[1] = r.q[0];
+#pragma unroll 1
+            for (int e = kVec - 1; e >= 0; --e) {
                 if constexpr (kKind == 2) {
-                    w[e] = i + e < V ? static_cast<const uint32_t*>(row)[i + e] : 0xFF800000u;
+                    const uint32_t v = i + e < V ? static_cast<const uint32_t*>(row)[i + e] : 0xFF800000u;
+                    r.q[1] = make_uint4(r.q[0].w, r.q[1].x, r.q[1].y, r.q[1].z);
+                    r.q[0] = make_uint4(v, r.q[0].x, r.q[0].y, r.q[0].z);
                 } else {
                     const uint32_t v = i + e < V ? static_cast<const uint16_t*>(row)[i + e] : kKind == 1 ? 0xFF80u : 0xFC00u;
-                    w[e / 2] = e & 1 ? w[e / 2] | v << 16 : v;
+                    uint4& q = r.q[0];
+                    q = make_uint4(q.x << 16 | v, q.y << 16 | q.x >> 16, q.z << 16 | q.y >> 16, q.w << 16 | q.z >> 16);
                 }
             }
-            r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            if constexpr (kKind == 2) r.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
         return r;
     }
@@ -96,6 +141,16 @@ template <int kKind> struct Logit {
         }
         return fmaxf(z, -INFINITY);
     }
+    // the seven behind the first move up
+    static __device__ __forceinline__ void next(Eight& r) {
+        if constexpr (kKind == 2) {
+            r.q[0] = make_uint4(r.q[0].y, r.q[0].z, r.q[0].w, r.q[1].x);
+            r.q[1] = make_uint4(r.q[1].y, r.q[1].z, r.q[1].w, 0u);
+        } else {
+            uint4& q = r.q[0];
+            q = make_uint4(q.x >> 16 | q.y << 16, q.y >> 16 | q.z << 16, q.z >> 16 | q.w << 16, q.w >> 16);
+        }
+    }
     // rises with z; either zero is the same
     static __device__ __forceinline__ uint32_t key(float z) {
         const uint32_t b = __float_as_uint(z + 0.f);
@@ -107,41 +162,47 @@ template <int kKind> struct Logit {
     }
 };
 
-// w of a logit in fp64: 2^x, x = (z - top) log2(e) / t, by Tang's scheme: x = n / 64 + f, 2^(n mod 64 / 64)
-// from a table, 2^f by its series to the fifth power (|f| <= 1/128: 4e-17 left out).
+// w of a logit in fp64: 2^x, x = (z - top) log2(e) / t = n + f, 2^f by its series to the twelfth
+// power (|f| <= 1/2: 2e-16 left out). (A table of 64 powers and a series to the fifth: 1.4 times the
+// time, in bank conflicts.)
 struct Weight {
     double top, per;        // log2(e) / t
-    const double* table;
     bool endless;           // the largest is +infinity: it alone weighs
+    __device__ __forceinline__ Weight(float largest, float t)
+        : top((double)largest), per(1.4426950408889634 / (double)t), endless(largest == INFINITY) {}
     __device__ __forceinline__ double octaves(float z) const { return fmax(((double)z - top) * per, -1100.0); }
     __device__ __forceinline__ double power(double x) const {
-        const double shifted = x * 64.0 + 6755399441055744.0;      // 1.5 * 2^52: its low bits are the nearest n
-        const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, shifted);
-        const double f = fma(shifted - 6755399441055744.0, -1.0 / 64.0, x);
-        double p = 1.3333558146428443e-3;                          // ln2^5 / 5!, ln2^4 / 4!, ...
+        const double n = rint(x), f = x - n;
+        double p = 2.5678435993488202e-11;                         // ln2^12 / 12!, ln2^11 / 11!, ...
+        p = fma(p, f, 4.4455382718708115e-10);
+        p = fma(p, f, 7.0549116208011234e-9);
+        p = fma(p, f, 1.0178086009239699e-7);
+        p = fma(p, f, 1.3215486790144307e-6);
+        p = fma(p, f, 1.5252733804059841e-5);
+        p = fma(p, f, 1.5403530393381608e-4);
+        p = fma(p, f, 1.3333558146428443e-3);
         p = fma(p, f, 9.618129107628477e-3);
         p = fma(p, f, 5.550410866482158e-2);
         p = fma(p, f, 0.2402265069591007);
         p = fma(p, f, 0.6931471805599453);
-        const double s = table[n & 63];
-        return ldexp(fma(s, p * f, s), n >> 6);
+        return ldexp(fma(p, f, 1.0), (int)n);
     }
     __device__ __forceinline__ double operator()(float z) const {
         return endless ? ((double)z == top ? 1.0 : 0.0) : power(octaves(z));
     }
 };
 
-struct Shared {
-    uint32_t count[256];
-    unsigned long long mass[256];
-    double table[64];
-    double part[kWaves], found_w;
-    int listed[kWaves];
-    int box[2];
-    uint64_t above;
-    uint32_t key[kWaves][kRoom];
-    int index[kWaves][kRoom];
-};
+// Weights in whole steps (unit <= 2^51: the sum's low 52 bits are the nearest whole number), and
+// their bins below the largest.
+__device__ __forceinline__ uint64_t fixed_point(double w, double unit) {
+    return __builtin_bit_cast(uint64_t, fma(w, unit, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
+}
+__device__ __forceinline__ int bin_of(double x) { return (int)(x * -(double)kBinsPerOctave); }
+// a bound a little below (by = 1e-6) or above (by = -1e-6) a bin's lower end
+__device__ __forceinline__ float bin_end(const Weight& w, int bin, double by) {
+    const double low = w.top - (double)(bin + 1) / kBinsPerOctave / w.per * (1.0 + by);
+    return (float)(low - by * (fabs(low) + 1e-3 * fabs(w.top)));
+}
 
 __device__ __forceinline__ double wave_sum(double v) {
     for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
@@ -158,6 +219,106 @@ __device__ __forceinline__ T wave_before(T v, T* all) {            // sum of the
     *all = __shfl(sum, 63);
     const T up = __shfl_up(sum, 1);
     return lane ? up : T(0);
+}
+
+template <int kKind> struct Row {
+    using L = Logit<kKind>;
+    using Eight = typename L::Eight;
+    const void* p;
+    int V, lane;
+    bool aligned;
+    __device__ __forceinline__ Row(const SampleArgs& a, int m) {
+        p = static_cast<const uint8_t*>(a.logits) + (int64_t)m * a.ld * (kKind == 2 ? 4 : 2);
+        V = a.V;
+        lane = (int)threadIdx.x & 63;
+        aligned = a.aligned != 0;
+    }
+    // logits of a piece, and of the part of it that one of `parts` waves takes
+    __device__ __forceinline__ int piece() const { return (int)(((int64_t)V + kPieces * kStep - 1) / (kPieces * kStep)) * kStep; }
+    __device__ __forceinline__ int start(int64_t i) const { return i < V ? (int)i : V; }
+    // f(logits, index of the first) for each eight of [i0, i1) that this wave's lane has, in rising order
+    template <int kAhead, class F>
+    __device__ __forceinline__ void walk(int i0, int i1, F f) const {
+        for (int i = i0 + kVec * lane; i - kVec * lane < i1; i += kAhead * kStep) {
+            Eight r[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) r[j] = L::load(p, i + j * kStep, i1, aligned);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) f(r[j], i + j * kStep);
+        }
+    }
+    // the same for a costly f, in less code
+    template <class F>
+    __device__ __forceinline__ void stroll(int i0, int i1, F f) const {
+        for (int i = i0 + kVec * lane; i - kVec * lane < i1; i += 4 * kStep) {
+            Eight r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = L::load(p, i + j * kStep, i1, aligned);
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                f(r[0], i + j * kStep);
+                r[0] = r[1];
+                r[1] = r[2];
+                r[2] = r[3];
+            }
+        }
+    }
+    // Entries of [i0, i1) from `low` up to below `high` (no number: all), in index order, from place n on; returns the
+    // place behind the last (entries past `room` are only counted).
+    __device__ __forceinline__ int gather(int i0, int i1, float low, float high, uint32_t* key, int* index, int room, int n) const {
+        constexpr int kAhead = kKind == 2 ? 2 : 4;
+        walk<kAhead>(i0, i1, [&](const Eight& r, int i) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) most = fmaxf(most, L::at(r, e));
+            if (__ballot(most >= low) == 0) return;
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) hits |= L::at(r, e) >= low && !(L::at(r, e) >= high) && i + e < i1 ? 1u << e : 0u;
+            int all;
+            int at = n + wave_before((int)__popc(hits), &all);
+#pragma unroll 1
+            for (Eight q = r; hits; hits >>= 1) {
+                if ((hits & 1u) && at < room) {
+                    key[at] = L::key(L::at(q, 0));
+                    index[at] = i;
+                }
+                at += (int)(hits & 1u);
+                ++i;
+                L::next(q);
+            }
+            n += all;
+        });
+        return n;
+    }
+};
+
+struct Shared {
+    uint32_t count[256];
+    unsigned long long mass[kBins];
+    double part[kPieces], above[kPieces], above_kept[kPieces];
+    double sorted[kShort];
+    int entry[kShort];      // of each rank
+    int listed[kPieces];
+    int box[2];
+    uint64_t above_cut;
+    uint4 short_key[kShort / 4];
+    int short_index[kShort];
+    uint32_t key[kPieces][kRoom];
+    int index[kPieces][kRoom];
+};
+
+// how many of the first n short keys come before the i-th: larger, or equal and earlier
+__device__ __forceinline__ int rank_of(const uint4* keys, int n, int i) {
+    const uint32_t key = reinterpret_cast<const uint32_t*>(keys)[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 4) {
+        const uint4 q = keys[j / 4];
+        rank += (j < n && (q.x > key || (q.x == key && j < i))) + (j + 1 < n && (q.y > key || (q.y == key && j + 1 < i))) +
+                (j + 2 < n && (q.z > key || (q.z == key && j + 2 < i))) + (j + 3 < n && (q.w > key || (q.w == key && j + 3 < i)));
+    }
+    return rank;
 }
 
 // The key of the left-th largest of what each(f) gives f, and how many of its equals are among
@@ -237,66 +398,241 @@ __device__ __forceinline__ void find_mass(Shared& sh, Each each, double target, 
                 while (b > some && (sh.count[b] == 0 || (double)(sum + sh.mass[b]) < target)) sum += sh.mass[b--];
                 sh.box[0] = b;
                 sh.box[1] = (int)sh.count[b];
-                sh.above = sum;
+                sh.above_cut = sum;
             }
         }
         __syncthreads();
         prefix = prefix << width | (uint32_t)sh.box[0];
-        above = sh.above;
+        above = sh.above_cut;
     }
     *cut = prefix;
     *above_cut = above;
     *there = sh.box[1];
 }
 
+// The bins, the likeliest first, in which the weights reach p of the whole: with sums of fixed-point
+// steps, up to what the whole's rounding may be off on either side. bins[0]: the first that may be it, [1]: the last;
+// [1] is -1 where the bins do not reach it. For the first wave; mass is in LDS.
+__device__ __forceinline__ void find_bins(const unsigned long long* mass, double want, int* bins) {
+    const int lane = (int)threadIdx.x & 63;
+    uint64_t own = 0, all;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) own += mass[4 * lane + j];
+    const uint64_t above = wave_before((uint64_t)own, &all);
+    if (lane == 0) bins[0] = bins[1] = -1;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const double at = fmax(side ? want * (1.0 + 1e-9) : want * (1.0 - 1e-9), 1.0);
+        if ((double)above < at && (double)(above + own) >= at) {
+            uint64_t sum = above;
+            int b = 4 * lane;
+            while ((double)(sum + mass[b]) < at) sum += mass[b++];
+            bins[side] = b;
+        }
+    }
+}
+
+// ---- few rows: a workgroup of 4 waves a piece
+
 template <int kKind>
+__global__ __launch_bounds__(kPieceThreads) void piece_max_kernel(const SampleArgs a) {
+    const int m = (int)blockIdx.x / kPieces, c = (int)blockIdx.x % kPieces, w = (int)threadIdx.x >> 6;
+    const Row<kKind> row(a, m);
+    const int part = (row.piece() + 4 * kStep - 1) / (4 * kStep) * kStep;
+    const int64_t base = (int64_t)c * row.piece();
+    const int end = row.start(base + row.piece()), i0 = row.start(base + (int64_t)w * part);
+    const int from = i0 < end ? i0 : end, to = end - from < part ? end : from + part;
+    float most = -INFINITY;
+    row.template walk<kKind == 2 ? 2 : 4>(from, to, [&](const auto& r, int) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) most = fmaxf(most, Logit<kKind>::at(r, e));
+    });
+    for (int s = 8; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor(most, s));
+    if ((threadIdx.x & 15) == 0) a.left[m].group_max[c * (kGroups / kPieces) + ((int)threadIdx.x >> 4)] = most;
+}
+
+// The largest of the groups, by 256 threads; the groups' keys are left in LDS.
+template <int kKind>
+__device__ __forceinline__ float top_of(const Left& left, uint4* keys, float* wave_top) {
+    const int tid = (int)threadIdx.x;
+    const float own = left.group_max[tid];
+    reinterpret_cast<uint32_t*>(keys)[tid] = Logit<kKind>::key(own);
+    float top = own;
+    for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+    if ((tid & 63) == 0) wave_top[tid >> 6] = top;
+    __syncthreads();
+    return fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+}
+
+// Each wave's list of a piece to its place behind those of the waves before it.
+struct PieceList {
+    uint32_t key[4][kRoom];
+    int index[4][kRoom];
+    int n[4];
+};
+__device__ __forceinline__ void leave_list(PieceList& l, Left& left, int c) {
+    const int w = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+    __syncthreads();
+    int first = 0;
+    for (int k = 0; k < w; ++k) first += l.n[k];
+    for (int j = lane; j < l.n[w] && first + j < kRoom; j += 64) {
+        left.key[c][first + j] = l.key[w][j];
+        left.index[c][first + j] = l.index[w][j];
+    }
+    if (threadIdx.x == kPieceThreads - 1) left.listed[c] = first + l.n[w];
+}
+
+template <int kKind>
+__global__ __launch_bounds__(kPieceThreads) void piece_sum_kernel(const SampleArgs a) {
+    __shared__ uint4 keys[kGroups / 4];
+    __shared__ float wave_top[4];
+    __shared__ double wave_part[4];
+    __shared__ unsigned long long mass[kBins];
+    __shared__ uint32_t bound;
+    __shared__ PieceList list;
+    using L = Logit<kKind>;
+    const int m = (int)blockIdx.x / kPieces, c = (int)blockIdx.x % kPieces, tid = (int)threadIdx.x, w = tid >> 6, lane = tid & 63;
+    const How how(a, m);
+    const float top = top_of<kKind>(a.left[m], keys, wave_top);
+    // (all, or left to the last launch)
+    if (how.greedy || !(top > -INFINITY) || top == INFINITY || (how.limit_k && !how.by_groups)) return;
+    const Row<kKind> row(a, m);
+    const int part = (row.piece() + 4 * kStep - 1) / (4 * kStep) * kStep;
+    const int64_t base = (int64_t)c * row.piece();
+    const int end = row.start(base + row.piece()), i0 = row.start(base + (int64_t)w * part);
+    const int from = i0 < end ? i0 : end, to = end - from < part ? end : from + part;
+    if (how.by_groups) {
+        if (rank_of(keys, kGroups, tid) == how.k - 1) bound = reinterpret_cast<uint32_t*>(keys)[tid];
+        __syncthreads();
+        const int n = row.gather(from, to, L::value(bound), NAN, list.key[w], list.index[w], kRoom, 0);
+        if (lane == 0) list.n[w] = n;
+        leave_list(list, a.left[m], c);
+        return;
+    }
+    const Weight weight(top, how.t);
+    const double unit = (double)(1ull << a.unit_shift);
+    mass[tid] = 0ull;
+    __syncthreads();
+    double sum = 0.0;
+    row.stroll(from, to, [&](const auto& r, int) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const double x = weight.octaves(L::at(r, e)), v = weight.power(x);
+            if (how.by_bins) {
+                sum += v;
+                if (x > -(double)(kBins / kBinsPerOctave)) atomicAdd(&mass[bin_of(x)], (unsigned long long)fixed_point(v, unit));
+            } else {
+                sum += v >= how.min_w ? v : 0.0;
+            }
+        }
+    });
+    sum = wave_sum(sum);
+    if (lane == 0) wave_part[w] = sum;
+    __syncthreads();
+    if (tid == 0) a.left[m].sum[c] = wave_part[0] + wave_part[1] + wave_part[2] + wave_part[3];
+    if (how.by_bins) a.left[m].mass[c][tid] = mass[tid];
+}
+
+template <int kKind>
+__global__ __launch_bounds__(kPieceThreads) void piece_cut_kernel(const SampleArgs a) {
+    __shared__ uint4 keys[kGroups / 4];
+    __shared__ float wave_top[4];
+    __shared__ double wave_part[4][2];
+    __shared__ unsigned long long mass[kBins];
+    __shared__ int bins[2];
+    __shared__ PieceList list;
+    using L = Logit<kKind>;
+    const int m = (int)blockIdx.x / kPieces, c = (int)blockIdx.x % kPieces, tid = (int)threadIdx.x, w = tid >> 6, lane = tid & 63;
+    const How how(a, m);
+    if (how.greedy || !how.by_bins) return;
+    Left& left = a.left[m];
+    uint64_t own = 0;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) own += left.mass[k][tid];
+    double whole = 0.0;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) whole += left.sum[k];
+    const float top = top_of<kKind>(left, keys, wave_top);
+    if (!(top > -INFINITY) || top == INFINITY) return;
+    mass[tid] = own;
+    __syncthreads();
+    const double unit = (double)(1ull << a.unit_shift);
+    if (w == 0) find_bins(mass, how.p * whole * unit, bins);
+    __syncthreads();
+    if (bins[0] < 0 || bins[1] < 0) {
+        if (tid == 0) left.listed[c] = kRoom + 1;              // over the row itself
+        return;
+    }
+    const Row<kKind> row(a, m);
+    const Weight weight(top, how.t);
+    const int part = (row.piece() + 4 * kStep - 1) / (4 * kStep) * kStep;
+    const int64_t base = (int64_t)c * row.piece();
+    const int end = row.start(base + row.piece()), i0 = row.start(base + (int64_t)w * part);
+    const int from = i0 < end ? i0 : end, to = end - from < part ? end : from + part;
+    // what may be cut, and what surely is not
+    const float low = bin_end(weight, bins[1], 1e-6), high = bins[0] > 0 ? bin_end(weight, bins[0] - 1, -1e-6) : INFINITY;
+    const int n = row.gather(from, to, low, high, list.key[w], list.index[w], kRoom, 0);
+    if (lane == 0) list.n[w] = n;
+    double above = 0.0, above_kept = 0.0;
+    row.stroll(from, to, [&](const auto& r, int) {
+        float most = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) most = fmaxf(most, L::at(r, e));
+        if (__ballot(most >= high) == 0) return;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const double v = L::at(r, e) >= high ? weight(L::at(r, e)) : 0.0;
+            above += v;
+            above_kept += v >= how.min_w ? v : 0.0;
+        }
+    });
+    above = wave_sum(above);
+    above_kept = wave_sum(above_kept);
+    if (lane == 0) {
+        wave_part[w][0] = above;
+        wave_part[w][1] = above_kept;
+    }
+    leave_list(list, left, c);
+    if (tid == 0) {
+        left.above[c] = wave_part[0][0] + wave_part[1][0] + wave_part[2][0] + wave_part[3][0];
+        left.above_kept[c] = wave_part[0][1] + wave_part[1][1] + wave_part[2][1] + wave_part[3][1];
+    }
+}
+
+// ---- the row's token: by one workgroup, from its logits alone or (kLeft) with what the launches above left
+
+template <int kKind, bool kLeft>
 __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     using L = Logit<kKind>;
     using Eight = typename L::Eight;
-    constexpr int kAhead = kKind == 2 ? 2 : 4;                     // pieces of a lane loaded at a time
     __shared__ Shared sh;
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int m = (int)blockIdx.x, V = a.V;
-    const void* row = static_cast<const uint8_t*>(a.logits) + (int64_t)m * a.ld * (kKind == 2 ? 4 : 2);
-    const bool aligned = a.aligned != 0;
-    const float t = a.temperatures ? a.temperatures[m] : a.temperature;
-    const bool greedy = !(t > 0.f);
-    const int kk = greedy ? 1 : a.top_ks ? a.top_ks[m] : a.top_k;
-    const bool limit_k = kk >= 1 && kk < V;
-    const float pf = a.top_ps ? a.top_ps[m] : a.top_p;
-    const bool limit_p = pf < 1.f;
-    const double p = (double)fmaxf(pf, 0.f);
-    const float mf = a.min_ps ? a.min_ps[m] : a.min_p;
-    const double min_w = mf > 0.f ? (double)fminf(mf, 1.f) : 0.0;
+    const int m = (int)blockIdx.x;
+    const Row<kKind> row(a, m);
+    const How how(a, m);
     const float uf = a.u[m];
-    const int piece = (int)(((int64_t)V + kWaves * kStep - 1) / (kWaves * kStep)) * kStep;     // of a wave
-    const int64_t from64 = (int64_t)wv * piece;
-    const int from = from64 < V ? (int)from64 : V, to = V - from < piece ? V : from + piece;
+    const int piece = row.piece();
+    const int from = row.start((int64_t)wv * piece), to = row.start((int64_t)(wv + 1) * piece);
+    [[maybe_unused]] const Left* left = kLeft ? a.left + m : nullptr;
 
-    // f(logits, index of the first) for each eight of [i0, i1), in rising order of a lane
-    auto walk = [&](int i0, int i1, auto f) {
-        for (int i = i0 + kVec * lane; i - kVec * lane < i1; i += kAhead * kStep) {
-            Eight r[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) r[j] = L::load(row, i + j * kStep, i1, aligned);
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) f(r[j], i + j * kStep);
-        }
-    };
-
-    // ---- the largest, of the thread and of all
+    // ---- 1. the largest, of the thread and of all
     float mine = -INFINITY;
-    walk(from, to, [&](const Eight& r, int) {
+    if constexpr (kLeft) {
+        if (tid < kGroups) mine = left->group_max[tid];
+    } else {
+        row.template walk<kKind == 2 ? 3 : 8>(from, to, [&](const Eight& r, int) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) mine = fmaxf(mine, L::at(r, e));
-    });
-    if (tid < 64) sh.table[tid] = exp2((double)tid / 64.0);
+            for (int e = 0; e < kVec; ++e) mine = fmaxf(mine, L::at(r, e));
+        });
+    }
     float top = mine;
     for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
     if (lane == 0) sh.part[wv] = (double)top;
     __syncthreads();
     for (int k = 0; k < kWaves; ++k) top = fmaxf(top, (float)sh.part[k]);
+    __syncthreads();
     if (top == -INFINITY) {
         if (tid == 0) {
             a.ids[m] = -1;
@@ -304,12 +640,12 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
         }
         return;
     }
-    if (greedy) {
+    if (how.greedy) {
         // the lowest index that has it
         if (tid == 0) sh.box[0] = kNone;
         __syncthreads();
         int at = kNone;
-        walk(from, to, [&](const Eight& r, int i) {
+        row.template walk<kKind == 2 ? 2 : 4>(from, to, [&](const Eight& r, int i) {
 #pragma unroll
             for (int e = kVec - 1; e >= 0; --e)
                 if (L::at(r, e) == top && i + e < at) at = i + e;
@@ -322,116 +658,239 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
         }
         return;
     }
-    const Weight weight{(double)top, 1.4426950408889634 / (double)t, sh.table, top == INFINITY};
-    const double unit = (double)(1ull << a.unit_shift);
-    // (unit <= 2^51: the sum's low 52 bits are the nearest whole number)
-    auto fixed = [&](double w) { return __builtin_bit_cast(uint64_t, fma(w, unit, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull; };
+    const Weight weight(top, how.t);
+    const double unit = (double)(1ull << a.unit_shift), min_w = how.min_w;
+    auto fixed = [&](double w) { return fixed_point(w, unit); };
     const bool last_of_all = uf >= 1.f;
     const double share = uf > 0.f ? (double)uf : 0.0;
     auto answer = [&](int id, double w, double total) {
         a.ids[m] = id;
         if (a.logprob) a.logprob[m] = (float)log(w / total);
     };
-
-    // ---- the list: logits that `take` wants, in index order; false where they are too many
-    auto gather = [&](auto take) {
-        int n = 0;
-        walk(from, to, [&](const Eight& r, int i) {
-            uint32_t hits = 0;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) hits |= take(L::at(r, e)) && i + e < to ? 1u << e : 0u;
-            if (__ballot(hits != 0) == 0) return;
-            int all;
-            int at = n + wave_before((int)__popc(hits), &all);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if ((hits >> e) & 1u) {
-                    if (at < kRoom) {
-                        sh.key[wv][at] = L::key(L::at(r, e));
-                        sh.index[wv][at] = i + e;
-                    }
-                    ++at;
-                }
-            n += all;
-        });
+    auto sums_of_waves = [&](double v, double* part) {            // -> of all
+        v = wave_sum(v);
+        __syncthreads();
+        if (lane == 0) part[wv] = v;
+        __syncthreads();
+        double all = 0.0;
+        for (int k = 0; k < kWaves; ++k) all += part[k];
+        return all;
+    };
+    auto lists_fit = [&](int n) {
         __syncthreads();
         if (lane == 0) sh.listed[wv] = n;
         __syncthreads();
         bool fits = true;
-        for (int k = 0; k < kWaves; ++k) fits = fits && sh.listed[k] <= kRoom;
+        for (int k = 0; k < kPieces; ++k) fits = fits && sh.listed[k] <= kRoom;
         return fits;
     };
 
-    bool listed = false;
-    double whole = 0.0;                          // the weight of all, where it is known
-    if (limit_k && kk <= kThreads) {
-        uint32_t bound;
-        int equals;
-        find_count<L>(sh, [&](auto f) { f(L::key(mine)); }, kk, &bound, &equals);
-        listed = gather([&](float z) { return L::key(z) >= bound; });
-    } else if (limit_p && !limit_k && !weight.endless) {
-        __syncthreads();
-        if (tid < 256) sh.mass[tid] = 0ull;
-        __syncthreads();
-        double sum = 0.0;
-        auto bin_of = [&](double x) { return (int)(x * -16.0); };
-        walk(from, to, [&](const Eight& r, int) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const double x = weight.octaves(L::at(r, e)), w = weight.power(x);
-                sum += w;
-                if (x > (double)-kOctaves) atomicAdd(&sh.mass[bin_of(x)], (unsigned long long)fixed(w));
+    // ---- 2. and 3. lists and sums of the pieces. `listed`: the list holds what is kept (top-k) or
+    // what may be cut (top-p); `summed`: sh.part holds the pieces' sums, sh.above what lies above the list
+    bool listed = false, summed = false;
+    double whole = 0.0;                          // the weight of all
+    if (how.limit_k ? how.k <= kThreads : !weight.endless) {
+        if (kLeft && how.by_groups && top != INFINITY) {
+            int n = left->listed[wv];
+            for (int j = lane; j < n && j < kRoom; j += 64) {
+                sh.key[wv][j] = left->key[wv][j];
+                sh.index[wv][j] = left->index[wv][j];
             }
-        });
-        sum = wave_sum(sum);
-        if (lane == 0) sh.part[wv] = sum;
-        if (tid == 0) sh.box[0] = -1;
-        __syncthreads();
-        for (int k = 0; k < kWaves; ++k) whole += sh.part[k];
-        if (tid < 64) {
-            uint64_t own = 0, all;
+            listed = lists_fit(n);
+        } else if (how.limit_k) {
+            uint32_t bound;
+            if (how.by_groups && !kLeft) {
+                float most = fmaxf(mine, __shfl_xor(mine, 1));
+                most = fmaxf(most, __shfl_xor(most, 2));
+                if ((lane & 3) == 0) reinterpret_cast<uint32_t*>(sh.short_key)[tid >> 2] = L::key(most);
+                __syncthreads();
+                if (tid < kGroups && rank_of(sh.short_key, kGroups, tid) == how.k - 1) sh.box[0] = (int)reinterpret_cast<uint32_t*>(sh.short_key)[tid];
+                __syncthreads();
+                bound = (uint32_t)sh.box[0];
+            } else {
+                if constexpr (kLeft) {
+                    mine = -INFINITY;
+                    row.template walk<kKind == 2 ? 2 : 4>(from, to, [&](const Eight& r, int) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) own += sh.mass[4 * lane + j];
-            uint64_t above = wave_before((uint64_t)own, &all);
-            // (a little more than p: the list only has to hold what is kept)
-            const double want = p * whole * unit * (1.0 + 1e-9) + 1.0;
-            if ((double)above < want && (double)(above + own) >= want) {
-                int b = 4 * lane;
-                while ((double)(above + sh.mass[b]) < want) above += sh.mass[b++];
-                sh.box[0] = b;
+                        for (int e = 0; e < kVec; ++e) mine = fmaxf(mine, L::at(r, e));
+                    });
+                }
+                int equals;
+                find_count<L>(sh, [&](auto f) { f(L::key(mine)); }, how.k, &bound, &equals);
+            }
+            listed = lists_fit(row.gather(from, to, L::value(bound), NAN, sh.key[wv], sh.index[wv], kRoom, 0));
+        } else if constexpr (kLeft) {
+            whole = 0.0;
+            if (tid < kPieces) {
+                sh.part[tid] = left->sum[tid];
+                if (how.by_bins) {
+                    sh.above[tid] = left->above[tid];
+                    sh.above_kept[tid] = left->above_kept[tid];
+                }
+            }
+            if (how.by_bins) {
+                int n = left->listed[wv];
+                for (int j = lane; j < n && j < kRoom; j += 64) {
+                    sh.key[wv][j] = left->key[wv][j];
+                    sh.index[wv][j] = left->index[wv][j];
+                }
+                listed = summed = lists_fit(n);
+            } else {
+                __syncthreads();
+                summed = true;
+            }
+            for (int k = 0; k < kPieces; ++k) whole += sh.part[k];
+        } else {
+            if (tid < kBins) sh.mass[tid] = 0ull;
+            __syncthreads();
+            double sum = 0.0;
+            row.stroll(from, to, [&](const Eight& r, int) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const double x = weight.octaves(L::at(r, e)), v = weight.power(x);
+                    if (how.by_bins) {
+                        sum += v;
+                        if (x > -(double)(kBins / kBinsPerOctave)) atomicAdd(&sh.mass[bin_of(x)], (unsigned long long)fixed(v));
+                    } else {
+                        sum += v >= min_w ? v : 0.0;
+                    }
+                }
+            });
+            whole = sums_of_waves(sum, sh.part);
+            summed = true;
+            if (how.by_bins) {
+                if (wv == 0) find_bins(sh.mass, how.p * whole * unit, sh.box);
+                __syncthreads();
+                const int first = sh.box[0], last = sh.box[1];
+                summed = first >= 0 && last >= 0;
+                if (summed) {
+                    const float low = bin_end(weight, last, 1e-6), high = first > 0 ? bin_end(weight, first - 1, -1e-6) : INFINITY;
+                    listed = summed = lists_fit(row.gather(from, to, low, high, sh.key[wv], sh.index[wv], kRoom, 0));
+                    double above = 0.0, above_kept = 0.0;
+                    if (listed)
+                        row.stroll(from, to, [&](const Eight& r, int) {
+                            float most = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < kVec; ++e) most = fmaxf(most, L::at(r, e));
+                            if (__ballot(most >= high) == 0) return;
+#pragma unroll
+                            for (int e = 0; e < kVec; ++e) {
+                                const double v = L::at(r, e) >= high ? weight(L::at(r, e)) : 0.0;
+                                above += v;
+                                above_kept += v >= min_w ? v : 0.0;
+                            }
+                        });
+                    sums_of_waves(above, sh.above);
+                    sums_of_waves(above_kept, sh.above_kept);
+                }
             }
         }
-        __syncthreads();
-        const int bin = sh.box[0];
-        if (bin >= 0) listed = gather([&](float z) {
-            const double x = weight.octaves(z);
-            return x > (double)-kOctaves && bin_of(x) <= bin;
-        });
     }
     __syncthreads();
 
-    if (listed) {
+    uint32_t cut = 0;                            // keys above it are kept,
+    int ties = kNone;                            // of those equal to it the first `ties`,
+    int last_tie = kNone;                        // which end at this index
+    int entries = 0, first_entry = 0;
+    if (listed)
+        for (int k = 0; k < kPieces; ++k) {
+            if (k == wv) first_entry = entries;
+            entries += sh.listed[k];
+        }
+    double over_list = 0.0;                      // the weight above the list
+    if (summed && how.by_bins)
+        for (int k = 0; k < kPieces; ++k) over_list += sh.above[k];
+    bool cut_found = summed && !how.by_bins;     // only the draw is left
+    if (listed && entries <= kShort) {
+        // ---- a short list: the entries in falling order by counting, then back in index order
+        for (int j = lane; j < sh.listed[wv]; j += 64) {
+            reinterpret_cast<uint32_t*>(sh.short_key)[first_entry + j] = sh.key[wv][j];
+            sh.short_index[first_entry + j] = sh.index[wv][j];
+        }
+        if (tid == 0) sh.box[0] = -1;
+        __syncthreads();
+        if (how.limit_k && tid >= kShort) return;
+        // sums over the first four waves: of the lower threads, and of all
+        auto before_of = [&](double v, double* all) {
+            double own;
+            double low = wave_before(v, &own);
+            __syncthreads();
+            if (lane == 0 && wv < kShort / 64) sh.sorted[kShort - 1 - wv] = own;
+            __syncthreads();
+            *all = 0.0;
+            for (int k = 0; k < kShort / 64; ++k) {
+                if (k == wv) low += *all;
+                *all += sh.sorted[kShort - 1 - k];
+            }
+            __syncthreads();
+            return low;
+        };
+        int rank = 0;
+        double own_w = 0.0;
+        if (tid < entries) {
+            rank = rank_of(sh.short_key, entries, tid);
+            own_w = weight(L::value(reinterpret_cast<uint32_t*>(sh.short_key)[tid]));
+            sh.sorted[rank] = own_w;
+            sh.entry[rank] = tid;
+        }
+        __syncthreads();
+        const int at = tid < entries ? sh.entry[tid] : 0;            // thread r: the entry of rank r
+        double w = tid < entries && (!how.limit_k || tid < how.k) ? sh.sorted[tid] : 0.0, all;
+        const double above = before_of(w, &all) + over_list;
+        const bool stays = tid < entries && (how.limit_k ? tid < how.k && (!how.limit_p || tid == 0 || above < how.p * all)
+                                                         : above < how.p * whole || (tid == 0 && over_list == 0.0));
+        if (how.by_bins) {
+            // the last that stays is the cut
+            if (stays) atomicMax(&sh.box[0], tid);
+            __syncthreads();
+            const int last = sh.box[0];
+            if (tid == (last < 0 ? 0 : last) && tid < entries) {
+                sh.box[1] = last < 0 ? -1 : sh.short_index[at];
+                sh.count[0] = reinterpret_cast<uint32_t*>(sh.short_key)[at];
+            }
+            __syncthreads();
+            cut = entries ? sh.count[0] : 0u;
+            last_tie = entries ? sh.box[1] : kNone;
+            cut_found = true;
+        } else {
+            if (!stays || w < min_w) w = 0.0;
+            if (tid < entries) sh.sorted[at] = w;
+            if (tid == 0) {
+                sh.box[0] = kNone;
+                sh.box[1] = -1;
+            }
+            __syncthreads();
+            w = tid < entries ? sh.sorted[tid] : 0.0;
+            double total;
+            const double low = before_of(w, &total);
+            if (w > 0.0) {
+                if (!last_of_all && low + w > share * total) atomicMin(&sh.box[0], tid);
+                atomicMax(&sh.box[1], tid);
+            }
+            __syncthreads();
+            if (tid == (sh.box[0] != kNone ? sh.box[0] : sh.box[1])) answer(sh.short_index[tid], w, total);
+            return;
+        }
+    } else if (listed) {
         const int n = sh.listed[wv];
         auto each = [&](auto f) {
             for (int j = lane; j < n; j += 64) f(sh.key[wv][j], sh.index[wv][j]);
         };
-        uint32_t cut = 0;                        // keys above it are kept,
-        int ties = kNone;                        // of those equal to it the first `ties`
-        if (limit_k) find_count<L>(sh, [&](auto f) { each([&](uint32_t key, int) { f(key); }); }, kk, &cut, &ties);
-        // sums of w over the entries down to the cut, ties in index order
-        auto kept_sums = [&](bool floor, double* before, double* all) {
-            int equals = 0;
+        if (how.limit_k) find_count<L>(sh, [&](auto f) { each([&](uint32_t key, int) { f(key); }); }, how.k, &cut, &ties);
+        // how many of the equals of the cut this wave keeps
+        auto keep_of = [&] {
+            int equals = 0, wave_equals;
             for (int j = lane; j < n; j += 64) equals += sh.key[wv][j] == cut;
-            int wave_equals;
             wave_before(equals, &wave_equals);
             __syncthreads();
             if (lane == 0) sh.listed[wv] = wave_equals;
             __syncthreads();
             int seen = 0;
             for (int k = 0; k < wv; ++k) seen += sh.listed[k];
-            // ties seen so far turn into the number of this wave's that are kept
-            const int keep = ties == kNone ? kNone : ties > seen ? ties - seen : 0;
-            double sum = 0.0;
+            return ties > seen ? ties - seen : 0;
+        };
+        // sum of w over the wave's entries that are kept; f(entry, w) for each round of 64
+        auto kept_entries = [&](int keep, auto f) {
             int met = 0;
             for (int j0 = 0; j0 < n; j0 += 64) {
                 const int j = j0 + lane;
@@ -441,159 +900,173 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
                 met += __popcll(mask);
                 double w = 0.0;
                 if (j < n && (sh.key[wv][j] > cut || (tie && rank < keep))) w = weight(L::value(sh.key[wv][j]));
-                if (floor && w < min_w) w = 0.0;
-                sum += wave_sum(w);
+                if (f(j, w)) return;
             }
-            __syncthreads();
-            if (lane == 0) sh.part[wv] = sum;
-            __syncthreads();
-            *before = *all = 0.0;
-            for (int k = 0; k < kWaves; ++k) {
-                if (k == wv) *before = *all;
-                *all += sh.part[k];
-            }
-            return keep;
         };
-        if (limit_p) {
+        auto kept_sum = [&](int keep) {
+            double sum = 0.0;
+            kept_entries(keep, [&](int, double w) {
+                sum += w;
+                return false;
+            });
+            return sum;
+        };
+        if (how.limit_p) {
             const uint32_t kcut = cut;
             const int kties = ties;
-            if (limit_k) {
-                double before;
-                kept_sums(false, &before, &whole);
-            }
-            // the ties of the k-th count as often as they are kept: one entry brings them all
-            const double target = p * whole * unit;
+            if (how.limit_k) whole = sums_of_waves(kept_sum(keep_of()), sh.part);
+            const double target = (how.p * whole - over_list) * unit;
             uint64_t above;
             int there;
-            const uint64_t tie_mass = limit_k ? (uint64_t)kties * fixed(weight(L::value(kcut))) : 0;
+            // the ties of the k-th count as often as they are kept: one entry brings them all
+            const uint64_t tie_mass = how.limit_k ? (uint64_t)kties * fixed(weight(L::value(kcut))) : 0;
             find_mass<L>(sh, [&](auto f) {
                 each([&](uint32_t key, int) {
-                    if (!limit_k || key > kcut) f(key, [&] { return fixed(weight(L::value(key))); });
+                    if (!how.limit_k || key > kcut) f(key, [&] { return fixed(weight(L::value(key))); });
                 });
-                if (limit_k && tid == 0) f(kcut, [&] { return tie_mass; });
+                if (how.limit_k && tid == 0) f(kcut, [&] { return tie_mass; });
             }, target, &cut, &above, &there);
-            if (limit_k && cut == kcut) there = kties;
+            if (how.limit_k && cut == kcut) there = kties;
             const uint64_t one = fixed(weight(L::value(cut)));
             // tie j (from 0) is kept while what lies before it is below the target
+            double need = one ? ceil((target - (double)above) / (double)one) : (double)there;
+            const double least = how.limit_k || over_list == 0.0 ? 1.0 : 0.0;
+            need = need < least ? least : need;
+            ties = need < (double)there ? (int)need : there;
+        }
+        const int keep = keep_of();
+        if (how.by_bins) {
+            // the index of the last tie that is kept (none: -1)
+            if (tid == 0) sh.box[0] = -1;
+            __syncthreads();
+            int met = 0;
+            for (int j0 = 0; j0 < n; j0 += 64) {
+                const int j = j0 + lane;
+                const bool tie = j < n && sh.key[wv][j] == cut;
+                const uint64_t mask = __ballot(tie);
+                if (tie && met + __popcll(mask & ((1ull << lane) - 1ull)) < keep) atomicMax(&sh.box[0], sh.index[wv][j]);
+                met += __popcll(mask);
+            }
+            // (what this wave's list had is overwritten: its length is still in n)
+            __syncthreads();
+            last_tie = sh.box[0];
+            cut_found = true;
+            if (lane == 0) sh.listed[wv] = n;
+            __syncthreads();
+        } else {
+            double sum = 0.0;
+            kept_entries(keep, [&](int, double w) {
+                sum += w >= min_w ? w : 0.0;
+                return false;
+            });
+            const double total = sums_of_waves(sum, sh.part);
+            const double target = share * total;
+            // the wave in which the running sum exceeds the target, or the last that keeps any
+            int wave = -1, fallback = 0;
+            double run = 0.0, before = 0.0;
+            for (int k = 0; k < kWaves; ++k) {
+                if (sh.part[k] > 0.0) {
+                    fallback = k;
+                    if (!last_of_all && wave < 0 && run + sh.part[k] > target) {
+                        wave = k;
+                        before = run;
+                    }
+                }
+                run += sh.part[k];
+            }
+            const bool exact = wave >= 0;
+            if (!exact) wave = fallback;
+            if (wv != wave) return;
+            int last_id = -1;
+            double at = before, last_w = 0.0;
+            bool done = false;
+            kept_entries(keep, [&](int j, double w) {
+                double all;
+                if (w < min_w) w = 0.0;
+                const double low = wave_before(w, &all);
+                const uint64_t over = exact ? __ballot(w > 0.0 && at + low + w > target) : 0;
+                if (over) {
+                    if (lane == __builtin_ctzll(over)) answer(sh.index[wv][j], w, total);
+                    done = true;
+                    return true;
+                }
+                const uint64_t some = __ballot(w > 0.0);
+                if (some) {
+                    const int from_lane = 63 - __builtin_clzll(some);
+                    last_id = __shfl(j < n ? sh.index[wv][j] : 0, from_lane);
+                    last_w = __shfl(w, from_lane);
+                }
+                at += all;
+                return false;
+            });
+            if (!done && lane == 0) answer(last_id, last_w, total);
+            return;
+        }
+    }
+
+    // ---- thresholds over the row itself
+    if (!cut_found) {
+        auto each = [&](auto f) {
+            row.stroll(from, to, [&](const Eight& r, int i) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (i + e < to) f(L::at(r, e));
+            });
+        };
+        if (how.limit_k) find_count<L>(sh, [&](auto f) { each([&](float z) { f(L::key(z)); }); }, how.k, &cut, &ties);
+        if (how.limit_p) {
+            const uint32_t kcut = cut;
+            const int kties = ties;
+            const uint64_t tie_mass = how.limit_k ? (uint64_t)kties * fixed(weight(L::value(kcut))) : 0;
+            double sum = 0.0;
+            each([&](float z) {
+                if (!how.limit_k || L::key(z) > kcut) sum += weight(z);
+            });
+            whole = sums_of_waves(sum, sh.part) + (how.limit_k ? (double)kties * weight(L::value(kcut)) : 0.0);
+            const double target = how.p * whole * unit;
+            uint64_t above;
+            int there;
+            find_mass<L>(sh, [&](auto f) {
+                each([&](float z) {
+                    if (!how.limit_k || L::key(z) > kcut) f(L::key(z), [&] { return fixed(weight(z)); });
+                });
+                if (how.limit_k && tid == 0) f(kcut, [&] { return tie_mass; });
+            }, target, &cut, &above, &there);
+            if (how.limit_k && cut == kcut) there = kties;
+            const uint64_t one = fixed(weight(L::value(cut)));
             double need = one ? ceil((target - (double)above) / (double)one) : (double)there;
             need = need < 1.0 ? 1.0 : need;
             ties = need < (double)there ? (int)need : there;
         }
-        double before, total;
-        const int keep = kept_sums(true, &before, &total);
-        const double target = share * total;
-        // the wave in which the running sum exceeds the target, or the last that keeps any
-        int wave = -1, fallback = 0;
-        double run = 0.0;
-        for (int k = 0; k < kWaves; ++k) {
-            if (sh.part[k] > 0.0) {
-                fallback = k;
-                if (!last_of_all && wave < 0 && run + sh.part[k] > target) wave = k;
-            }
-            run += sh.part[k];
+        // the index of the last tie that is kept
+        if (ties != kNone) {
+            int equals = 0, wave_equals;
+            each([&](float z) { equals += L::key(z) == cut; });
+            wave_before(equals, &wave_equals);
+            __syncthreads();
+            if (lane == 0) sh.listed[wv] = wave_equals;
+            if (tid == 0) sh.box[0] = kNone;
+            __syncthreads();
+            int seen = 0;
+            for (int k = 0; k < wv; ++k) seen += sh.listed[k];
+            if (seen < ties && seen + sh.listed[wv] >= ties)
+                row.stroll(from, to, [&](const Eight& r, int i) {
+                    int n = 0, all;
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) n += i + e < to && L::key(L::at(r, e)) == cut;
+                    int at = seen + wave_before(n, &all);
+                    seen += all;
+                    if (at < ties && at + n >= ties) {
+#pragma unroll
+                        for (int e = 0; e < kVec; ++e)
+                            if (i + e < to && L::key(L::at(r, e)) == cut && ++at == ties) sh.box[0] = i + e;
+                    }
+                });
+            __syncthreads();
+            last_tie = sh.box[0];
         }
-        const bool exact = wave >= 0;
-        if (!exact) wave = fallback;
-        if (wv != wave) return;
-        double sum = before;
-        int met = 0, last_id = -1;
-        double last_w = 0.0;
-        for (int j0 = 0; j0 < n; j0 += 64) {
-            const int j = j0 + lane;
-            const bool tie = j < n && sh.key[wv][j] == cut;
-            const uint64_t mask = __ballot(tie);
-            const int rank = met + __popcll(mask & ((1ull << lane) - 1ull));
-            met += __popcll(mask);
-            double w = 0.0, all;
-            if (j < n && (sh.key[wv][j] > cut || (tie && rank < keep))) w = weight(L::value(sh.key[wv][j]));
-            if (w < min_w) w = 0.0;
-            const double low = wave_before(w, &all);
-            const uint64_t over = exact ? __ballot(w > 0.0 && sum + low + w > target) : 0;
-            if (over) {
-                if (lane == __builtin_ctzll(over)) answer(sh.index[wv][j], w, total);
-                return;
-            }
-            const uint64_t some = __ballot(w > 0.0);
-            if (some) {
-                const int from_lane = 63 - __builtin_clzll(some);
-                last_id = __shfl(j < n ? sh.index[wv][j] : 0, from_lane);
-                last_w = __shfl(w, from_lane);
-            }
-            sum += all;
-        }
-        if (lane == 0) answer(last_id, last_w, total);
-        return;
     }
-
-    // ---- over the row itself
-    uint32_t cut = 0;
-    int ties = kNone;
-    auto each = [&](auto f) {
-        walk(from, to, [&](const Eight& r, int i) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (i + e < to) f(L::at(r, e));
-        });
-    };
-    if (limit_k) find_count<L>(sh, [&](auto f) { each([&](float z) { f(L::key(z)); }); }, kk, &cut, &ties);
-    if (limit_p) {
-        const uint32_t kcut = cut;
-        const int kties = ties;
-        const uint64_t tie_mass = limit_k ? (uint64_t)kties * fixed(weight(L::value(kcut))) : 0;
-        double sum = 0.0;
-        each([&](float z) {
-            if (!limit_k || L::key(z) > kcut) sum += weight(z);
-        });
-        sum = wave_sum(sum);
-        __syncthreads();
-        if (lane == 0) sh.part[wv] = sum;
-        __syncthreads();
-        whole = limit_k ? (double)kties * weight(L::value(kcut)) : 0.0;
-        for (int k = 0; k < kWaves; ++k) whole += sh.part[k];
-        const double target = p * whole * unit;
-        uint64_t above;
-        int there;
-        find_mass<L>(sh, [&](auto f) {
-            each([&](float z) {
-                if (!limit_k || L::key(z) > kcut) f(L::key(z), [&] { return fixed(weight(z)); });
-            });
-            if (limit_k && tid == 0) f(kcut, [&] { return tie_mass; });
-        }, target, &cut, &above, &there);
-        if (limit_k && cut == kcut) there = kties;
-        const uint64_t one = fixed(weight(L::value(cut)));
-        double need = one ? ceil((target - (double)above) / (double)one) : (double)there;
-        need = need < 1.0 ? 1.0 : need;
-        ties = need < (double)there ? (int)need : there;
-    }
-    // the index of the last tie that is kept
-    int last_tie = kNone;
-    if (ties != kNone) {
-        int equals = 0, wave_equals;
-        each([&](float z) { equals += L::key(z) == cut; });
-        wave_before(equals, &wave_equals);
-        __syncthreads();
-        if (lane == 0) sh.listed[wv] = wave_equals;
-        if (tid == 0) sh.box[0] = kNone;
-        __syncthreads();
-        int seen = 0;
-        for (int k = 0; k < wv; ++k) seen += sh.listed[k];
-        if (seen < ties && seen + sh.listed[wv] >= ties)
-            walk(from, to, [&](const Eight& r, int i) {
-                int n = 0, all;
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) n += i + e < to && L::key(L::at(r, e)) == cut;
-                int at = seen + wave_before(n, &all);
-                seen += all;
-                if (at < ties && at + n >= ties) {
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        if (i + e < to && L::key(L::at(r, e)) == cut && ++at == ties) sh.box[0] = i + e;
-                }
-            });
-        __syncthreads();
-        last_tie = sh.box[0];
-    }
-    const bool all_kept = ties == kNone && min_w == 0.0;
+    const bool all_kept = cut == 0 && min_w == 0.0;
     auto kept = [&](float z, int i) -> double {
         if (!all_kept) {
             const uint32_t key = L::key(z);
@@ -602,27 +1075,34 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
         const double w = weight(z);
         return w >= min_w ? w : 0.0;
     };
-    // Sums of the sixteen pieces of a range, then of those of the one in which the running sum
-    // exceeds the target, until a piece is one step of a wave.
-    int i0 = 0, i1 = V;
-    double run = 0.0, total = 0.0, target = 0.0;
-    bool exact = !last_of_all;
-    for (int size = piece;;) {
-        const int64_t b64 = (int64_t)i0 + (int64_t)wv * size;
-        const int b = b64 < i1 ? (int)b64 : i1, e1 = i1 - b < size ? i1 : b + size;
+    // ---- 4. sums of the pieces, then of the sixteenths of the one in which the running sum exceeds the
+    // target, until one is a step of a wave
+    if (!summed) {
         double sum = 0.0;
-        walk(b, e1, [&](const Eight& r, int i) {
+        row.stroll(from, to, [&](const Eight& r, int i) {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) sum += i + e < e1 ? kept(L::at(r, e), i + e) : 0.0;
+            for (int e = 0; e < kVec; ++e) sum += i + e < to ? kept(L::at(r, e), i + e) : 0.0;
         });
+        sums_of_waves(sum, sh.part);
+    } else if (how.by_bins) {
+        // what is surely kept, and what of the list is
+        double sum = 0.0;
+        for (int j = lane; j < sh.listed[wv]; j += 64) {
+            const double w = sh.key[wv][j] > cut || (sh.key[wv][j] == cut && sh.index[wv][j] <= last_tie) ? weight(L::value(sh.key[wv][j])) : 0.0;
+            sum += w >= min_w ? w : 0.0;
+        }
         sum = wave_sum(sum);
         __syncthreads();
-        if (lane == 0) sh.part[wv] = sum;
+        if (lane == 0) sh.part[wv] = sum + sh.above_kept[wv];
         __syncthreads();
-        if (total == 0.0) {
-            for (int k = 0; k < kWaves; ++k) total += sh.part[k];
-            target = share * total;
-        }
+    }
+    double total = 0.0;
+    for (int k = 0; k < kPieces; ++k) total += sh.part[k];
+    const double target = share * total;
+    int i0 = 0, i1 = row.V;
+    double run = 0.0;
+    bool exact = !last_of_all;
+    for (int size = piece;;) {
         int wave = -1, fallback = 0;
         double at = run, before = run, before_last = run;
         for (int k = 0; k < kWaves; ++k) {
@@ -647,10 +1127,18 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
         i0 = (int)n0;
         if (size <= kStep) break;
         size = (int)(((int64_t)size + kWaves * kStep - 1) / (kWaves * kStep)) * kStep;
+        const int64_t b64 = (int64_t)i0 + (int64_t)wv * size;
+        const int b = b64 < i1 ? (int)b64 : i1, e1 = i1 - b < size ? i1 : b + size;
+        double sum = 0.0;
+        row.stroll(b, e1, [&](const Eight& r, int i) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) sum += i + e < e1 ? kept(L::at(r, e), i + e) : 0.0;
+        });
+        sums_of_waves(sum, sh.part);
     }
     if (wv != 0) return;
     const int i = i0 + kVec * lane;
-    const Eight r = L::load(row, i, i1, aligned);
+    const Eight r = L::load(row.p, i, i1, row.aligned);
     double w[kVec], own = 0.0, all;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
@@ -675,14 +1163,34 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     const uint64_t over = exact ? __ballot(hit != kNone) : 0, some = __ballot(last_kept >= 0);
     if (over) {
         if (lane == __builtin_ctzll(over)) answer(hit, hit_w, total);
-    } else if (lane == 63 - __builtin_clzll(some)) {
+    } else if (some && lane == 63 - __builtin_clzll(some)) {
         answer(last_kept, last_w, total);
     }
 }
 
+template <int kKind>
+void launch_kind(const SampleArgs& a, hipStream_t s) {
+    if (a.left) {
+        const dim3 pieces((unsigned)(a.M * kPieces)), block(kPieceThreads);
+        hipLaunchKernelGGL((piece_max_kernel<kKind>), pieces, block, 0, s, a);
+        hipLaunchKernelGGL((piece_sum_kernel<kKind>), pieces, block, 0, s, a);
+        // (without settings of each row, the host knows which rows cut by bins: none or all)
+        if (a.top_ks || a.top_ps || (a.top_p < 1.f && !(a.top_k >= 1 && a.top_k < a.V)))
+            hipLaunchKernelGGL((piece_cut_kernel<kKind>), pieces, block, 0, s, a);
+        hipLaunchKernelGGL((sample_kernel<kKind, true>), dim3((unsigned)a.M), dim3(kThreads), 0, s, a);
+    } else {
+        hipLaunchKernelGGL((sample_kernel<kKind, false>), dim3((unsigned)a.M), dim3(kThreads), 0, s, a);
+    }
+}
+
+// Rows that leave most of the chip idle with a workgroup each, where they are long enough to be worth the launches.
+bool in_pieces(int64_t M, int64_t V) { return M <= 64 && V >= 16384; }
+
 }  // namespace
 
-hipError_t launch_sample(const SampleCall& q, hipStream_t stream) {
+size_t sample_workspace(int64_t M, int64_t V) { return in_pieces(M, V) ? (size_t)M * sizeof(Left) : 0; }
+
+hipError_t launch_sample(const SampleCall& q, void* scratch, hipStream_t stream) {
     SampleArgs a{};
     a.logits = q.logits;
     a.ld = q.ld;
@@ -703,10 +1211,10 @@ hipError_t launch_sample(const SampleCall& q, hipStream_t stream) {
     a.ids = q.ids;
     a.logprob = q.logprob;
     a.aligned = (reinterpret_cast<uintptr_t>(q.logits) & 15) == 0 && (q.ld * (q.kind == 2 ? 4 : 2)) % 16 == 0;
-    const dim3 grid((unsigned)q.M), block(kThreads);
-    if (q.kind == 0) hipLaunchKernelGGL((sample_kernel<0>), grid, block, 0, stream, a);
-    else if (q.kind == 1) hipLaunchKernelGGL((sample_kernel<1>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((sample_kernel<2>), grid, block, 0, stream, a);
+    a.left = in_pieces(q.M, q.V) ? static_cast<Left*>(scratch) : nullptr;
+    if (q.kind == 0) launch_kind<0>(a, stream);
+    else if (q.kind == 1) launch_kind<1>(a, stream);
+    else launch_kind<2>(a, stream);
     return hipGetLastError();
 }
 
