@@ -7,11 +7,10 @@
 // its rows' last experts (a counter, as split_k.h has it) reads the l of its rows back and
 // chooses, a wave a row: each lane holds every 64th expert, the largest of all lanes comes by
 // row shifts, its owner by a ballot.
-#include <type_traits>
-
 #include "device_common.h"
 #include "launch.h"
 #include "split_k.h"
+#include "wave.h"
 
 namespace w4a16 {
 namespace {
@@ -33,36 +32,6 @@ struct RouteArgs {
     uint32_t* counters;     // one per group of rows
     uint64_t* logits;       // fp64 bits [M][E]
 };
-
-// v combined over the wave by row shifts, whole in lane 63 (lanes without a source take `none`)
-template <class Op>
-__device__ __forceinline__ double wave_join(double v, double none, Op op) {
-    auto step = [&](auto ctrl, auto rows) {
-        const uint64_t b = __builtin_bit_cast(uint64_t, v), n = __builtin_bit_cast(uint64_t, none);
-        const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)n, (int)(uint32_t)b, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-        const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(n >> 32), (int)(b >> 32), decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-        v = op(v, __builtin_bit_cast(double, (uint64_t)hi << 32 | lo));
-    };
-    using std::integral_constant;
-    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});      // row_shr 1, 2, 4, 8
-    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
-    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
-    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
-    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});      // lane 15 of a row to the next row
-    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});      // lane 31 to the upper half
-    return v;
-}
-__device__ __forceinline__ double from_lane(double v, int lane) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double wave_sum(double v) {
-    return from_lane(wave_join(v, 0.0, [](double a, double b) { return a + b; }), 63);
-}
-__device__ __forceinline__ double wave_max(double v) {
-    return from_lane(wave_join(v, -INFINITY, [](double a, double b) { return fmax(a, b); }), 63);
-}
 
 template <bool kBF16>
 __device__ __forceinline__ void dot8(const uint4& a, const uint4& b, double (&acc)[2]) {
@@ -115,7 +84,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int m) {
         double best = by[0];
 #pragma unroll
         for (int i = 1; i < N; ++i) best = fmax(best, by[i]);
-        best = from_lane(wave_join(best, NAN, [](double x, double y) { return fmax(x, y); }), 63);
+        best = from_lane(wave_scan(best, (double)NAN, [](double x, double y) { return fmax(x, y); }), 63);
         // the lowest expert that has it
         bool found = false;
 #pragma unroll
@@ -163,8 +132,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a) {
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) dot8<kBF16>(xw[p], rw[p], acc);
             for (int q = lane + 64 * kPieces; q < pieces; q += 64) dot8<kBF16>(x[q], r[q], acc);
-            const double sum = wave_join(acc[0] + acc[1], 0.0, [](double u, double v) { return u + v; });
-            if (lane == 63)
+            const double sum = wave_sum(acc[0] + acc[1]);
+            if (lane == 0)
                 __hip_atomic_store(a.logits + (size_t)m * a.E + e, __builtin_bit_cast(uint64_t, sum), __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
         }

@@ -10,8 +10,8 @@
 //   2. top-k up to 192: the k-th largest of the groups' bounds the k-th of all from below, and the
 //      few logits from it on are put into a list, in index order; all the rest happens there (a
 //      random row of 131072 and k = 50 lists 56). Otherwise: the sums of w, and with top-p w by
-//      eighths of an octave below the largest;
-//   3. top-p alone: the logits of the eighth in which p is reached are listed, those above it summed;
+//      32nds of an octave below the largest;
+//   3. top-p alone: the logits of the 32nd in which p is reached are listed, those above it summed;
 //   4. the draw: the piece whose sum of kept w holds the target, its sixteenth, and so on.
 // A few rows take 16 workgroups each, in a launch for each of these; many rows one workgroup each,
 // a wave a piece, in one launch. What the lists do not hold (top-k over 1024, lists of more than 512
@@ -24,6 +24,7 @@
 // of the draw are in fp64: next to a border 32 bits would give another token.
 #include "device_common.h"
 #include "launch.h"
+#include "wave.h"
 
 namespace w4a16 {
 namespace {
@@ -37,7 +38,7 @@ constexpr int kStep = 64 * kVec;                // of a wave
 constexpr int kRoom = 512;                      // listed logits of a piece
 constexpr int kShort = 256;                     // and of all in a short list
 constexpr int kGroups = 256;
-constexpr int kBins = 256, kBinsPerOctave = 8;  // below the largest
+constexpr int kBins = 1024, kBinsPerOctave = 32;   // of weights, below the largest
 constexpr int kNone = 0x7FFFFFFF;
 
 // what the launches for few rows leave to each other
@@ -47,8 +48,7 @@ struct Left {
     double above[kPieces];                      // top-p: of w above the list, and of those that min-p keeps
     double above_kept[kPieces];
     int listed[kPieces];
-    int pad[16];
-    unsigned long long mass[kPieces][kBins];
+    unsigned long long mass[kBins];
     uint32_t key[kPieces][kRoom];
     int index[kPieces][kRoom];
 };
@@ -112,8 +112,10 @@ template <int kKind> struct Logit {
             }
         } else {
             // (rolled: it is in every loop over the row, and rarely taken)
-            r.q[0] = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t none = kKind == 2 ? 0xFF800000u : kKind == 1 ? 0xFF80FF80u : 0xFC00FC00u;
+            r.q[0] = make_uint4(none, none, none, none);
             if constexpr (kKind == 2) r.q[1] = r.q[0];
+            if (i >= V) return r;
 #pragma unroll 1
             for (int e = kVec - 1; e >= 0; --e) {
                 if constexpr (kKind == 2) {
@@ -128,6 +130,10 @@ template <int kKind> struct Logit {
             }
         }
         return r;
+    }
+    static __device__ __forceinline__ float one(const void* row, int i) {
+        if constexpr (kKind == 2) return fmaxf(static_cast<const float*>(row)[i], -INFINITY);
+        else return fmaxf(half_bits_to_f32<kKind == 1>(static_cast<const uint16_t*>(row)[i]), -INFINITY);
     }
     // the e-th; -infinity for what is no number
     static __device__ __forceinline__ float at(const Eight& r, int e) {
@@ -204,23 +210,6 @@ __device__ __forceinline__ float bin_end(const Weight& w, int bin, double by) {
     return (float)(low - by * (fabs(low) + 1e-3 * fabs(w.top)));
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-    for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
-    return v;
-}
-template <class T>
-__device__ __forceinline__ T wave_before(T v, T* all) {            // sum of the lower lanes; of all
-    const int lane = (int)threadIdx.x & 63;
-    T sum = v;
-    for (int s = 1; s < 64; s <<= 1) {
-        const T o = __shfl_up(sum, s);
-        if (lane >= s) sum += o;
-    }
-    *all = __shfl(sum, 63);
-    const T up = __shfl_up(sum, 1);
-    return lane ? up : T(0);
-}
-
 template <int kKind> struct Row {
     using L = Logit<kKind>;
     using Eight = typename L::Eight;
@@ -250,24 +239,83 @@ template <int kKind> struct Row {
     // the same for a costly f, in less code
     template <class F>
     __device__ __forceinline__ void stroll(int i0, int i1, F f) const {
-        for (int i = i0 + kVec * lane; i - kVec * lane < i1; i += 4 * kStep) {
+        for (int i = i0; i < i1; i += 4 * kStep) {
             Eight r[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = L::load(p, i + j * kStep, i1, aligned);
+            for (int j = 0; j < 4; ++j) r[j] = L::load(p, i + j * kStep + kVec * lane, i1, aligned);
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                f(r[0], i + j * kStep);
+            for (int j = 0; j < 4 && i + j * kStep < i1; ++j) {
+                f(r[0], i + j * kStep + kVec * lane);
                 r[0] = r[1];
                 r[1] = r[2];
                 r[2] = r[3];
             }
         }
     }
+    // f(logit, its index), where speed matters least
+    template <class F>
+    __device__ __forceinline__ void each(int i0, int i1, F f) const {
+        stroll(i0, i1, [&](Eight q, int i) {
+#pragma unroll 1
+            for (int e = 0; e < kVec; ++e) {
+                if (i + e < i1) f(L::at(q, 0), i + e);
+                L::next(q);
+            }
+        });
+    }
+    // this lane's sum of w (without bins: of those that min-p keeps); with them, w by bins too
+    __device__ __forceinline__ double sum_of(int i0, int i1, const Weight& weight, const How& how, double unit, unsigned long long* mass) const {
+        double sum = 0.0;
+        if (how.by_bins) {
+            stroll(i0, i1, [&](const Eight& r, int) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const double x = weight.octaves(L::at(r, e)), v = weight.power(x);
+                    sum += v;
+                    if (x > -(double)(kBins / kBinsPerOctave)) atomicAdd(&mass[bin_of(x)], (unsigned long long)fixed_point(v, unit));
+                }
+            });
+        } else if (how.min_w > 0.0) {
+            stroll(i0, i1, [&](const Eight& r, int) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const double v = weight.power(weight.octaves(L::at(r, e)));
+                    sum += v >= how.min_w ? v : 0.0;
+                }
+            });
+        } else {
+            stroll(i0, i1, [&](const Eight& r, int) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) sum += weight.power(weight.octaves(L::at(r, e)));
+            });
+        }
+        return sum;
+    }
+    // of those from `high` on: all, and those that min-p keeps
+    __device__ __forceinline__ void sum_above(int i0, int i1, float high, const Weight& weight, double min_w, double* above, double* kept) const {
+        double all = 0.0, some = 0.0;
+        stroll(i0, i1, [&](Eight r, int) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) most = fmaxf(most, L::at(r, e));
+            if (__ballot(most >= high) == 0) return;
+#pragma unroll 1
+            for (int e = 0; e < kVec; ++e) {
+                const double v = L::at(r, 0) >= high ? weight(L::at(r, 0)) : 0.0;
+                all += v;
+                some += v >= min_w ? v : 0.0;
+                L::next(r);
+            }
+        });
+        *above = wave_sum(all);
+        *kept = wave_sum(some);
+    }
     // Entries of [i0, i1) from `low` up to below `high` (no number: all), in index order, from place n on; returns the
     // place behind the last (entries past `room` are only counted).
     __device__ __forceinline__ int gather(int i0, int i1, float low, float high, uint32_t* key, int* index, int room, int n) const {
         constexpr int kAhead = kKind == 2 ? 2 : 4;
         walk<kAhead>(i0, i1, [&](const Eight& r, int i) {
+            if (i - kVec * lane >= i1) return;
             float most = -INFINITY;
 #pragma unroll
             for (int e = 0; e < kVec; ++e) most = fmaxf(most, L::at(r, e));
@@ -307,6 +355,21 @@ struct Shared {
     uint32_t key[kPieces][kRoom];
     int index[kPieces][kRoom];
 };
+
+// The k-th largest of 256 keys, 4 a lane: bit by bit from the top, the largest bound that k reach.
+template <int kBits>
+__device__ __forceinline__ uint32_t kth_of(const uint32_t (&key)[4], int k) {
+    uint32_t bound = 0;
+#pragma unroll 1
+    for (uint32_t bit = 1u << (kBits - 1); bit; bit >>= 1) {
+        const uint32_t at = bound | bit;
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n += __popcll(__ballot(key[j] >= at));
+        if (n >= k) bound = at;
+    }
+    return bound;
+}
 
 // how many of the first n short keys come before the i-th: larger, or equal and earlier
 __device__ __forceinline__ int rank_of(const uint4* keys, int n, int i) {
@@ -415,10 +478,11 @@ __device__ __forceinline__ void find_mass(Shared& sh, Each each, double target, 
 // [1] is -1 where the bins do not reach it. For the first wave; mass is in LDS.
 __device__ __forceinline__ void find_bins(const unsigned long long* mass, double want, int* bins) {
     const int lane = (int)threadIdx.x & 63;
+    constexpr int kEach = kBins / 64;
     uint64_t own = 0, all;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) own += mass[4 * lane + j];
-    const uint64_t above = wave_before((uint64_t)own, &all);
+    for (int j = 0; j < kEach; ++j) own += mass[kEach * lane + j];
+    const uint64_t above = wave_before(own, &all);
     if (lane == 0) bins[0] = bins[1] = -1;
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -426,7 +490,7 @@ __device__ __forceinline__ void find_bins(const unsigned long long* mass, double
         const double at = fmax(side ? want * (1.0 + 1e-9) : want * (1.0 - 1e-9), 1.0);
         if ((double)above < at && (double)(above + own) >= at) {
             uint64_t sum = above;
-            int b = 4 * lane;
+            int b = kEach * lane;
             while ((double)(sum + mass[b]) < at) sum += mass[b++];
             bins[side] = b;
         }
@@ -449,20 +513,8 @@ __global__ __launch_bounds__(kPieceThreads) void piece_max_kernel(const SampleAr
         for (int e = 0; e < kVec; ++e) most = fmaxf(most, Logit<kKind>::at(r, e));
     });
     for (int s = 8; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor(most, s));
+    if (threadIdx.x < kBins / kPieces) a.left[m].mass[c * (kBins / kPieces) + (int)threadIdx.x] = 0ull;
     if ((threadIdx.x & 15) == 0) a.left[m].group_max[c * (kGroups / kPieces) + ((int)threadIdx.x >> 4)] = most;
-}
-
-// The largest of the groups, by 256 threads; the groups' keys are left in LDS.
-template <int kKind>
-__device__ __forceinline__ float top_of(const Left& left, uint4* keys, float* wave_top) {
-    const int tid = (int)threadIdx.x;
-    const float own = left.group_max[tid];
-    reinterpret_cast<uint32_t*>(keys)[tid] = Logit<kKind>::key(own);
-    float top = own;
-    for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-    if ((tid & 63) == 0) wave_top[tid >> 6] = top;
-    __syncthreads();
-    return fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
 }
 
 // Each wave's list of a piece to its place behind those of the waves before it.
@@ -485,16 +537,14 @@ __device__ __forceinline__ void leave_list(PieceList& l, Left& left, int c) {
 
 template <int kKind>
 __global__ __launch_bounds__(kPieceThreads) void piece_sum_kernel(const SampleArgs a) {
-    __shared__ uint4 keys[kGroups / 4];
-    __shared__ float wave_top[4];
     __shared__ double wave_part[4];
     __shared__ unsigned long long mass[kBins];
-    __shared__ uint32_t bound;
     __shared__ PieceList list;
     using L = Logit<kKind>;
     const int m = (int)blockIdx.x / kPieces, c = (int)blockIdx.x % kPieces, tid = (int)threadIdx.x, w = tid >> 6, lane = tid & 63;
     const How how(a, m);
-    const float top = top_of<kKind>(a.left[m], keys, wave_top);
+    const f32x4 groups = reinterpret_cast<const f32x4*>(a.left[m].group_max)[lane];
+    const float top = wave_max(fmaxf(fmaxf(groups[0], groups[1]), fmaxf(groups[2], groups[3])));
     // (all, or left to the last launch)
     if (how.greedy || !(top > -INFINITY) || top == INFINITY || (how.limit_k && !how.by_groups)) return;
     const Row<kKind> row(a, m);
@@ -503,59 +553,42 @@ __global__ __launch_bounds__(kPieceThreads) void piece_sum_kernel(const SampleAr
     const int end = row.start(base + row.piece()), i0 = row.start(base + (int64_t)w * part);
     const int from = i0 < end ? i0 : end, to = end - from < part ? end : from + part;
     if (how.by_groups) {
-        if (rank_of(keys, kGroups, tid) == how.k - 1) bound = reinterpret_cast<uint32_t*>(keys)[tid];
-        __syncthreads();
-        const int n = row.gather(from, to, L::value(bound), NAN, list.key[w], list.index[w], kRoom, 0);
+        const uint32_t keys[4] = {L::key(groups[0]), L::key(groups[1]), L::key(groups[2]), L::key(groups[3])};
+        const int n = row.gather(from, to, L::value(kth_of<L::kBits>(keys, how.k)), NAN, list.key[w], list.index[w], kRoom, 0);
         if (lane == 0) list.n[w] = n;
         leave_list(list, a.left[m], c);
         return;
     }
     const Weight weight(top, how.t);
     const double unit = (double)(1ull << a.unit_shift);
-    mass[tid] = 0ull;
+    for (int b = tid; b < kBins; b += kPieceThreads) mass[b] = 0ull;
     __syncthreads();
-    double sum = 0.0;
-    row.stroll(from, to, [&](const auto& r, int) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const double x = weight.octaves(L::at(r, e)), v = weight.power(x);
-            if (how.by_bins) {
-                sum += v;
-                if (x > -(double)(kBins / kBinsPerOctave)) atomicAdd(&mass[bin_of(x)], (unsigned long long)fixed_point(v, unit));
-            } else {
-                sum += v >= how.min_w ? v : 0.0;
-            }
-        }
-    });
-    sum = wave_sum(sum);
+    double sum = wave_sum(row.sum_of(from, to, weight, how, unit, mass));
     if (lane == 0) wave_part[w] = sum;
     __syncthreads();
     if (tid == 0) a.left[m].sum[c] = wave_part[0] + wave_part[1] + wave_part[2] + wave_part[3];
-    if (how.by_bins) a.left[m].mass[c][tid] = mass[tid];
+    if (how.by_bins)
+        for (int b = tid; b < kBins; b += kPieceThreads)
+            if (mass[b]) atomicAdd(&a.left[m].mass[b], mass[b]);
 }
 
 template <int kKind>
 __global__ __launch_bounds__(kPieceThreads) void piece_cut_kernel(const SampleArgs a) {
-    __shared__ uint4 keys[kGroups / 4];
-    __shared__ float wave_top[4];
     __shared__ double wave_part[4][2];
     __shared__ unsigned long long mass[kBins];
     __shared__ int bins[2];
     __shared__ PieceList list;
-    using L = Logit<kKind>;
     const int m = (int)blockIdx.x / kPieces, c = (int)blockIdx.x % kPieces, tid = (int)threadIdx.x, w = tid >> 6, lane = tid & 63;
     const How how(a, m);
     if (how.greedy || !how.by_bins) return;
     Left& left = a.left[m];
-    uint64_t own = 0;
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) own += left.mass[k][tid];
+    const f32x4 groups = reinterpret_cast<const f32x4*>(left.group_max)[lane];
+    for (int b = tid; b < kBins; b += kPieceThreads) mass[b] = left.mass[b];
     double whole = 0.0;
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) whole += left.sum[k];
-    const float top = top_of<kKind>(left, keys, wave_top);
+    const float top = wave_max(fmaxf(fmaxf(groups[0], groups[1]), fmaxf(groups[2], groups[3])));
     if (!(top > -INFINITY) || top == INFINITY) return;
-    mass[tid] = own;
     __syncthreads();
     const double unit = (double)(1ull << a.unit_shift);
     if (w == 0) find_bins(mass, how.p * whole * unit, bins);
@@ -573,23 +606,10 @@ __global__ __launch_bounds__(kPieceThreads) void piece_cut_kernel(const SampleAr
     // what may be cut, and what surely is not
     const float low = bin_end(weight, bins[1], 1e-6), high = bins[0] > 0 ? bin_end(weight, bins[0] - 1, -1e-6) : INFINITY;
     const int n = row.gather(from, to, low, high, list.key[w], list.index[w], kRoom, 0);
-    if (lane == 0) list.n[w] = n;
-    double above = 0.0, above_kept = 0.0;
-    row.stroll(from, to, [&](const auto& r, int) {
-        float most = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) most = fmaxf(most, L::at(r, e));
-        if (__ballot(most >= high) == 0) return;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const double v = L::at(r, e) >= high ? weight(L::at(r, e)) : 0.0;
-            above += v;
-            above_kept += v >= how.min_w ? v : 0.0;
-        }
-    });
-    above = wave_sum(above);
-    above_kept = wave_sum(above_kept);
+    double above, above_kept;
+    row.sum_above(from, to, high, weight, how.min_w, &above, &above_kept);
     if (lane == 0) {
+        list.n[w] = n;
         wave_part[w][0] = above;
         wave_part[w][1] = above_kept;
     }
@@ -627,8 +647,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
             for (int e = 0; e < kVec; ++e) mine = fmaxf(mine, L::at(r, e));
         });
     }
-    float top = mine;
-    for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+    float top = wave_max(mine);
     if (lane == 0) sh.part[wv] = (double)top;
     __syncthreads();
     for (int k = 0; k < kWaves; ++k) top = fmaxf(top, (float)sh.part[k]);
@@ -704,9 +723,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
                 most = fmaxf(most, __shfl_xor(most, 2));
                 if ((lane & 3) == 0) reinterpret_cast<uint32_t*>(sh.short_key)[tid >> 2] = L::key(most);
                 __syncthreads();
-                if (tid < kGroups && rank_of(sh.short_key, kGroups, tid) == how.k - 1) sh.box[0] = (int)reinterpret_cast<uint32_t*>(sh.short_key)[tid];
-                __syncthreads();
-                bound = (uint32_t)sh.box[0];
+                const uint4 q = sh.short_key[lane];
+                const uint32_t keys[4] = {q.x, q.y, q.z, q.w};
+                bound = kth_of<L::kBits>(keys, how.k);
             } else {
                 if constexpr (kLeft) {
                     mine = -INFINITY;
@@ -741,22 +760,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
             }
             for (int k = 0; k < kPieces; ++k) whole += sh.part[k];
         } else {
-            if (tid < kBins) sh.mass[tid] = 0ull;
+            sh.mass[tid] = 0ull;
             __syncthreads();
-            double sum = 0.0;
-            row.stroll(from, to, [&](const Eight& r, int) {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const double x = weight.octaves(L::at(r, e)), v = weight.power(x);
-                    if (how.by_bins) {
-                        sum += v;
-                        if (x > -(double)(kBins / kBinsPerOctave)) atomicAdd(&sh.mass[bin_of(x)], (unsigned long long)fixed(v));
-                    } else {
-                        sum += v >= min_w ? v : 0.0;
-                    }
-                }
-            });
-            whole = sums_of_waves(sum, sh.part);
+            whole = sums_of_waves(row.sum_of(from, to, weight, how, unit, sh.mass), sh.part);
             summed = true;
             if (how.by_bins) {
                 if (wv == 0) find_bins(sh.mass, how.p * whole * unit, sh.box);
@@ -767,21 +773,11 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
                     const float low = bin_end(weight, last, 1e-6), high = first > 0 ? bin_end(weight, first - 1, -1e-6) : INFINITY;
                     listed = summed = lists_fit(row.gather(from, to, low, high, sh.key[wv], sh.index[wv], kRoom, 0));
                     double above = 0.0, above_kept = 0.0;
-                    if (listed)
-                        row.stroll(from, to, [&](const Eight& r, int) {
-                            float most = -INFINITY;
-#pragma unroll
-                            for (int e = 0; e < kVec; ++e) most = fmaxf(most, L::at(r, e));
-                            if (__ballot(most >= high) == 0) return;
-#pragma unroll
-                            for (int e = 0; e < kVec; ++e) {
-                                const double v = L::at(r, e) >= high ? weight(L::at(r, e)) : 0.0;
-                                above += v;
-                                above_kept += v >= min_w ? v : 0.0;
-                            }
-                        });
-                    sums_of_waves(above, sh.above);
-                    sums_of_waves(above_kept, sh.above_kept);
+                    if (listed) row.sum_above(from, to, high, weight, min_w, &above, &above_kept);
+                    if (lane == 0) {
+                        sh.above[wv] = above;
+                        sh.above_kept[wv] = above_kept;
+                    }
                 }
             }
         }
@@ -1006,13 +1002,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
 
     // ---- thresholds over the row itself
     if (!cut_found) {
-        auto each = [&](auto f) {
-            row.stroll(from, to, [&](const Eight& r, int i) {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e)
-                    if (i + e < to) f(L::at(r, e));
-            });
-        };
+        auto each = [&](auto f) { row.each(from, to, [&](float z, int) { f(z); }); };
         if (how.limit_k) find_count<L>(sh, [&](auto f) { each([&](float z) { f(L::key(z)); }); }, how.k, &cut, &ties);
         if (how.limit_p) {
             const uint32_t kcut = cut;
@@ -1079,10 +1069,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     // target, until one is a step of a wave
     if (!summed) {
         double sum = 0.0;
-        row.stroll(from, to, [&](const Eight& r, int i) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) sum += i + e < to ? kept(L::at(r, e), i + e) : 0.0;
-        });
+        row.each(from, to, [&](float z, int i) { sum += kept(z, i); });
         sums_of_waves(sum, sh.part);
     } else if (how.by_bins) {
         // what is surely kept, and what of the list is
@@ -1130,42 +1117,32 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
         const int64_t b64 = (int64_t)i0 + (int64_t)wv * size;
         const int b = b64 < i1 ? (int)b64 : i1, e1 = i1 - b < size ? i1 : b + size;
         double sum = 0.0;
-        row.stroll(b, e1, [&](const Eight& r, int i) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) sum += i + e < e1 ? kept(L::at(r, e), i + e) : 0.0;
-        });
+        row.each(b, e1, [&](float z, int i) { sum += kept(z, i); });
         sums_of_waves(sum, sh.part);
     }
-    if (wv != 0) return;
-    const int i = i0 + kVec * lane;
-    const Eight r = L::load(row.p, i, i1, row.aligned);
-    double w[kVec], own = 0.0, all;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-        w[e] = i + e < i1 ? kept(L::at(r, e), i + e) : 0.0;
-        own += w[e];
-    }
-    double at = run + wave_before(own, &all);
-    int hit = kNone, last_kept = -1;
-    double hit_w = 0.0, last_w = 0.0;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-        at += w[e];
-        if (w[e] > 0.0) {
-            if (hit == kNone && at > target) {
-                hit = i + e;
-                hit_w = w[e];
+    // the step's eight times 64, a logit a lane: the wave that has it answers
+    const int i = i0 + tid;
+    const double w = tid < kStep && i < i1 ? kept(L::one(row.p, i), i) : 0.0;
+    double all;
+    const double low = wave_before(w, &all);
+    __syncthreads();
+    if (lane == 0) sh.part[wv] = all;
+    __syncthreads();
+    int wave = -1, fallback = 0;
+    double at = run, before = 0.0;
+    for (int k = 0; k < kStep / 64; ++k) {
+        if (sh.part[k] > 0.0) {
+            fallback = k;
+            if (exact && wave < 0 && at + sh.part[k] > target) {
+                wave = k;
+                before = at;
             }
-            last_kept = i + e;
-            last_w = w[e];
         }
+        at += sh.part[k];
     }
-    const uint64_t over = exact ? __ballot(hit != kNone) : 0, some = __ballot(last_kept >= 0);
-    if (over) {
-        if (lane == __builtin_ctzll(over)) answer(hit, hit_w, total);
-    } else if (some && lane == 63 - __builtin_clzll(some)) {
-        answer(last_kept, last_w, total);
-    }
+    if (wv != (wave < 0 ? fallback : wave)) return;
+    const uint64_t over = wave >= 0 ? __ballot(w > 0.0 && before + low + w > target) : 0, some = __ballot(w > 0.0);
+    if (lane == (over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some))) answer(i, w, total);
 }
 
 template <int kKind>
