@@ -33,7 +33,8 @@ def check(w, x, router, T, **how):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("M,K,E,T", [(1, 128, 1, 1), (1, 2048, 64, 8), (3, 384, 5, 5), (13, 2048, 60, 4), (16, 1024, 128, 8),
-                                     (127, 256, 64, 2), (129, 128, 8, 2), (300, 640, 17, 3), (5, 256, 1000, 32), (2, 128, 1024, 32)])
+                                     (127, 256, 64, 2), (129, 128, 8, 2), (300, 640, 17, 3), (5, 256, 1000, 32), (2, 128, 1024, 32),
+                                     (65, 160 * 8, 250, 9), (512, 384, 130, 8), (40, 128, 1023, 4)])
 def test_route(w, M, K, E, T, dtype):
     x, router, bias = make(M + K + E, M, K, E, dtype)
     check(w, x, router, T)
