@@ -141,13 +141,23 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const MoeArgs a) {
 
     const int id = tid < M * a.T ? a.ids[tid] : -1;
     if (tid < M * a.T) entry_weight[tid] = a.weights[tid];
-    // rows past M are left as they are: they feed results that are not used
+    // the rows' 16-byte chunks, chunk by chunk, a row each in turn; rows past M are left as they
+    // are: they feed results that are not used
     {
-        const int m = tid & 15;
-        const uint16_t* xr = a.x + (size_t)m * a.K;
-        if (m < M)
-            for (int q = tid >> 4; q < a.K / 8; q += kThreads / 16)
-                xs[(q >> 2) * 64 + 16 * (q & 3) + m] = *reinterpret_cast<const uint4*>(xr + 8 * q);
+        const int chunks = M * (a.K / 8);
+        for (int t0 = tid; t0 < chunks; t0 += 4 * kThreads) {
+            uint4 v[4];
+            int to[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = t0 + j * kThreads < chunks ? t0 + j * kThreads : chunks - 1;
+                const int q = t / M, m = t - q * M;
+                to[j] = (q >> 2) * 64 + 16 * (q & 3) + m;
+                v[j] = *reinterpret_cast<const uint4*>(a.x + (size_t)m * a.K + 8 * q);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xs[to[j]] = v[j];
+        }
     }
     int place;
     const int listed = make_list(a, list, id, &place);

@@ -257,8 +257,10 @@ template <int kKind> struct Row {
     __device__ __forceinline__ void each(int i0, int i1, F f) const {
         stroll(i0, i1, [&](Eight q, int i) {
 #pragma unroll 1
-            for (int e = 0; e < kVec; ++e) {
+            for (int e = 0; e < kVec; e += 2) {
                 if (i + e < i1) f(L::at(q, 0), i + e);
+                if (i + e + 1 < i1) f(L::at(q, 1), i + e + 1);
+                L::next(q);
                 L::next(q);
             }
         });
@@ -299,12 +301,11 @@ template <int kKind> struct Row {
 #pragma unroll
             for (int e = 0; e < kVec; ++e) most = fmaxf(most, L::at(r, e));
             if (__ballot(most >= high) == 0) return;
-#pragma unroll 1
+#pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                const double v = L::at(r, 0) >= high ? weight(L::at(r, 0)) : 0.0;
+                const double w = weight.power(weight.octaves(L::at(r, e))), v = L::at(r, e) >= high ? w : 0.0;
                 all += v;
                 some += v >= min_w ? v : 0.0;
-                L::next(r);
             }
         });
         *above = wave_sum(all);
@@ -483,18 +484,31 @@ __device__ __forceinline__ void find_bins(const unsigned long long* mass, double
 #pragma unroll
     for (int j = 0; j < kEach; ++j) own += mass[kEach * lane + j];
     const uint64_t above = wave_before(own, &all);
-    if (lane == 0) bins[0] = bins[1] = -1;
-    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const double at = fmax(side ? want * (1.0 + 1e-9) : want * (1.0 - 1e-9), 1.0);
-        if ((double)above < at && (double)(above + own) >= at) {
-            uint64_t sum = above;
-            int b = kEach * lane;
-            while ((double)(sum + mass[b]) < at) sum += mass[b++];
-            bins[side] = b;
+        const uint64_t hit = __ballot((double)above < at && (double)(above + own) >= at);
+        int bin = -1;
+        if (hit) {
+            const int from = __builtin_ctzll(hit);           // the lane whose bins hold it: one of them a lane
+            const uint64_t one = lane < kEach ? mass[kEach * from + lane] : 0, low = from_lane(above, from) + wave_before(one, &all);
+            bin = kEach * from + __builtin_ctzll(__ballot((double)(low + one) >= at));
         }
+        if (lane == 0) bins[side] = bin;
     }
+}
+
+// The part, of n <= 64, in which the running sum from `run` on exceeds the target, and what lies before it; where
+// none does (rounding, or not asked for: !exact) the last that is not 0, and exact becomes false.
+__device__ __forceinline__ int pick_part(const double* part, int n, double target, double* run, bool* exact) {
+    const int lane = (int)threadIdx.x & 63;
+    double own = lane < n ? part[lane] : 0.0, all;
+    const double low = *run + wave_before(own, &all);
+    const uint64_t some = __ballot(own > 0.0), over = *exact ? __ballot(own > 0.0 && low + own > target) : 0;
+    if (!over) *exact = false;
+    const int at = over ? __builtin_ctzll(over) : some ? 63 - __builtin_clzll(some) : 0;
+    *run = from_lane(low, at);
+    return at;
 }
 
 // ---- few rows: a workgroup of 4 waves a piece
@@ -958,20 +972,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
             const double total = sums_of_waves(sum, sh.part);
             const double target = share * total;
             // the wave in which the running sum exceeds the target, or the last that keeps any
-            int wave = -1, fallback = 0;
-            double run = 0.0, before = 0.0;
-            for (int k = 0; k < kWaves; ++k) {
-                if (sh.part[k] > 0.0) {
-                    fallback = k;
-                    if (!last_of_all && wave < 0 && run + sh.part[k] > target) {
-                        wave = k;
-                        before = run;
-                    }
-                }
-                run += sh.part[k];
-            }
-            const bool exact = wave >= 0;
-            if (!exact) wave = fallback;
+            bool exact = !last_of_all;
+            double before = 0.0;
+            const int wave = pick_part(sh.part, kWaves, target, &before, &exact);
             if (wv != wave) return;
             int last_id = -1;
             double at = before, last_w = 0.0;
@@ -1090,25 +1093,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     double run = 0.0;
     bool exact = !last_of_all;
     for (int size = piece;;) {
-        int wave = -1, fallback = 0;
-        double at = run, before = run, before_last = run;
-        for (int k = 0; k < kWaves; ++k) {
-            if (sh.part[k] > 0.0) {
-                fallback = k;
-                before_last = at;
-                if (exact && wave < 0 && at + sh.part[k] > target) {
-                    wave = k;
-                    before = at;
-                }
-            }
-            at += sh.part[k];
-        }
-        if (wave < 0) {
-            exact = false;                       // (rounding, or u of 1) the last that is kept
-            wave = fallback;
-            before = before_last;
-        }
-        run = before;
+        const int wave = pick_part(sh.part, kPieces, target, &run, &exact);
         const int64_t n0 = (int64_t)i0 + (int64_t)wave * size;
         i1 = i1 - n0 < size ? i1 : (int)n0 + size;
         i0 = (int)n0;
@@ -1128,20 +1113,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     __syncthreads();
     if (lane == 0) sh.part[wv] = all;
     __syncthreads();
-    int wave = -1, fallback = 0;
-    double at = run, before = 0.0;
-    for (int k = 0; k < kStep / 64; ++k) {
-        if (sh.part[k] > 0.0) {
-            fallback = k;
-            if (exact && wave < 0 && at + sh.part[k] > target) {
-                wave = k;
-                before = at;
-            }
-        }
-        at += sh.part[k];
-    }
-    if (wv != (wave < 0 ? fallback : wave)) return;
-    const uint64_t over = wave >= 0 ? __ballot(w > 0.0 && before + low + w > target) : 0, some = __ballot(w > 0.0);
+    if (wv != pick_part(sh.part, kStep / 64, target, &run, &exact)) return;
+    const uint64_t over = exact ? __ballot(w > 0.0 && run + low + w > target) : 0, some = __ballot(w > 0.0);
     if (lane == (over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some))) answer(i, w, total);
 }
 
