@@ -14,7 +14,9 @@
 //   3. top-p alone: the logits of the 32nd in which p is reached are listed, those above it summed;
 //   4. the draw: the piece whose sum of kept w holds the target, its sixteenth, and so on.
 // A few rows take 16 workgroups each, in a launch for each of these; many rows one workgroup each,
-// a wave a piece, in one launch. What the lists do not hold (top-k over 1024, lists of more than 512
+// a wave a piece, in one launch. Bound by latency (a few rows: three or four launches of 3 to 10 us whose
+// steps wait for each other) and by the vector units (many rows: 256 x 131072 in 45 us, 1.5 TB/s, 25 fp64
+// instructions a logit). What the lists do not hold (top-k over 1024, lists of more than 512
 // in a piece) is found over the row itself.
 //
 // Logits are compared as whole numbers (order-preserving keys). Lists of up to 256 are sorted by
@@ -1133,8 +1135,12 @@ void launch_kind(const SampleArgs& a, hipStream_t s) {
     }
 }
 
-// Rows that leave most of the chip idle with a workgroup each, where they are long enough to be worth the launches.
-bool in_pieces(int64_t M, int64_t V) { return M <= 64 && V >= 16384; }
+// Pieces where one workgroup a row would leave most of the chip idle and the row is long enough to be worth the
+// launches. Both ways, us, bf16 (pieces / a workgroup a row), without limits, top-k 50 with top-p 0.9, top-p 0.95:
+//   1 x 131072    18 / 36    18 / 24    37 / 108        64 x 131072   23 / 38    24 / 27    58 / 111
+//   128 x 131072  32 / 38    30 / 27    83 / 112        16 x 32768    18 / 15    19 / 19    34 / 44
+//   64 x 16384    18 / 13    21 / 18    38 / 32         192 x 131072  44 / 44    38 / 32    111 / 119
+bool in_pieces(int64_t M, int64_t V) { return V > 24576 && (M <= 64 || (M <= 128 && V >= 65536)); }
 
 }  // namespace
 
@@ -1161,7 +1167,9 @@ hipError_t launch_sample(const SampleCall& q, void* scratch, hipStream_t stream)
     a.ids = q.ids;
     a.logprob = q.logprob;
     a.aligned = (reinterpret_cast<uintptr_t>(q.logits) & 15) == 0 && (q.ld * (q.kind == 2 ? 4 : 2)) % 16 == 0;
-    a.left = in_pieces(q.M, q.V) ? static_cast<Left*>(scratch) : nullptr;
+    // (the largest logit alone is found faster by one launch: 15 us against 18)
+    const bool greedy = !q.temperatures && !(q.temperature > 0.f);
+    a.left = in_pieces(q.M, q.V) && !greedy ? static_cast<Left*>(scratch) : nullptr;
     if (q.kind == 0) launch_kind<0>(a, stream);
     else if (q.kind == 1) launch_kind<1>(a, stream);
     else launch_kind<2>(a, stream);
