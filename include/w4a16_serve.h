@@ -112,7 +112,7 @@ typedef struct {
  * all others. A row with nothing to draw gives id -1, logprob -infinity. u below 0 (or no
  * number) counts as 0, 1 and above draws the last token kept.
  *   logits  [M, V], `type`, row m at logits + m * row_stride elements (row_stride >= V), aligned
- *           to its element; read only. Rows on 16-byte boundaries are read faster.
+ *           to its element; read only.
  * 1 <= V <= 2^28. Weights and their sums are in fp64; top_p's sums in 64-bit fixed point, a
  * step of 2^-62 V (V rounded up to a power of two; at least 2^-51) of the largest weight. */
 size_t w4a16_sample_workspace_bytes(int64_t M, int64_t V);

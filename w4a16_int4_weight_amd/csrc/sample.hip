@@ -69,7 +69,6 @@ struct SampleArgs {
     const float* min_ps;
     int32_t* ids;
     float* logprob;
-    int aligned;            // rows on 16-byte boundaries
     Left* left;             // [M], or NULL: one workgroup a row
 };
 
@@ -102,16 +101,13 @@ template <int kKind> struct Logit {
         uint4 q[kKind == 2 ? 2 : 1];
     };
     // logits i .. i + 7; past the end -infinity
-    static __device__ __forceinline__ Eight load(const void* row, int i, int V, bool aligned) {
+    static __device__ __forceinline__ Eight load(const void* row, int i, int V) {
         Eight r;
-        if (aligned && i + kVec <= V) {
-            if constexpr (kKind == 2) {
-                const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + i);
-                r.q[0] = p[0];
-                r.q[1] = p[1];
-            } else {
-                r.q[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
-            }
+        if (i + kVec <= V) {
+            // (rows may begin anywhere: one load of 16 bytes either way)
+            const char* from = static_cast<const char*>(row) + (size_t)i * (kKind == 2 ? 4 : 2);
+            __builtin_memcpy(&r.q[0], from, 16);
+            if constexpr (kKind == 2) __builtin_memcpy(&r.q[1], from + 16, 16);
         } else {
             // (rolled: it is in every loop over the row, and rarely taken)
             const uint32_t none = kKind == 2 ? 0xFF800000u : kKind == 1 ? 0xFF80FF80u : 0xFC00FC00u;
@@ -217,12 +213,10 @@ template <int kKind> struct Row {
     using Eight = typename L::Eight;
     const void* p;
     int V, lane;
-    bool aligned;
     __device__ __forceinline__ Row(const SampleArgs& a, int m) {
         p = static_cast<const uint8_t*>(a.logits) + (int64_t)m * a.ld * (kKind == 2 ? 4 : 2);
         V = a.V;
         lane = (int)threadIdx.x & 63;
-        aligned = a.aligned != 0;
     }
     // logits of a piece, and of the part of it that one of `parts` waves takes
     __device__ __forceinline__ int piece() const { return (int)(((int64_t)V + kPieces * kStep - 1) / (kPieces * kStep)) * kStep; }
@@ -233,7 +227,7 @@ template <int kKind> struct Row {
         for (int i = i0 + kVec * lane; i - kVec * lane < i1; i += kAhead * kStep) {
             Eight r[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) r[j] = L::load(p, i + j * kStep, i1, aligned);
+            for (int j = 0; j < kAhead; ++j) r[j] = L::load(p, i + j * kStep, i1);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) f(r[j], i + j * kStep);
         }
@@ -244,7 +238,7 @@ template <int kKind> struct Row {
         for (int i = i0; i < i1; i += 4 * kStep) {
             Eight r[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = L::load(p, i + j * kStep + kVec * lane, i1, aligned);
+            for (int j = 0; j < 4; ++j) r[j] = L::load(p, i + j * kStep + kVec * lane, i1);
 #pragma unroll 1
             for (int j = 0; j < 4 && i + j * kStep < i1; ++j) {
                 f(r[0], i + j * kStep + kVec * lane);
@@ -1166,7 +1160,6 @@ hipError_t launch_sample(const SampleCall& q, void* scratch, hipStream_t stream)
     a.min_ps = q.min_ps;
     a.ids = q.ids;
     a.logprob = q.logprob;
-    a.aligned = (reinterpret_cast<uintptr_t>(q.logits) & 15) == 0 && (q.ld * (q.kind == 2 ? 4 : 2)) % 16 == 0;
     // (the largest logit alone is found faster by one launch: 15 us against 18)
     const bool greedy = !q.temperatures && !(q.temperature > 0.f);
     a.left = in_pieces(q.M, q.V) && !greedy ? static_cast<Left*>(scratch) : nullptr;
