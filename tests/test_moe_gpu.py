@@ -158,3 +158,20 @@ def test_large_values_keep_their_range(w):
 def test_more_rows_than_a_pass(w):
     ex = experts(w, 3, 128, 128, "bf16", 128)
     run(w, ex, 2 * 512 + 5, 32)        # 16384 / 32 rows a pass
+
+
+@pytest.mark.parametrize("M", [2, 16, 40])
+def test_experts_past_32_bits_of_bytes(w, M):
+    """Experts whose offsets pass 4 GiB."""
+    ex = su.Experts(w, 700, 3, 256, 128, "bf16", 128)
+    stride = 3 << 30
+
+    def spread(packed):
+        n = packed.shape[1]
+        far = torch.empty(2 * stride + n, dtype=torch.uint8, device=DEV).as_strided((3, n), (stride, 1))
+        far.copy_(packed)
+        return far
+    ids, weights = entries(3, M, 3, 2)
+    x, x64 = tu.normal(4, (M, 256), "bf16")
+    y = w.w4a16_moe(x, ids, weights, spread(ex.gate_up), spread(ex.down_packed), ex.F, ex.G)
+    su.check_moe(y, su.moe(ex, x64, ids, weights.double()), "bf16")

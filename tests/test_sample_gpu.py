@@ -140,6 +140,30 @@ def test_numbers_at_the_ends(w, V):
         check(w, z, u, **s)
 
 
+@pytest.mark.parametrize("M,V", [(4, 3001), (3, 40000), (70, 26000)])
+def test_extreme_temperatures_and_logits(w, M, V):
+    z, u = make(V, M, V, "fp32")
+    for t in (1e-42, 1e-20, 1e-3, 1e4, 1e30, math.inf, math.nan, -1.0):
+        for how in (dict(), dict(p=0.6), dict(k=30, p=0.6)):
+            check(w, z, u, t=t, **how)
+    for lift in (1e4, -3e38):
+        far = (z + lift).clamp(min=-3.4e38)
+        for how in (dict(), dict(p=0.9), dict(k=30), dict(min_p=0.1)):
+            check(w, far, u, **how)
+
+
+@pytest.mark.parametrize("p", [0.5, 0.999, 1.0 - 2.0 ** -24, 2.0 ** -149])
+@pytest.mark.parametrize("M,V", [(2, 40000), (2, 9000), (90, 24580)])
+def test_top_p_at_its_ends(w, M, V, p):
+    """Weights that all lie far below the largest count in the sum that p is reached in."""
+    z = torch.full((M, V), -26.0, device=DEV)
+    z[:, V // 3] = 0.0
+    z[:, V // 2:V // 2 + 7] = -1.0
+    check(w, z, torch.rand((M,), generator=torch.Generator().manual_seed(1)).to(DEV), p=p)
+    z, u = make(V, M, V, "fp32", spread=6.0)
+    check(w, z, u, p=p)
+
+
 def test_every_token_by_its_share(w):
     """u on a grid: each token as often as its weight says."""
     z = torch.tensor([[0.0, math.log(3.0), -math.inf, math.log(4.0)]], device=DEV).expand(800, 4)

@@ -915,7 +915,7 @@ def w4a16_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=
             settings[name] = value
             setattr(how, name + "s", value.data_ptr())
         else:
-            setattr(how, name, value)
+            setattr(how, name, value if dtype is torch.float32 else max(min(value, 2 ** 31 - 1), 0))
     ids = _result(ids, "ids", (M,), torch.int32, logits.device)
     logprob = _result(logprob, "logprob", (M,), torch.float32, logits.device)
     _beside(logits, u=u, ids=ids, logprob=logprob, workspace=workspace, **settings)

@@ -55,6 +55,8 @@ struct Left {
     int index[kPieces][kRoom];
 };
 
+static_assert(sizeof(Left) % 16 == 0, "read 16 bytes at a time");
+
 struct SampleArgs {
     const void* logits;
     int64_t ld;
@@ -470,10 +472,10 @@ __device__ __forceinline__ void find_mass(Shared& sh, Each each, double target, 
     *there = sh.box[1];
 }
 
-// The bins, the likeliest first, in which the weights reach p of the whole: with sums of fixed-point
-// steps, up to what the whole's rounding may be off on either side. bins[0]: the first that may be it, [1]: the last;
-// [1] is -1 where the bins do not reach it. For the first wave; mass is in LDS.
-__device__ __forceinline__ void find_bins(const unsigned long long* mass, double want, int* bins) {
+// The bins, the likeliest first, in which the weights reach `want` steps: on either side by what the bins' sums of V
+// weights in whole steps, half a step each, and the whole's own rounding may be off. bins[0]: the first that may be it,
+// [1]: the last; -1 where the bins do not reach it. For the first wave; mass is in LDS.
+__device__ __forceinline__ void find_bins(const unsigned long long* mass, double want, int V, int* bins) {
     const int lane = (int)threadIdx.x & 63;
     constexpr int kEach = kBins / 64;
     uint64_t own = 0, all;
@@ -482,7 +484,7 @@ __device__ __forceinline__ void find_bins(const unsigned long long* mass, double
     const uint64_t above = wave_before(own, &all);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-        const double at = fmax(side ? want * (1.0 + 1e-9) : want * (1.0 - 1e-9), 1.0);
+        const double off = want * 1e-12 + (double)V, at = fmax(side ? want + off : want - off, 1.0);
         const uint64_t hit = __ballot((double)above < at && (double)(above + own) >= at);
         int bin = -1;
         if (hit) {
@@ -601,7 +603,7 @@ __global__ __launch_bounds__(kPieceThreads) void piece_cut_kernel(const SampleAr
     if (!(top > -INFINITY) || top == INFINITY) return;
     __syncthreads();
     const double unit = (double)(1ull << a.unit_shift);
-    if (w == 0) find_bins(mass, how.p * whole * unit, bins);
+    if (w == 0) find_bins(mass, how.p * whole * unit, a.V, bins);
     __syncthreads();
     if (bins[0] < 0 || bins[1] < 0) {
         if (tid == 0) left.listed[c] = kRoom + 1;              // over the row itself
@@ -775,7 +777,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
             whole = sums_of_waves(row.sum_of(from, to, weight, how, unit, sh.mass), sh.part);
             summed = true;
             if (how.by_bins) {
-                if (wv == 0) find_bins(sh.mass, how.p * whole * unit, sh.box);
+                if (wv == 0) find_bins(sh.mass, how.p * whole * unit, a.V, sh.box);
                 __syncthreads();
                 const int first = sh.box[0], last = sh.box[1];
                 summed = first >= 0 && last >= 0;
