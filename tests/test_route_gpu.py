@@ -54,6 +54,16 @@ def test_ties_go_to_the_lowest_expert(w):
     assert torch.equal(weights, torch.full_like(weights, float(torch.tensor(1 / 6, dtype=torch.float64))))
 
 
+@pytest.mark.parametrize("M,E", [(3, 20), (130, 80)])
+def test_products_beyond_fp32(w, M, E):
+    """bf16 values whose products lie outside fp32's range, on either side."""
+    x, router, _ = make(8, M, 256, E, "bf16")
+    check(w, (x.float() * 1e25).bfloat16(), (router.float() * 1e25).bfloat16(), 4, normalize=False)
+    ids, _ = w.w4a16_route((x.float() * 1e-30).bfloat16(), (router.float() * 1e-30).bfloat16(), 4)
+    want, _ = su.route((x.float() * 1e-30).bfloat16().double(), (router.float() * 1e-30).bfloat16().double(), 4)
+    assert torch.equal(ids.long(), want)
+
+
 def test_rows_of_no_numbers_still_choose(w):
     x, router, _ = make(4, 4, 128, 12, "bf16")
     x[1] = float("nan")

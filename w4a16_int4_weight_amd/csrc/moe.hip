@@ -22,6 +22,12 @@
 //
 // Per metadata unit: s (T - (16 + z) X), T = sum x (16 + q), as product_small.hip has it; fp16
 // activations take q - z exactly in 16 bits.
+//
+// Measured (2048 x 1024, 64 experts, 8 a row): one row 10.0 + 8.4 us, of which a launch takes 1.5,
+// the ids and their list 2, the first codes 2 to 3 (16.8 and 8.4 MB), and the splits' meeting 2.3;
+// 16 rows 31 us for 132 MB (4.2 TB/s; with the loads alone 31 too) and 24 us for 66 MB. A barrier a batch
+// of units, as product_small.hip has it, took 39 us for up_kernel at 16 rows; two workgroups a compute unit
+// 48 (up) and 30 us (down); 8 columns a down workgroup and no splits 50 us.
 #include "device_common.h"
 #include "gate.h"
 #include "launch.h"

@@ -11,6 +11,11 @@
 // the others, so that one pass over the codes serves both, to fp32 rows of pairs; and each
 // row's sum over its pairs in their order. No atomics on results: they do not depend on timing.
 // The products are tile_product.h's.
+//
+// Measured (2048 x 1024, 64 experts, 8 a row): 77 rows 5 + 56 + 51 + 7 us (143 and 67 MB of codes: 2.5 and 1.3
+// TB/s; 75 tiles of 8 column tiles are a round and a bit of two workgroups a compute unit), 512 rows 10 + 115 + 99
+// + 9 us (64-row tiles, half the experts with a second one; 300 and, each half by itself, 350 TFLOP/s). A ring of 4
+// stages: the same at 64 rows, 74 instead of 56 us at 16. Tiles of 32 rows for 512: 138 and 99 us.
 #include "device_common.h"
 #include "gate.h"
 #include "launch.h"
@@ -254,7 +259,7 @@ void launch_typed(const MoeCall& q, int mr, int sub, MoeTileArgs& up, MoeTileArg
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Rows of a tile (pairs of one expert): 16, 32 or 64, the least that holds the rows an expert
-// meets on average (the 128-row tile of the down projection's halves does not fit in LDS with
+// meets on average (77 rows of 8: tiles of 16 56 us, of 32 69; 512 rows: 64 115, 32 138, 16 145) (the 128-row tile of the down projection's halves does not fit in LDS with
 // finer groups than 128).
 int tile_mr(int64_t M, int64_t E, int64_t T, int64_t G) {
     const int64_t each = M * T / (E < M * T ? E : M * T);
