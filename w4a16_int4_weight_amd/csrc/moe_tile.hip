@@ -12,10 +12,11 @@
 // row's sum over its pairs in their order. No atomics on results: they do not depend on timing.
 // The products are tile_product.h's.
 //
-// Measured (2048 x 1024, 64 experts, 8 a row): 77 rows 5 + 56 + 51 + 7 us (143 and 67 MB of codes: 2.5 and 1.3
-// TB/s; 75 tiles of 8 column tiles are a round and a bit of two workgroups a compute unit), 512 rows 10 + 115 + 99
-// + 9 us (64-row tiles, half the experts with a second one; 300 and, each half by itself, 350 TFLOP/s). A ring of 4
-// stages: the same at 64 rows, 74 instead of 56 us at 16. Tiles of 32 rows for 512: 138 and 99 us.
+// Measured (2048 x 1024, 64 experts, 8 a row): 77 rows 5 + 56 + 51 + 5 us (143 and 67 MB of codes: 2.5 and 1.3
+// TB/s; 75 tiles of 8 column tiles are a round and a bit of two workgroups a compute unit), 512 rows 6 + 115 + 99
+// + 7 us (64-row tiles, half the experts with a second one; 300 and, each half by itself, 350 TFLOP/s). A ring of 4
+// stages: the same at 64 rows, 74 instead of 56 us at 16. Tiles of 32 rows for 512: 138 and 99 us,
+// of 128 for the first product 127; tiles that begin at different row blocks: the same.
 #include "device_common.h"
 #include "gate.h"
 #include "launch.h"
@@ -24,7 +25,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kListThreads = 256;
+constexpr int kListThreads = 1024;
 
 // Expert e's tiles take the slots from floor(pairs of lower experts / rows of a tile) + e on:
 // at least as many as it has tiles, so that no expert waits for another's count; the last
@@ -213,17 +214,30 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ out
     const int64_t m = q / per;
     const int n = (int)(q % per) * 8;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < T; ++j) {
-        const int id = ids[m * T + j];
-        if (id < 0 || id >= E) continue;                    // none: its row of `out` is not written
-        const float wt = weights[m * T + j];
-        const f32x4* p = reinterpret_cast<const f32x4*>(out + (size_t)(m * T + j) * K + n);
-        const f32x4 lo = p[0], hi = p[1];
+    // four entries at a time, added in order; what names no expert has no row in `out`, and is read as another
+    for (int j0 = 0; j0 < T; j0 += 4) {
+        f32x4 lo[4], hi[4];
+        float wt[4];
+        bool in[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = fmaf(wt, lo[e], v[e]);
-            v[4 + e] = fmaf(wt, hi[e], v[4 + e]);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t at = m * T + (j0 + j < T ? j0 + j : T - 1);
+            const int id = ids[at];
+            in[j] = j0 + j < T && id >= 0 && id < E;
+            wt[j] = weights[at];
+            const f32x4* p = reinterpret_cast<const f32x4*>(out + (size_t)at * K + n);
+            lo[j] = p[0];
+            hi[j] = p[1];
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (in[j]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = fmaf(wt[j], lo[j][e], v[e]);
+                    v[4 + e] = fmaf(wt[j], hi[j][e], v[4 + e]);
+                }
+            }
     }
     if (residual) {
         const uint4 r = *reinterpret_cast<const uint4*>(residual + m * K + n);
@@ -236,7 +250,7 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ out
 }
 
 template <bool kBF16, int MR, int kSub>
-void launch_pair(const MoeCall& q, MoeTileArgs& up, MoeTileArgs& down, hipStream_t s) {
+void launch_pair(const MoeTileArgs& up, const MoeTileArgs& down, hipStream_t s) {
     using Up = TileProduct<kBF16, MR, kProductColumns / 128, 8, kSub, true, RowsOfPairs>;
     using Down = TileProduct<true, 2 * MR, kProductColumns / 128, 8, kSub, false, HalvesOfPairs<16 * MR>, kBF16>;
     hipLaunchKernelGGL((up_kernel<Up>), dim3((unsigned)product_ids(up.p.tiles_m, up.p.tiles_n, 1)), dim3(Up::kThreads), 0, s, up);
@@ -244,16 +258,16 @@ void launch_pair(const MoeCall& q, MoeTileArgs& up, MoeTileArgs& down, hipStream
 }
 
 template <bool kBF16>
-void launch_typed(const MoeCall& q, int mr, int sub, MoeTileArgs& up, MoeTileArgs& down, hipStream_t s) {
+void launch_typed(int mr, int sub, const MoeTileArgs& up, const MoeTileArgs& down, hipStream_t s) {
     if (sub == 4) {
-        if (mr == 1) launch_pair<kBF16, 1, 4>(q, up, down, s);
-        else launch_pair<kBF16, 2, 4>(q, up, down, s);
+        if (mr == 1) launch_pair<kBF16, 1, 4>(up, down, s);
+        else launch_pair<kBF16, 2, 4>(up, down, s);
     } else if (sub == 2) {
-        if (mr == 1) launch_pair<kBF16, 1, 2>(q, up, down, s);
-        else launch_pair<kBF16, 2, 2>(q, up, down, s);
-    } else if (mr == 1) launch_pair<kBF16, 1, 1>(q, up, down, s);
-    else if (mr == 2) launch_pair<kBF16, 2, 1>(q, up, down, s);
-    else launch_pair<kBF16, 4, 1>(q, up, down, s);
+        if (mr == 1) launch_pair<kBF16, 1, 2>(up, down, s);
+        else launch_pair<kBF16, 2, 2>(up, down, s);
+    } else if (mr == 1) launch_pair<kBF16, 1, 1>(up, down, s);
+    else if (mr == 2) launch_pair<kBF16, 2, 1>(up, down, s);
+    else launch_pair<kBF16, 4, 1>(up, down, s);
 }
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -316,8 +330,8 @@ hipError_t launch_moe_tile(const MoeCall& q, uint8_t* scratch, hipStream_t strea
     down.stride = q.down_stride;
     down.out = reinterpret_cast<float*>(scratch + l.out);
     const int sub = units_per_block(q.G);
-    if (q.bf16) launch_typed<true>(q, l.mr, sub, up, down, stream);
-    else launch_typed<false>(q, l.mr, sub, up, down, stream);
+    if (q.bf16) launch_typed<true>(l.mr, sub, up, down, stream);
+    else launch_typed<false>(l.mr, sub, up, down, stream);
     const int64_t chunks = q.M * (q.K / 8);
     const dim3 grid((unsigned)((chunks + 255) / 256));
     if (q.bf16) hipLaunchKernelGGL((join_kernel<true>), grid, dim3(256), 0, stream, down.out, q.ids, q.weights, q.residual, q.y, chunks, (int)q.K, (int)q.E, (int)q.T);
