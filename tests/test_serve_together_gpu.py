@@ -206,3 +206,36 @@ def test_a_vocabulary_past_32_bits_of_bytes(w):
     for how in (dict(t=1.0), dict(k=9), dict(p=0.9)):
         ids, _ = w.w4a16_sample(z, u, temperature=how.get("t", 1.0), top_k=how.get("k", 0), top_p=how.get("p", 1.0))
         assert ids.tolist() == su.sample(z, u, **how)[0].tolist()
+
+
+def test_no_rows(w, model):
+    ex, _, router, _ = model
+    x = torch.empty((0, K), dtype=torch.bfloat16, device=DEV)
+    ids, weights = w.w4a16_route(x, router, T)
+    assert ids.shape == (0, T) and weights.shape == (0, T)
+    assert w.w4a16_moe(x, ids, weights, ex.gate_up, ex.down_packed, F, G).shape == (0, K)
+    assert w.w4a16_moe_layer(x, router, ex.gate_up, ex.down_packed, F, T, G)[0].shape == (0, K)
+    new, logprob = w.w4a16_sample(torch.empty((0, V), device=DEV), torch.empty((0,), device=DEV), top_p=0.9)
+    assert new.shape == (0,) and logprob.shape == (0,)
+
+
+def test_graphs_of_few_rows_side_by_side(w, model):
+    """Two captured draws replayed on two streams at once, each with the workspace of its own graph."""
+    z = torch.randn((2, 3, 40000), device=DEV)
+    u = torch.rand((2, 3), device=DEV)
+    want = [w.w4a16_sample(z[k], u[k], top_p=0.8) for k in range(2)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for k in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(w.w4a16_sample(z[k], u[k], top_p=0.8))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                graphs[k].replay()
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert torch.equal(outs[k][0], want[k][0]) and torch.equal(outs[k][1], want[k][1])
