@@ -42,6 +42,9 @@ constexpr int kShort = 256;                     // and of all in a short list
 constexpr int kGroups = 256;
 constexpr int kBins = 1024, kBinsPerOctave = 32;   // of weights, below the largest
 constexpr int kNone = 0x7FFFFFFF;
+// Of a launch of one workgroup a row: a grid's size is 32 bits of threads, and HIP launches what is
+// left of a larger one without an error (2^22 + 3 rows of 1024 threads: the first three).
+constexpr int kRowsPerLaunch = 1 << 20;
 
 // what the launches for few rows leave to each other
 struct Left {
@@ -1116,6 +1119,20 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     if (lane == (over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some))) answer(i, w, total);
 }
 
+// Rows m0 and on of a call.
+SampleArgs rows_from(SampleArgs a, int m0, int bytes) {
+    a.logits = static_cast<const uint8_t*>(a.logits) + (int64_t)m0 * a.ld * bytes;
+    a.M -= m0;
+    a.u += m0;
+    if (a.temperatures) a.temperatures += m0;
+    if (a.top_ks) a.top_ks += m0;
+    if (a.top_ps) a.top_ps += m0;
+    if (a.min_ps) a.min_ps += m0;
+    a.ids += m0;
+    if (a.logprob) a.logprob += m0;
+    return a;
+}
+
 template <int kKind>
 void launch_kind(const SampleArgs& a, hipStream_t s) {
     if (a.left) {
@@ -1127,7 +1144,10 @@ void launch_kind(const SampleArgs& a, hipStream_t s) {
             hipLaunchKernelGGL((piece_cut_kernel<kKind>), pieces, block, 0, s, a);
         hipLaunchKernelGGL((sample_kernel<kKind, true>), dim3((unsigned)a.M), dim3(kThreads), 0, s, a);
     } else {
-        hipLaunchKernelGGL((sample_kernel<kKind, false>), dim3((unsigned)a.M), dim3(kThreads), 0, s, a);
+        for (int64_t m0 = 0; m0 < a.M; m0 += kRowsPerLaunch) {
+            const SampleArgs b = rows_from(a, (int)m0, kKind == 2 ? 4 : 2);
+            hipLaunchKernelGGL((sample_kernel<kKind, false>), dim3((unsigned)(b.M < kRowsPerLaunch ? b.M : kRowsPerLaunch)), dim3(kThreads), 0, s, b);
+        }
     }
 }
 
