@@ -34,14 +34,16 @@ typedef enum {
 /* The router of a mixture of E experts: T of them for each row.
  *   l[m, e] = sum_k x[m, k] * router[e, k],  s = score(l)
  *   ids[m, :]      the T experts of the largest l (of the largest s + bias[e] where a bias is
- *                  given), the largest first, ties to the lowest expert
+ *                  given), the largest first, ties to the lowest expert; what is no number
+ *                  there comes last
  *   weights[m, j]  s of expert ids[m, j] (without the bias); with `normalize` over the sum of
  *                  the row's T (0 where that sum is 0); times `scale`
  *   x [M, K], router [E, K] row-major, `dtype`, 16-byte aligned. bias fp32 [E] or NULL.
  *   ids int32, weights fp32 [M, T], written in full.
  * K % 128 == 0, K <= 2^20, 1 <= T <= min(E, 32), E <= 1024. l is summed in fp64, so that the
- * choice is that of exact arithmetic up to rounding in the 53rd bit. A row in which some l is
- * no number still gets T different experts, with weights that are no numbers. An unknown
+ * choice is that of exact arithmetic up to rounding in the 53rd bit. A row in which some s is
+ * no number (that expert's l is none, or +infinity or all -infinity under softmax), chosen or
+ * not, still gets T different experts, with weights that are all no numbers. An unknown
  * score gives W4A16_ERR_PATH; scale must be finite. */
 size_t w4a16_route_workspace_bytes(int64_t M, int64_t K, int64_t E, int64_t T);
 w4a16_status w4a16_route(const void* x, const void* router, const float* bias, w4a16_dtype dtype, int64_t M, int64_t K,

@@ -824,7 +824,8 @@ def w4a16_route(x, router, top_k, bias=None, score="softmax", normalize=True, sc
     """Router of a mixture of experts. x [M, K], router [E, K] (fp16/bf16) -> (ids int32,
     weights float32) [M, top_k]: the experts of the largest x . router^T, ties to the lowest,
     and their scores ("softmax" over the experts, or each expert's "sigmoid"), with `normalize`
-    over their sum, times `scale`. bias float32 [E] enters the choice alone."""
+    over their sum, times `scale`. bias float32 [E] enters the choice alone. A row with a score
+    that is no number, chosen or not, has weights that are none."""
     M, K, E, code, ids, weights = _router_args(x, router, top_k, bias, score, ids, weights)
     _beside(x, router=router, bias=bias, ids=ids, weights=weights, workspace=workspace)
     _launch("w4a16_route",

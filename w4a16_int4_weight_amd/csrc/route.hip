@@ -74,11 +74,14 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int m) {
     top = wave_max(top);
     // scores; softmax's are divided by their sum at the end, unless it leaves with `normalize`
     double s[N], sum = 0.0;
+    bool none = false;                                    // some score is no number: no weight of the row is one
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         s[i] = a.sigmoid ? 1.0 / (1.0 + exp(-l[i])) : exp(l[i] - top);
         sum += lane + 64 * i < a.E ? s[i] : 0.0;
+        none = none || (lane + 64 * i < a.E && s[i] != s[i]);
     }
+    none = __ballot(none) != 0;
     sum = a.sigmoid ? 1.0 : wave_sum(sum);
     // what the choice goes by: -infinity for no number, no number for what is taken or not there
     double by[N];
@@ -114,7 +117,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int m) {
         }
     }
     if (lane < a.T) {
-        const double w = a.normalize ? (total == 0.0 ? 0.0 : mine / total) : mine / sum;
+        const double w = none ? NAN : a.normalize ? (total == 0.0 ? 0.0 : mine / total) : mine / sum;
         a.ids[(size_t)m * a.T + lane] = my_id;
         a.weights[(size_t)m * a.T + lane] = (float)(w * (double)a.scale);
     }
