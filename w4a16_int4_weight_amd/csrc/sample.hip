@@ -40,6 +40,7 @@ constexpr int kStep = 64 * kVec;                // of a wave
 constexpr int kRoom = 512;                      // listed logits of a piece
 constexpr int kShort = 256;                     // and of all in a short list
 constexpr int kGroups = 256;
+constexpr int kGroupK = kGroups * 3 / 4;        // top-k up to here goes by the groups' largest
 constexpr int kBins = 1024, kBinsPerOctave = 32;   // of weights, below the largest
 constexpr int kNone = 0x7FFFFFFF;
 // Of a launch of one workgroup a row: a grid's size is 32 bits of threads, and HIP launches what is
@@ -93,7 +94,7 @@ struct How {
         p = (double)fmaxf(pf, 0.f);
         const float mf = a.min_ps ? a.min_ps[m] : a.min_p;
         min_w = mf > 0.f ? (double)fminf(mf, 1.f) : 0.0;
-        by_groups = limit_k && k <= kGroups * 3 / 4;
+        by_groups = limit_k && k <= kGroupK;
         by_bins = limit_p && !limit_k;
     }
 };
@@ -1152,10 +1153,12 @@ void launch_kind(const SampleArgs& a, hipStream_t s) {
 }
 
 // Pieces where one workgroup a row would leave most of the chip idle and the row is long enough to be worth the
-// launches. Both ways, us, bf16 (pieces / a workgroup a row), without limits, top-k 50 with top-p 0.9, top-p 0.95:
-//   1 x 131072    18 / 36    18 / 24    37 / 108        64 x 131072   23 / 38    24 / 27    58 / 111
-//   128 x 131072  32 / 38    30 / 27    83 / 112        16 x 32768    18 / 15    19 / 19    34 / 44
-//   64 x 16384    18 / 13    21 / 18    38 / 32         192 x 131072  44 / 44    38 / 32    111 / 119
+// launches; one rule for all settings, which may differ from row to row. Both ways, us, bf16, calls of a graph (pieces /
+// a workgroup a row), without limits, top-k 50 with top-p 0.9, top-p 0.95:
+//   1 x 131072    16 / 36    18 / 24    36 / 108        64 x 131072   25 / 38    24 / 27    64 / 115
+//   128 x 131072  34 / 40    31 / 28    90 / 116        128 x 65536   25 / 24    27 / 22    68 / 72
+//   1 x 24600     13 / 14    16 / 16    28 / 34         64 x 24600    16 / 15    20 / 18    40 / 38
+//   16 x 32768    13 / 16    17 / 18    33 / 43         64 x 32768    16 / 16    20 / 18    42 / 44
 bool in_pieces(int64_t M, int64_t V) { return V > 24576 && (M <= 64 || (M <= 128 && V >= 65536)); }
 
 }  // namespace
@@ -1182,9 +1185,12 @@ hipError_t launch_sample(const SampleCall& q, void* scratch, hipStream_t stream)
     a.min_ps = q.min_ps;
     a.ids = q.ids;
     a.logprob = q.logprob;
-    // (the largest logit alone is found faster by one launch: 15 us against 18)
+    // One launch where the pieces' own leave it all the work: for the largest logit alone (15 us against 18), and
+    // for a top-k that the groups do not bound (1 and 64 rows of 131072, bf16, one launch / pieces: k = 200 38 / 43
+    // and 42 / 49, 1000 50 / 54 and 52 / 59, 5000 147 / 149 and 151 / 155).
     const bool greedy = !q.temperatures && !(q.temperature > 0.f);
-    a.left = in_pieces(q.M, q.V) && !greedy ? static_cast<Left*>(scratch) : nullptr;
+    const bool long_k = !q.top_ks && q.top_k > kGroupK && q.top_k < q.V;
+    a.left = in_pieces(q.M, q.V) && !greedy && !long_k ? static_cast<Left*>(scratch) : nullptr;
     if (q.kind == 0) launch_kind<0>(a, stream);
     else if (q.kind == 1) launch_kind<1>(a, stream);
     else launch_kind<2>(a, stream);
