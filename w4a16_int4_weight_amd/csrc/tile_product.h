@@ -110,8 +110,8 @@ __device__ __forceinline__ float quarter_max(float v) {
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
-// kScaleBF16: the type of the weight's scales, where it is not that of x. kStages_: see there.
-template <bool kBF16_, int MR_, int CBW_, int W_, int kSub_, bool kGated_, class Rows = RowsInOrder, bool kScaleBF16 = kBF16_, int kStages_ = 3>
+// kScaleBF16: the type of the weight's scales, where it is not that of x.
+template <bool kBF16_, int MR_, int CBW_, int W_, int kSub_, bool kGated_, class Rows = RowsInOrder, bool kScaleBF16 = kBF16_>
 struct TileProduct {
     static constexpr bool kBF16 = kBF16_, kGated = kGated_;
     static constexpr int MR = MR_, CBW = CBW_, W = W_, kSub = kSub_;
@@ -127,10 +127,8 @@ struct TileProduct {
     // Stages t and t + 1 are read in turn t, t + 2 is on its way. (Rings of 4 to 6 stages, where
     // they fit, measured the same for 64-row tiles and 15% slower for 16-row ones, which then
     // run one workgroup a compute unit instead of two.)
-    static constexpr int kStages = kStages_;
-    // a group's is read until its last block is done, and in the turn behind it
-    static constexpr int kMetaSlots = kStages > 4 ? 3 : 2;
-    static_assert(kStages >= 3 && kStages <= 8, "the metadata of a group comes at most one group before its slot is free");
+    static constexpr int kStages = 3;
+    static constexpr int kMetaSlots = 2;                   // a group's is read until its last block is done
     struct Stage {
         uint4 x[BM * 16];                 // chunk j of row r at chunk j ^ (r % 16)
         uint4 w[W * CBW * 64];
