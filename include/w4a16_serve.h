@@ -66,8 +66,11 @@ w4a16_status w4a16_route(const void* x, const void* router, const float* bias, w
  * F % 128 == 0 (a row block of the down projection), K and F <= 2^15, E <= 1024. g, u and the activation stay in fp32, h between
  * the projections in two bf16 values (16 bits), the sum over experts in fp32. Only the
  * experts that some row names are read. A row of x that is not finite gives a row of y that is
- * not, and touches no other. Made for few rows: up to 16, with M T <= 256 and K <= 4096, take two
- * launches, more take four and are met 16384 / T rows at a time. */
+ * not (where it names an expert), and touches no other. Made for few rows: up to 16, with M T <= 256 and K <= 4096, take two
+ * launches, more take four and are met 16384 / T rows at a time. The workspace holds 4 (F + K) bytes for
+ * each of at most 16384 entries of ids (1.2 GB where K = 4096 and F = 14336 and the rows fill a pass, 4.3 GB
+ * at the widest), or, where two launches serve, 4 M F for each expert that may be named (at most
+ * min(E, M T)). */
 size_t w4a16_moe_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t T, int64_t group_size);
 w4a16_status w4a16_moe(const void* x, const int32_t* ids, const float* weights, const void* gate_up,
                        size_t gate_up_bytes, size_t gate_up_stride, const void* down, size_t down_bytes,
@@ -98,7 +101,7 @@ typedef struct {
     float temperature;          /* t; not above 0: the largest logit (the lowest v of it), whatever
                                    the rest says, with logprob 0 */
     int32_t top_k;              /* below 1, or V and above: all                             */
-    float top_p;                /* 1 and above: all; not above 0: the first                 */
+    float top_p;                /* 1 and above or no number: all; not above 0: the first    */
     float min_p;                /* not above 0: all; above 1: as 1                          */
     const float* temperatures;
     const int32_t* top_ks;

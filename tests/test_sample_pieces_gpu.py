@@ -122,3 +122,14 @@ def test_few_tokens_that_can_be_drawn(w, k):
     u = torch.tensor([0.0, 1.0 - 2.0 ** -24, 0.3, 0.6, 0.9, 0.1], device=DEV)
     check(w, z, u, k=k)
     check(w, z, u, k=k, p=0.8)
+
+
+@pytest.mark.parametrize("M,V", [(6, 40000), (6, 5000)])
+def test_settings_of_no_number(w, M, V):
+    """A temperature that is no number draws the largest; a top_p or min_p that is none limits nothing."""
+    z, u = make(V, M, V, "bf16")
+    none = math.nan
+    for s in (dict(t=none), dict(p=none), dict(min_p=none), dict(k=40, p=none), dict(p=0.8, min_p=none),
+              dict(t=each_row([none, 0.7], M, torch.float32), p=each_row([0.9, none, 1.0], M, torch.float32), min_p=each_row([none, 0.1], M, torch.float32))):
+        ids, _ = w.w4a16_sample(z, u, temperature=s.get("t", 1.0), top_k=s.get("k", 0), top_p=s.get("p", 1.0), min_p=s.get("min_p", 0.0))
+        assert np.array_equal(ids.cpu().numpy(), su.sample(z, u, **s)[0])

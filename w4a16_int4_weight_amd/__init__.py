@@ -857,7 +857,9 @@ def w4a16_moe(x, ids, weights, gate_up, down, F, group_size=128, act="silu", res
     """Experts' gated feed-forward blocks on packed int4 weights: x [M, K] (fp16/bf16), ids
     int32 and weights float32 [M, T] (an id outside [0, E): none) -> y [M, K] = residual +
     sum_j weights[:, j] * (act(x Wg) * (x Wu)) Wd over the experts ids[:, j]. gate_up and down:
-    uint8 [E, bytes], row e expert e's packed [K, 2F] and [F, K] weight."""
+    uint8 [E, bytes], row e expert e's packed [K, 2F] and [F, K] weight. Long prompts of wide layers
+    need a large workspace (w4a16_moe_workspace_bytes: 4 (F + K) bytes for each of up to 16384 entries of
+    ids), which the stream keeps unless one is given."""
     M, K = _rows(x, "x")
     E, experts, y = _experts_args(x, gate_up, down, F, group_size, residual, y)
     Mi, T = _rows(ids, "ids")

@@ -23,9 +23,11 @@
 // Per metadata unit: s (T - (16 + z) X), T = sum x (16 + q), as product_small.hip has it; fp16
 // activations take q - z exactly in 16 bits.
 //
-// Measured (2048 x 1024, 64 experts, 8 a row): one row 10.0 + 8.4 us, of which a launch takes 1.5,
+// Measured (2048 x 1024, 64 experts, 8 a row): one row 11.0 + 8.7 us, of which a launch takes 1.5,
 // the ids and their list 2, the first codes 2 to 3 (16.8 and 8.4 MB), and the splits' meeting 2.3;
-// 16 rows 31 us for 132 MB (4.2 TB/s; with the loads alone 31 too) and 24 us for 66 MB. A barrier a batch
+// 16 rows 32 us for 132 MB (4.1 TB/s; with the loads alone 31) and 24 us for 66 MB (decoding takes the vector units
+// 46% of its cycles, both halves of h the matrix cores 18%, and the two waves of a SIMD wait 42% of
+// theirs). A barrier a batch
 // of units, as product_small.hip has it, took 39 us for up_kernel at 16 rows; two workgroups a compute unit
 // 48 (up) and 30 us (down); 8 columns a down workgroup and no splits 50 us.
 #include "device_common.h"

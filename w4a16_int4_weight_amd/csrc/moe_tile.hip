@@ -12,8 +12,8 @@
 // row's sum over its pairs in their order. No atomics on results: they do not depend on timing.
 // The products are tile_product.h's.
 //
-// Measured (2048 x 1024, 64 experts, 8 a row): 77 rows 5 + 56 + 51 + 5 us (143 and 67 MB of codes: 2.5 and 1.3
-// TB/s; 75 tiles of 8 column tiles are a round and a bit of two workgroups a compute unit), 512 rows 6 + 115 + 99
+// Measured (2048 x 1024, 64 experts, 8 a row): 77 rows 5 + 57 + 52 + 5 us (143 and 67 MB of codes: 2.5 and 1.3
+// TB/s; 75 tiles of 8 column tiles are a round and a bit of two workgroups a compute unit), 512 rows 6 + 115 + 98
 // + 7 us (64-row tiles, half the experts with a second one; 300 and, each half by itself, 350 TFLOP/s). A ring of 4
 // stages: the same at 64 rows, 74 instead of 56 us at 16. Tiles of 32 rows for 512: 138 and 99 us,
 // of 128 for the first product 127; tiles that begin at different row blocks: the same.

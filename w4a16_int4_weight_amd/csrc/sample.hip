@@ -15,8 +15,8 @@
 //   4. the draw: the piece whose sum of kept w holds the target, its sixteenth, and so on.
 // A few rows take 16 workgroups each, in a launch for each of these; many rows one workgroup each,
 // a wave a piece, in one launch. Bound by latency (a few rows: three or four launches of 3 to 10 us whose
-// steps wait for each other) and by the vector units (many rows: 256 x 131072 in 45 us, 1.5 TB/s, 25 fp64
-// instructions a logit). What the lists do not hold (top-k over 1024, lists of more than 512
+// steps wait for each other) and by the vector units (many rows: 256 x 131072 in 45 to 50 us, 1.4 TB/s: 36 vector
+// instructions a logit, 25 of them in fp64, fill 73% of the cycles). What the lists do not hold (top-k over 1024, lists of more than 512
 // in a piece) is found over the row itself.
 //
 // Logits are compared as whole numbers (order-preserving keys). Lists of up to 256 are sorted by
